@@ -418,6 +418,194 @@ MONARCH_API const char *monarch_status_string(monarch_status status);
 MONARCH_API int monarch_attn_path(int B, int H, int f, int h, int w, int d, int b1, int b2, int tiles,
                       int iters, monarch_dtype dtype);
 
+/* ------------------------------------------------------------------------
+ * Exact attention over a window, for the layers and rollouts that do not use
+ * the Monarch factors.  (No counterpart in the MonarchRT pages; the pages'
+ * setting, autoregressive video with a cache of earlier frames, is theirs.)
+ *
+ *   out_i = sum_j P_ij v_j,  P_ij = exp(scale q_i.k_j - lse_i),
+ *   lse_i = log sum_j exp(scale q_i.k_j)   over the keys j that query i sees.
+ *
+ * Sequence b holds lengths[b] keys (clamped to [0, Nk]).  Query i sits at
+ * position p = start_b + i.  It is a real row when 0 <= p < lengths[b]; any other
+ * row gives zeros, lse = -infinity and no gradients.  In frames of `frame` tokens,
+ * fq = p / frame and fk = j / frame, a real row sees key j < lengths[b] when
+ *   fk <= fq + right                       (right = -1: no limit)   and
+ *   fk >= fq - left  or  fk < sinks        (left = -1: no limit).
+ * So (left, right) = (-1, 0) with frame = 1 is causal attention, (w - 1, 0) a
+ * sliding window of w tokens, frame = h*w a window of whole video frames in which
+ * every frame sees itself, and `sinks` keeps the first frames visible.
+ *
+ * H query heads share Hkv key heads, H a multiple of Hkv: query head h reads key
+ * head h / (H / Hkv).  All tensors have stride 1 along d; their other strides are
+ * free, in elements and positive, each a multiple of 16 bytes; pointers are 16-byte
+ * aligned.  Outputs must not overlap inputs or each other.
+ *
+ * Keys and values at or past lengths[b] are never used, whatever they hold, and
+ * neither are queries and dout of rows that are not real.  Keys and values below
+ * lengths[b] should be finite: a NaN or an infinity there can reach every query that
+ * shares a tile with one that sees it.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int64_t batch, head, token;   /* elements between batches, heads and tokens */
+} monarch_strides;
+
+/* start: the position of every sequence's first query, or MONARCH_NEWEST: the queries
+ * are the newest tokens, start_b = lengths[b] - Nq. */
+#define MONARCH_NEWEST INT32_MIN
+
+typedef struct {
+    int32_t B, H, Hkv, Nq, Nk, d;      /* all >= 1; d = 32, 64 or 128; B*H <= 65535 */
+    int32_t frame, left, right, sinks; /* frame >= 1; left, right >= -1; sinks >= 0 */
+    int32_t start;                     /* used when starts is NULL */
+    monarch_dtype dtype;
+    float scale;                       /* finite and > 0; usually 1/sqrt(d) */
+    const int32_t *lengths;            /* device, [B]; NULL: Nk keys each */
+    const int32_t *starts;             /* device, [B]; NULL: start */
+    monarch_strides q, k, v, out;      /* of [B][H][Nq][d], [B][Hkv][Nk][d] (k, v), like q */
+} monarch_window_desc;
+
+/*
+ * Workspace bytes of monarch_window_attn_fwd_ws, or 0 if the arguments fail
+ * validation (256 where none is needed).  Pure host function.
+ * Source: no counterpart in the pages (a property of this implementation).
+ */
+MONARCH_API size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc);
+
+/*
+ * Which kernels a forward call runs: 0 = float32 FMA kernels, 1 = sm_100a tensor-core
+ * kernels (bfloat16), 2 = the kernels for few query rows (Nq * H / Hkv at most 64),
+ * which split the keys over CTAs; -1 = the arguments fail validation.
+ * Source: no counterpart in the pages (dispatch of this library).
+ */
+MONARCH_API int monarch_window_attn_path(const monarch_window_desc *desc);
+
+/*
+ * Forward pass.
+ *   q, k, v     device pointers, read only.     out  device pointer, fully overwritten.
+ *   lse         device pointer, float32 [B][H][Nq] contiguous, or NULL.
+ *   workspace   device memory, 256-byte aligned, at least the bytes above
+ *               (MONARCH_ERR_NO_MEMORY if ws_bytes is smaller); contents need no
+ *               initialisation.  Calls that share it must not overlap on the GPU.
+ * Softmax and sums are float32; the tensor-core kernels round the probabilities to
+ * bfloat16 as operands of the second product.  Deterministic.
+ * Source: no counterpart in the pages (see above).
+ */
+MONARCH_API monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc *desc,
+                                                      const void *q, const void *k,
+                                                      const void *v, void *out, float *lse,
+                                                      void *workspace, size_t ws_bytes,
+                                                      monarch_stream_t stream);
+
+/*
+ * Backward pass: with out and lse of the forward call and dout = dPhi/dout,
+ *   delta_i = dout_i.out_i,  dS_ij = P_ij (dout_i.v_j - delta_i),
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i,
+ * dk and dv summed over the query heads that share a key head.  `grads` holds the
+ * strides of dout and of the three gradients (same rules as desc's).  dq, dk and dv are
+ * fully overwritten: zeros in rows that are not real and keys past lengths[b].
+ * Deterministic: no atomics.
+ * Source: no counterpart in the pages (the derivative of the forward map).
+ */
+typedef struct {
+    monarch_strides dout, dq, dk, dv;
+} monarch_window_grads;
+
+MONARCH_API size_t monarch_window_attn_bwd_workspace_bytes(const monarch_window_desc *desc);
+MONARCH_API monarch_status monarch_window_attn_bwd_ws(
+    const monarch_window_desc *desc, const monarch_window_grads *grads, const void *q,
+    const void *k, const void *v, const void *out, const float *lse, const void *dout, void *dq,
+    void *dk, void *dv, void *workspace, size_t ws_bytes, monarch_stream_t stream);
+
+/*
+ * The forward pass of one new token a sequence over a paged cache.  desc as above
+ * with Nq = 1; Nk is the page table's width times the page size, k and v point to
+ * the pools of pages, and desc->k.batch and desc->v.batch are the elements between pages
+ * (head and token: inside a page).  lengths is required; the query is the newest
+ * token (start and starts are not used).
+ *   page_table    device, int32, row b at page_table + b*table_stride: key j of
+ *                 sequence b is row j % page_size of page page_table[b][j / page_size].
+ *   page_size     a power of two from 8 to 65536.     num_pages  pages in each pool.
+ * Only entries of pages that hold a visible key are read; the others may be
+ * anything (-1 for pages that a window has given back).  An entry that is read and
+ * lies outside [0, num_pages) is reported as MONARCH_ERR_INVALID_ARG by
+ * monarch_last_device_status, and its keys count as absent.
+ * Source: no counterpart in the pages (see above).
+ */
+MONARCH_API size_t monarch_paged_attn_workspace_bytes(const monarch_window_desc *desc);
+MONARCH_API monarch_status monarch_paged_attn_ws(const monarch_window_desc *desc, const void *q,
+                                                 const void *k_pages, const void *v_pages,
+                                                 const int32_t *page_table, int64_t table_stride,
+                                                 int32_t page_size, int32_t num_pages, void *out,
+                                                 float *lse, void *workspace, size_t ws_bytes,
+                                                 monarch_stream_t stream);
+
+/*
+ * Rotary positions of queries and keys: each pair (a, b) of the first 2*pairs
+ * elements of a head becomes
+ *   magnitude (a cos t - b sin t, a sin t + b cos t),  t = position * freqs[pair],
+ * the other elements are copied.  Pairs are (2i, 2i + 1), or (i, i + pairs) with
+ * half = 1.  With several axes the pairs split into runs of pairs_of_axis[0..axes-1],
+ * each turning with its own position.  inverse = 1 turns by -t: the backward pass,
+ * on the gradients of the outputs.
+ * Positions of token n of sequence b: positions[b*pos_batch + n*pos_token + axis]
+ * (device, int32), or, when that is NULL, with first = starts ? starts[b] : start,
+ *   axes = 1: first + n;     axes = 3, tokens on a grid of grid_h x grid_w a frame:
+ *   (first + n / (grid_h*grid_w), n / grid_w % grid_h, n % grid_w).
+ * Angles are formed exactly modulo one turn, so far positions lose no accuracy.
+ *   freqs   device, float64 [pairs], radians per position, finite.
+ *   k, k_out  may be NULL with Hkv = 0.  Outputs may be the inputs (in place) or must
+ *   not overlap them.  d is a multiple of 16 bytes of elements, at most 1024.
+ * Source: no counterpart in the pages (the positions of the video models whose
+ * attention they replace).
+ */
+typedef struct {
+    int32_t B, N, H, Hkv, d;
+    int32_t pairs, axes, pairs_of_axis[3];
+    int32_t half, inverse;
+    int32_t grid_h, grid_w;            /* axes = 3 without positions; else 0 */
+    int32_t start;
+    monarch_dtype dtype;
+    float magnitude;                   /* finite; 1 unless a long-context scaling sets it */
+    const int32_t *starts, *positions;
+    int64_t pos_batch, pos_token;
+    monarch_strides q, k, q_out, k_out;
+} monarch_rotary_desc;
+
+MONARCH_API monarch_status monarch_rotary(const monarch_rotary_desc *desc, const void *q,
+                                          const void *k, const double *freqs, void *q_out,
+                                          void *k_out, monarch_stream_t stream);
+
+/*
+ * Frequencies of one axis of `pairs` pairs, in radians per position (host, float64
+ * freqs[pairs]): base^(-i/pairs), scaled for contexts beyond the trained length:
+ *   MONARCH_ROTARY_PLAIN   unscaled;
+ *   MONARCH_ROTARY_LINEAR  positions interpolated: divided by factor;
+ *   MONARCH_ROTARY_NTK     base raised to base * factor^(pairs/(pairs - 1)): the
+ *                          lowest frequency is divided by factor, the highest kept;
+ *   MONARCH_ROTARY_YARN    divided by factor where a pair turns less than beta_slow
+ *                          times in `original` positions, kept where it turns more than
+ *                          beta_fast times, a linear blend over the pair index between
+ *                          the two; *magnitude = 0.1 ln(factor) + 1.
+ * magnitude may be NULL; it is 1 except for YARN.  Returns MONARCH_ERR_INVALID_ARG for
+ * pairs < 1, base <= 1, factor < 1, an unknown scaling or (YARN) original <= 0 or
+ * beta_fast <= beta_slow or beta_slow <= 0.
+ * Source: no counterpart in the pages; the scalings are the published ones
+ * (position interpolation, NTK-aware base, YaRN's by-parts blend and temperature).
+ */
+typedef enum {
+    MONARCH_ROTARY_PLAIN = 0,
+    MONARCH_ROTARY_LINEAR = 1,
+    MONARCH_ROTARY_NTK = 2,
+    MONARCH_ROTARY_YARN = 3
+} monarch_rotary_scaling;
+
+MONARCH_API monarch_status monarch_rotary_frequencies(int pairs, double base,
+                                                      monarch_rotary_scaling scaling,
+                                                      double factor, double original,
+                                                      double beta_fast, double beta_slow,
+                                                      double *freqs, double *magnitude);
+
 #ifdef __cplusplus
 }
 #endif

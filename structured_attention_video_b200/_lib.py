@@ -26,8 +26,44 @@ STATUS = {0: "MONARCH_OK", 1: "MONARCH_ERR_INVALID_ARG", 2: "MONARCH_ERR_SHAPE",
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _vp, _i, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+_i32, _i64, _dbl = ctypes.c_int32, ctypes.c_int64, ctypes.c_double
 _ip = ctypes.POINTER(ctypes.c_int32)
+_dp = ctypes.POINTER(ctypes.c_double)
 _SHAPE = [_i] * 10          # B, H, f, h, w, d, b1, b2, tiles, iters
+
+
+
+class Strides(ctypes.Structure):
+    """monarch_strides: elements between batches, heads and tokens."""
+    _fields_ = [("batch", _i64), ("head", _i64), ("token", _i64)]
+
+
+class WindowDesc(ctypes.Structure):
+    """monarch_window_desc."""
+    _fields_ = ([(n, _i32) for n in ("B", "H", "Hkv", "Nq", "Nk", "d", "frame", "left", "right",
+                                     "sinks", "start")] +
+                [("dtype", _i), ("scale", ctypes.c_float), ("lengths", _vp), ("starts", _vp)] +
+                [(n, Strides) for n in ("q", "k", "v", "out")])
+
+
+class WindowGrads(ctypes.Structure):
+    """monarch_window_grads."""
+    _fields_ = [(n, Strides) for n in ("dout", "dq", "dk", "dv")]
+
+
+class RotaryDesc(ctypes.Structure):
+    """monarch_rotary_desc."""
+    _fields_ = ([(n, _i32) for n in ("B", "N", "H", "Hkv", "d", "pairs", "axes")] +
+                [("pairs_of_axis", _i32 * 3)] +
+                [(n, _i32) for n in ("half", "inverse", "grid_h", "grid_w", "start")] +
+                [("dtype", _i), ("magnitude", ctypes.c_float), ("starts", _vp),
+                 ("positions", _vp), ("pos_batch", _i64), ("pos_token", _i64)] +
+                [(n, Strides) for n in ("q", "k", "q_out", "k_out")])
+
+
+_wd, _wg, _rd = (ctypes.POINTER(t) for t in (WindowDesc, WindowGrads, RotaryDesc))
+NEWEST = -2 ** 31   # MONARCH_NEWEST
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_YARN = 0, 1, 2, 3   # monarch_rotary_scaling
 
 SIGNATURES = {
     "monarch_attn_fwd": ([_vp, _vp, _vp, _vp] + _SHAPE + [_i, _vp], _i),
@@ -47,6 +83,16 @@ SIGNATURES = {
     "monarch_attn_bwd_workspace_bytes": (_SHAPE + [_i], _sz),
     "monarch_attn_bwd_ws": ([_vp] * 7 + _SHAPE + [_i, _vp, _sz, _vp], _i),
     "monarch_attn_bwd": ([_vp] * 7 + _SHAPE + [_i, _vp], _i),
+    "monarch_window_attn_workspace_bytes": ([_wd], _sz),
+    "monarch_window_attn_path": ([_wd], _i),
+    "monarch_window_attn_fwd_ws": ([_wd] + [_vp] * 6 + [_sz, _vp], _i),
+    "monarch_window_attn_bwd_workspace_bytes": ([_wd], _sz),
+    "monarch_window_attn_bwd_ws": ([_wd, _wg] + [_vp] * 10 + [_sz, _vp], _i),
+    "monarch_paged_attn_workspace_bytes": ([_wd], _sz),
+    "monarch_paged_attn_ws": ([_wd] + [_vp] * 4 + [_i64, _i32, _i32] + [_vp] * 3 + [_sz, _vp],
+                              _i),
+    "monarch_rotary": ([_rd] + [_vp] * 6, _i),
+    "monarch_rotary_frequencies": ([_i, _dbl, _i, _dbl, _dbl, _dbl, _dbl, _dp, _dp], _i),
     "monarch_index_maps": ([_i] * 6 + [_ip, _ip, _ip, _ip], _i),
     "monarch_index_maps_device": ([_i] * 6 + [_vp, _vp, _vp, _vp, _vp], _i),
     "monarch_last_device_status": ([_vp], _i),
@@ -167,6 +213,52 @@ def monarch_attn_bwd(q, k, v, dy, dq, dk, dv, B, H, f, h, w, d, b1, b2, tiles, i
                      stream):
     return _lib.monarch_attn_bwd(q, k, v, dy, dq, dk, dv, B, H, f, h, w, d, b1, b2, tiles, iters,
                                  dtype, stream)
+
+
+# The structs are passed by reference; ctypes converts a Structure instance itself.
+def monarch_window_attn_workspace_bytes(desc):
+    return _lib.monarch_window_attn_workspace_bytes(desc)
+
+
+def monarch_window_attn_path(desc):
+    return _lib.monarch_window_attn_path(desc)
+
+
+def monarch_window_attn_fwd_ws(desc, q, k, v, out, lse, workspace, ws_bytes, stream):
+    return _lib.monarch_window_attn_fwd_ws(desc, q, k, v, out, lse, workspace, ws_bytes, stream)
+
+
+def monarch_window_attn_bwd_workspace_bytes(desc):
+    return _lib.monarch_window_attn_bwd_workspace_bytes(desc)
+
+
+def monarch_window_attn_bwd_ws(desc, grads, q, k, v, out, lse, dout, dq, dk, dv, workspace,
+                               ws_bytes, stream):
+    return _lib.monarch_window_attn_bwd_ws(desc, grads, q, k, v, out, lse, dout, dq, dk, dv,
+                                           workspace, ws_bytes, stream)
+
+
+def monarch_paged_attn_workspace_bytes(desc):
+    return _lib.monarch_paged_attn_workspace_bytes(desc)
+
+
+def monarch_paged_attn_ws(desc, q, k_pages, v_pages, page_table, table_stride, page_size,
+                          num_pages, out, lse, workspace, ws_bytes, stream):
+    return _lib.monarch_paged_attn_ws(desc, q, k_pages, v_pages, page_table, table_stride,
+                                      page_size, num_pages, out, lse, workspace, ws_bytes, stream)
+
+
+def monarch_rotary(desc, q, k, freqs, q_out, k_out, stream):
+    return _lib.monarch_rotary(desc, q, k, freqs, q_out, k_out, stream)
+
+
+def monarch_rotary_frequencies(pairs, base, scaling, factor, original, beta_fast, beta_slow):
+    """(status, [pairs] frequencies in radians per position, magnitude)."""
+    freqs = (_dbl * max(pairs, 1))()
+    magnitude = _dbl()
+    status = _lib.monarch_rotary_frequencies(pairs, base, scaling, factor, original, beta_fast,
+                                             beta_slow, freqs, ctypes.byref(magnitude))
+    return status, list(freqs), magnitude.value
 
 
 def monarch_index_maps(f, h, w, b1, b2, tiles, u_of_n, v_of_n, perm, tile_begin):

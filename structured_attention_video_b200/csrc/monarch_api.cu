@@ -64,6 +64,10 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
+int *device_status_word() { return status_word_on_current_device(); }
+long long device_wait_limit() { return g_wait_limit.load(); }
+int device_inject_stall() { return g_inject_stall.load(); }
+
 bool current_context_id(unsigned long long *id) {
     static CtxGetCurrentFn get_current = nullptr;
     static CtxGetIdFn get_id = nullptr;

@@ -188,6 +188,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(x);
 }
 
+// For entry points in other translation units: the status word of the current
+// context (null if it cannot be found), the poll limit of the bounded waits and the
+// fault-injection switch (monarch_set_wait_limit, monarch_debug_inject_stall).
+int *device_status_word();
+long long device_wait_limit();
+int device_inject_stall();
+
 // Host-side argument validation shared by the entry points; fills *p on success.
 monarch_status validate_shape(int B, int H, int f, int h, int w, int d, int b1, int b2, int tiles,
                               int iters, monarch_dtype dtype, Problem *p);

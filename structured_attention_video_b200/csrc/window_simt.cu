@@ -1,0 +1,471 @@
+// window_simt.cu -- window attention in 32-bit arithmetic on the FMA pipes, forward
+// and backward (float32 inputs; the tensor cores round operands to fewer bits), and
+// the row sums delta = dO.O of both types' backward.
+//
+// One CTA of 256 threads takes 64 rows of one side (queries; keys for dk and dv)
+// and walks tiles of the other side.  Thread (ty, tx) of a 16 x 16 grid owns rows
+// 4 ty .. 4 ty + 3: in the logit products columns tx, tx + 16, ..., in the
+// accumulating products d/16 columns of the head dimension.  The products run on
+// packed pairs of float32 (fma.rn.f32x2).  The 16 threads of a row are half a warp,
+// so softmax rows reduce with shuffles and the probabilities pass from the first
+// product to the second through shared memory without a CTA barrier.
+// No atomics: each output element is summed by one thread in a fixed order.
+#include "tc_primitives.cuh"
+#include "window_common.cuh"
+
+namespace monarch {
+namespace win {
+namespace {
+
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_mul;
+using tc::f2_pack;
+using tc::f2_unpack;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRows = 64;
+
+// Shared-memory row of D floats, padded so that 16-byte reads of 8 consecutive rows
+// cover all banks.
+template <int D> constexpr int kPitch = D + 4;
+
+__device__ __forceinline__ float4 load4(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store2(float *p, float a, float b) {
+    *reinterpret_cast<float2 *>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
+    *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16(a, b);
+}
+
+// Rows [r0, r0 + R) of a [tokens][D] matrix into shared memory; rows outside
+// [0, valid) become zero.
+template <int D, int R, typename T>
+__device__ __forceinline__ void load_rows(float *sm, const T *base, int64_t stride, int r0,
+                                          int valid) {
+    constexpr int kChunks = D / 4;
+    for (int i = threadIdx.x; i < R * kChunks; i += 256) {
+        const int r = i / kChunks, c = i % kChunks;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r0 + r < valid)
+            x = load4(base + (int64_t)(r0 + r) * stride + c * 4);
+        *reinterpret_cast<float4 *>(sm + r * kPitch<D> + c * 4) = x;
+    }
+}
+
+// s[i][j] = row (4 ty + i) of a . row (tx + 16 j) of b.
+template <int D, int NC>
+__device__ __forceinline__ void dot_tile(const float *a, const float *b, int ty, int tx,
+                                         float (&s)[4][NC]) {
+    uint64_t acc[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < NC; j++) acc[i][j] = 0;
+    const float *ap = a + 4 * ty * kPitch<D>, *bp = b + tx * kPitch<D>;
+#pragma unroll 4
+    for (int x = 0; x < D; x += 4) {
+        ulonglong2 av[4], bv[NC];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            av[i] = *reinterpret_cast<const ulonglong2 *>(ap + i * kPitch<D> + x);
+#pragma unroll
+        for (int j = 0; j < NC; j++)
+            bv[j] = *reinterpret_cast<const ulonglong2 *>(bp + j * 16 * kPitch<D> + x);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < NC; j++) {
+                acc[i][j] = f2_fma(av[i].x, bv[j].x, acc[i][j]);
+                acc[i][j] = f2_fma(av[i].y, bv[j].y, acc[i][j]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            float lo, hi;
+            f2_unpack(acc[i][j], lo, hi);
+            s[i][j] = lo + hi;
+        }
+}
+
+// Columns of the head dimension that thread tx owns: pair q of D/32 covers
+// columns 2 tx + 32 q and the next.
+// o[i][q] += sum over the C columns of w of w[4 ty + i][c] * b[c][columns].
+template <int D, int C, int PW>
+__device__ __forceinline__ void add_product(const float *w, const float *b, int ty, int tx,
+                                            uint64_t (&o)[4][D / 32]) {
+    const float *wp = w + 4 * ty * PW, *bp = b + 2 * tx;
+#pragma unroll 2
+    for (int c = 0; c < C; c += 4) {
+        float4 wv[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) wv[i] = *reinterpret_cast<const float4 *>(wp + i * PW + c);
+#pragma unroll
+        for (int cc = 0; cc < 4; cc++) {
+            uint64_t bv[D / 32];
+#pragma unroll
+            for (int q = 0; q < D / 32; q++)
+                bv[q] = *reinterpret_cast<const uint64_t *>(bp + (c + cc) * kPitch<D> + 32 * q);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float x = cc == 0 ? wv[i].x : cc == 1 ? wv[i].y : cc == 2 ? wv[i].z : wv[i].w;
+                const uint64_t xx = f2_pack(x, x);
+#pragma unroll
+                for (int q = 0; q < D / 32; q++) o[i][q] = f2_fma(xx, bv[q], o[i][q]);
+            }
+        }
+    }
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void store_rows(T *base, int64_t stride, int r0, int valid, int ty,
+                                           int tx, const uint64_t (&o)[4][D / 32],
+                                           const float (&scale)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = r0 + 4 * ty + i;
+        if (r >= valid) continue;
+#pragma unroll
+        for (int q = 0; q < D / 32; q++) {
+            float lo, hi;
+            f2_unpack(o[i][q], lo, hi);
+            store2(base + (int64_t)r * stride + 2 * tx + 32 * q, lo * scale[i], hi * scale[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ float half_warp_max(float x) {
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+__device__ __forceinline__ float half_warp_sum(float x) {
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
+// ---------------------------------------------------------------- forward
+// 64 queries of one head against tiles of 64 keys.  K and V take turns in one
+// buffer, so that two CTAs fit on an SM at d = 128 and one computes while the
+// other loads.
+template <int D>
+constexpr int fwd_smem() {
+    return (2 * kRows * kPitch<D> + kRows * 68) * 4;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 2)
+simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, float *out,
+                float *lse) {
+    extern __shared__ __align__(16) float smf[];
+    float *sq = smf, *skv = smf + kRows * kPitch<D>, *sp = skv + kRows * kPitch<D>;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
+    const int i0 = blockIdx.x * kRows;
+    const Sequence seq = sequence(p, b);
+    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + kRows);
+    const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
+    const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
+    load_rows<D, kRows>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    RowKeys rk[4];
+    float m[4], l[4];
+    uint64_t o[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        rk[i] = row_keys(p, seq, i0 + 4 * ty + i);
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 32; x++) o[i][x] = 0;
+    }
+    for (int it = 0; it < kt.count(); it++) {
+        const int j0 = kt.tile(it) * 64;
+        __syncthreads();   // the buffer's last readers are done
+        load_rows<D, 64>(skv, kb, p.k.token, j0, seq.len);
+        __syncthreads();
+        float s[4][4];
+        dot_tile<D, 4>(sq, skv, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                // a key outside the row's window never enters, whatever its value
+                s[i][j] = rk[i].sees(j0 + tx + 16 * j) ? s[i][j] * p.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            mx = fmaxf(m[i], half_warp_max(mx));
+            const float safe = mx == -INFINITY ? 0.f : mx;   // a row without keys so far
+            const float alpha = exp2f(m[i] - safe);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float e = exp2f(s[i][j] - safe);
+                sum += e;
+                sp[(4 * ty + i) * 68 + tx + 16 * j] = e;
+            }
+            l[i] = l[i] * alpha + sum;   // this thread's columns; joined at the end
+            m[i] = mx;
+            const uint64_t aa = f2_pack(alpha, alpha);
+#pragma unroll
+            for (int x = 0; x < D / 32; x++) o[i][x] = f2_mul(o[i][x], aa);
+        }
+        __syncthreads();   // K is read
+        load_rows<D, 64>(skv, vb, p.v.token, j0, seq.len);
+        __syncthreads();
+        add_product<D, 64, 68>(sp, skv, ty, tx, o);
+    }
+    float inv[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float total = half_warp_sum(l[i]);
+        inv[i] = total > 0.f ? 1.f / total : 0.f;
+        if (total != total) inv[i] = total;   // NaN inputs stay visible
+        const int r = i0 + 4 * ty + i;
+        if (lse && tx == 0 && r < p.Nq)
+            lse[((int64_t)b * p.H + h) * p.Nq + r] =
+                total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
+    }
+    store_rows<D>(out + b * p.o.batch + h * p.o.head, p.o.token, i0, p.Nq, ty, tx, o, inv);
+}
+
+// ---------------------------------------------------------------- backward
+// dq: 64 queries against tiles of 32 keys.  dS = P (dO.V - delta) with
+// P = exp(S - lse); dq = scale * dS K.
+template <int D>
+constexpr int dq_smem() {
+    return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256, 2)
+simt_dq_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
+               const float *lse, const float *delta, const T *dout, T *dq) {
+    extern __shared__ __align__(16) float smf[];
+    float *sq = smf, *sdo = sq + kRows * kPitch<D>, *sk = sdo + kRows * kPitch<D>;
+    float *sv = sk + 32 * kPitch<D>, *sds = sv + 32 * kPitch<D>;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
+    const int i0 = blockIdx.x * kRows;
+    const Sequence seq = sequence(p, b);
+    const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + kRows);
+    const T *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
+    const T *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
+    load_rows<D, kRows>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    load_rows<D, kRows>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
+    RowKeys rk[4];
+    float lm[4], dl[4];
+    uint64_t o[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = i0 + 4 * ty + i;
+        rk[i] = row_keys(p, seq, r);
+        const int64_t at = ((int64_t)b * p.H + h) * p.Nq + r;
+        lm[i] = r < p.Nq ? lse[at] * (1.f / kLn2) : 0.f;
+        dl[i] = r < p.Nq ? delta[at] : 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 32; x++) o[i][x] = 0;
+    }
+    for (int it = 0; it < kt.count(); it++) {
+        const int j0 = kt.tile(it) * 32;
+        __syncthreads();
+        load_rows<D, 32>(sk, kb, p.k.token, j0, seq.len);
+        load_rows<D, 32>(sv, vb, p.v.token, j0, seq.len);
+        __syncthreads();
+        float s[4][2], dp[4][2];
+        dot_tile<D, 2>(sq, sk, ty, tx, s);
+        dot_tile<D, 2>(sdo, sv, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const float e = exp2f(fmaf(s[i][j], p.scale_log2, -lm[i]));
+                sds[(4 * ty + i) * 36 + tx + 16 * j] =
+                    rk[i].sees(j0 + tx + 16 * j) ? e * (dp[i][j] - dl[i]) : 0.f;
+            }
+        __syncwarp();
+        add_product<D, 32, 36>(sds, sk, ty, tx, o);
+    }
+    const float sc[4] = {p.scale, p.scale, p.scale, p.scale};
+    store_rows<D>(dq + b * g.dq.batch + h * g.dq.head, g.dq.token, i0, p.Nq, ty, tx, o, sc);
+}
+
+// dk, dv: 64 keys of one key head against tiles of 32 queries of every head of its
+// group.  dv += P^T dO, dk += dS^T q (times scale at the end).
+template <int D>
+constexpr int dkv_smem() {
+    return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256, 2)
+simt_dkv_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
+                const float *lse, const float *delta, const T *dout, T *dk, T *dv) {
+    extern __shared__ __align__(16) float smf[];
+    float *sk = smf, *sv = sk + kRows * kPitch<D>, *sq = sv + kRows * kPitch<D>;
+    float *sdo = sq + 32 * kPitch<D>, *sw = sdo + 32 * kPitch<D>;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int hk = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv;
+    const int j0 = blockIdx.x * kRows;
+    const Sequence seq = sequence(p, b);
+    int first, last;
+    query_rows(p, seq, j0, j0 + kRows, first, last);
+    load_rows<D, kRows>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);
+    load_rows<D, kRows>(sv, v + b * p.v.batch + hk * p.v.head, p.v.token, j0, seq.len);
+    uint64_t ok[4][D / 32], ov[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int x = 0; x < D / 32; x++) ok[i][x] = ov[i][x] = 0;
+    int rfirst, rlast;
+    real_rows(p, seq, 0, p.Nq, rfirst, rlast);
+    for (int gh = 0; gh < p.G; gh++) {
+        const int h = hk * p.G + gh;
+        const T *qb = q + b * p.q.batch + h * p.q.head;
+        const T *db = dout + b * g.dout.batch + h * g.dout.head;
+        const int64_t row = ((int64_t)b * p.H + h) * p.Nq;
+        for (int i0 = first / 32 * 32; i0 < last; i0 += 32) {
+            __syncthreads();
+            // rows behind the sequence's end enter as zeros, whatever they hold
+            load_rows<D, 32>(sq, qb, p.q.token, i0, rlast);
+            load_rows<D, 32>(sdo, db, g.dout.token, i0, rlast);
+            __syncthreads();
+            float s[4][2], dp[4][2];
+            dot_tile<D, 2>(sk, sq, ty, tx, s);
+            dot_tile<D, 2>(sv, sdo, ty, tx, dp);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int i = i0 + tx + 16 * c;
+                const RowKeys rk = row_keys(p, seq, i);
+                const bool real = rk.hi > 0;
+                const float lm = real ? lse[row + i] * (1.f / kLn2) : 0.f;
+                const float dl = real ? delta[row + i] : 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const bool see = rk.sees(j0 + 4 * ty + r);
+                    const float e = see ? exp2f(fmaf(s[r][c], p.scale_log2, -lm)) : 0.f;
+                    s[r][c] = e;
+                    dp[r][c] = see ? e * (dp[r][c] - dl) : 0.f;
+                    sw[(4 * ty + r) * 36 + tx + 16 * c] = e;
+                }
+            }
+            __syncwarp();
+            add_product<D, 32, 36>(sw, sdo, ty, tx, ov);
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) sw[(4 * ty + r) * 36 + tx + 16 * c] = dp[r][c];
+            __syncwarp();
+            add_product<D, 32, 36>(sw, sq, ty, tx, ok);
+        }
+    }
+    const float sc[4] = {p.scale, p.scale, p.scale, p.scale}, one[4] = {1.f, 1.f, 1.f, 1.f};
+    store_rows<D>(dk + b * g.dk.batch + hk * g.dk.head, g.dk.token, j0, p.Nk, ty, tx, ok, sc);
+    store_rows<D>(dv + b * g.dv.batch + hk * g.dv.head, g.dv.token, j0, p.Nk, ty, tx, ov, one);
+}
+
+// ---------------------------------------------------------------- delta
+// One warp a row; rows without keys get 0 (their dO may be anything).  Bound by
+// memory: dO and O are read once.
+template <typename T>
+__global__ void __launch_bounds__(256)
+row_delta_kernel(WinProblem p, WinGrads g, const T *out, const T *dout, float *delta) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= (int64_t)p.B * p.H * p.Nq) return;
+    const int i = (int)(row % p.Nq), h = (int)(row / p.Nq % p.H), b = (int)(row / p.Nq / p.H);
+    const Sequence seq = sequence(p, b);
+    float sum = 0.f;
+    if (row_keys(p, seq, i).hi > 0) {
+        const T *o = out + b * p.o.batch + h * p.o.head + i * p.o.token;
+        const T *d = dout + b * g.dout.batch + h * g.dout.head + i * g.dout.token;
+        for (int x = lane; x < p.d; x += 32) sum = fmaf(to_f32(o[x]), to_f32(d[x]), sum);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == 0) delta[row] = sum;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int D>
+cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const float *v,
+                      float *out, float *lse, cudaStream_t stream) {
+    cudaError_t e = allow_smem(simt_fwd_kernel<D>, fwd_smem<D>());
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.Nq + kRows - 1) / kRows, p.B * p.H);
+    simt_fwd_kernel<D><<<grid, 256, fwd_smem<D>(), stream>>>(p, q, k, v, out, lse);
+    return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const T *q, const T *k,
+                       const T *v, const float *lse, const float *delta, const T *dout,
+                       T *dq, T *dk, T *dv, cudaStream_t stream) {
+    cudaError_t e = allow_smem(simt_dq_kernel<D, T>, dq_smem<D>());
+    if (e == cudaSuccess) e = allow_smem(simt_dkv_kernel<D, T>, dkv_smem<D>());
+    if (e != cudaSuccess) return e;
+    const dim3 gq((p.Nq + kRows - 1) / kRows, p.B * p.H);
+    simt_dq_kernel<D, T><<<gq, 256, dq_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dq);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const dim3 gk((p.Nk + kRows - 1) / kRows, p.B * p.Hkv);
+    simt_dkv_kernel<D, T><<<gk, 256, dkv_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, const float *v,
+                         float *out, float *lse, cudaStream_t stream) {
+    if (p.d == 32) return forward_d<32>(p, q, k, v, out, lse, stream);
+    if (p.d == 64) return forward_d<64>(p, q, k, v, out, lse, stream);
+    return forward_d<128>(p, q, k, v, out, lse, stream);
+}
+
+template <typename T>
+cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const T *q, const T *k,
+                          const T *v, const float *lse, const float *delta, const T *dout, T *dq,
+                          T *dk, T *dv, cudaStream_t stream) {
+    if (p.d == 32) return backward_d<32>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
+    if (p.d == 64) return backward_d<64>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
+    return backward_d<128>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
+}
+template cudaError_t simt_backward<float>(const WinProblem &, const WinGrads &, const float *,
+                                          const float *, const float *, const float *,
+                                          const float *, const float *, float *, float *, float *,
+                                          cudaStream_t);
+template cudaError_t simt_backward<__nv_bfloat16>(
+    const WinProblem &, const WinGrads &, const __nv_bfloat16 *, const __nv_bfloat16 *,
+    const __nv_bfloat16 *, const float *, const float *, const __nv_bfloat16 *, __nv_bfloat16 *,
+    __nv_bfloat16 *, __nv_bfloat16 *, cudaStream_t);
+
+cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
+                      const void *dout, float *delta, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.B * p.H * p.Nq;
+    const unsigned grid = (unsigned)((rows + 7) / 8);
+    if (dtype == MONARCH_F32)
+        row_delta_kernel<float><<<grid, 256, 0, stream>>>(p, g, (const float *)out,
+                                                          (const float *)dout, delta);
+    else
+        row_delta_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
+            p, g, (const __nv_bfloat16 *)out, (const __nv_bfloat16 *)dout, delta);
+    return cudaGetLastError();
+}
+
+}  // namespace win
+}  // namespace monarch
