@@ -40,7 +40,7 @@ monarch_status validate_window(const monarch_window_desc *c, WinProblem *p) {
     if (c->d != 32 && c->d != 64 && c->d != 128) return MONARCH_ERR_UNSUPPORTED;
     if (c->H % c->Hkv) return MONARCH_ERR_SHAPE;
     if ((int64_t)c->B * c->H > 65535 || c->Nq > (1 << 30) || c->Nk > (1 << 30) ||
-        (int64_t)c->B * c->H * c->Nq >= (1LL << 33))
+        (int64_t)c->B * c->H * c->Nq >= (1LL << 33) || (int64_t)c->B * c->Hkv * c->Nk >= (1LL << 33))
         return MONARCH_ERR_SHAPE;
     const int64_t size = c->dtype == MONARCH_BF16 ? 2 : 4;
     const monarch_strides *all[4] = {&c->q, &c->k, &c->v, &c->out};
@@ -196,10 +196,10 @@ monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
         return status_of(win::simt_backward(p, g, (const float *)q, (const float *)k,
                                             (const float *)v, lse, delta, (const float *)dout,
                                             (float *)dq, (float *)dk, (float *)dv, s));
-    using bf16 = __nv_bfloat16;
-    return status_of(win::simt_backward(p, g, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v,
-                                        lse, delta, (const bf16 *)dout, (bf16 *)dq, (bf16 *)dk,
-                                        (bf16 *)dv, s));
+    int *status = device_status_word();
+    if (!status) return MONARCH_ERR_CUDA;
+    return status_of(win::tc_backward(p, g, q, k, v, lse, delta, dout, dq, dk, dv, status,
+                                      device_wait_limit(), s));
 }
 
 size_t monarch_paged_attn_workspace_bytes(const monarch_window_desc *desc) {

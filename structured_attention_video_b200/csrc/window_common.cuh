@@ -133,10 +133,9 @@ struct WinGrads {
 // SIMT kernels, 32-bit arithmetic (window_simt.cu).
 cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, const float *v,
                          float *out, float *lse, cudaStream_t stream);
-template <typename T>
-cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const T *q, const T *k,
-                          const T *v, const float *lse, const float *delta, const T *dout, T *dq,
-                          T *dk, T *dv, cudaStream_t stream);
+cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
+                          const float *v, const float *lse, const float *delta, const float *dout,
+                          float *dq, float *dk, float *dv, cudaStream_t stream);
 // delta_i = dO_i . O_i of every query row, [B][H][Nq].
 cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
                       const void *dout, float *delta, cudaStream_t stream);
@@ -152,9 +151,14 @@ cudaError_t token_forward(const WinProblem &p, monarch_dtype dtype, const TokenP
                           const void *q, const void *k, const void *v, void *out, float *lse,
                           void *workspace, int *status, cudaStream_t stream);
 
-// Tensor-core kernels, bfloat16 (window_sm100.cu).
+// Tensor-core kernels, bfloat16 (window_sm100.cu, window_bwd_sm100.cu).
 cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const void *v, void *out,
                        float *lse, int *status, long long limit, cudaStream_t stream);
+
+cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
+                        const void *v, const float *lse, const float *delta, const void *dout,
+                        void *dq, void *dk, void *dv, int *status, long long limit,
+                        cudaStream_t stream);
 
 }  // namespace win
 }  // namespace monarch

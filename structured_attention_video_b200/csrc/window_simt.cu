@@ -30,32 +30,17 @@ constexpr int kRows = 64;
 // cover all banks.
 template <int D> constexpr int kPitch = D + 4;
 
-__device__ __forceinline__ float4 load4(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ void store2(float *p, float a, float b) {
-    *reinterpret_cast<float2 *>(p) = make_float2(a, b);
-}
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
-    *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16(a, b);
-}
-
 // Rows [r0, r0 + R) of a [tokens][D] matrix into shared memory; rows outside
 // [0, valid) become zero.
-template <int D, int R, typename T>
-__device__ __forceinline__ void load_rows(float *sm, const T *base, int64_t stride, int r0,
+template <int D, int R>
+__device__ __forceinline__ void load_rows(float *sm, const float *base, int64_t stride, int r0,
                                           int valid) {
     constexpr int kChunks = D / 4;
     for (int i = threadIdx.x; i < R * kChunks; i += 256) {
         const int r = i / kChunks, c = i % kChunks;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r0 + r < valid)
-            x = load4(base + (int64_t)(r0 + r) * stride + c * 4);
+            x = *reinterpret_cast<const float4 *>(base + (int64_t)(r0 + r) * stride + c * 4);
         *reinterpret_cast<float4 *>(sm + r * kPitch<D> + c * 4) = x;
     }
 }
@@ -126,8 +111,8 @@ __device__ __forceinline__ void add_product(const float *w, const float *b, int 
     }
 }
 
-template <int D, typename T>
-__device__ __forceinline__ void store_rows(T *base, int64_t stride, int r0, int valid, int ty,
+template <int D>
+__device__ __forceinline__ void store_rows(float *base, int64_t stride, int r0, int valid, int ty,
                                            int tx, const uint64_t (&o)[4][D / 32],
                                            const float (&scale)[4]) {
 #pragma unroll
@@ -138,7 +123,8 @@ __device__ __forceinline__ void store_rows(T *base, int64_t stride, int r0, int 
         for (int q = 0; q < D / 32; q++) {
             float lo, hi;
             f2_unpack(o[i][q], lo, hi);
-            store2(base + (int64_t)r * stride + 2 * tx + 32 * q, lo * scale[i], hi * scale[i]);
+            *reinterpret_cast<float2 *>(base + (int64_t)r * stride + 2 * tx + 32 * q) =
+                make_float2(lo * scale[i], hi * scale[i]);
         }
     }
 }
@@ -247,10 +233,10 @@ constexpr int dq_smem() {
     return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(256, 2)
-simt_dq_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
-               const float *lse, const float *delta, const T *dout, T *dq) {
+simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
+               const float *lse, const float *delta, const float *dout, float *dq) {
     extern __shared__ __align__(16) float smf[];
     float *sq = smf, *sdo = sq + kRows * kPitch<D>, *sk = sdo + kRows * kPitch<D>;
     float *sv = sk + 32 * kPitch<D>, *sds = sv + 32 * kPitch<D>;
@@ -259,8 +245,8 @@ simt_dq_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
     const int i0 = blockIdx.x * kRows;
     const Sequence seq = sequence(p, b);
     const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + kRows);
-    const T *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
-    const T *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
+    const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
+    const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
     load_rows<D, kRows>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
     load_rows<D, kRows>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
     RowKeys rk[4];
@@ -307,10 +293,10 @@ constexpr int dkv_smem() {
     return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(256, 2)
-simt_dkv_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
-                const float *lse, const float *delta, const T *dout, T *dk, T *dv) {
+simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
+                const float *lse, const float *delta, const float *dout, float *dk, float *dv) {
     extern __shared__ __align__(16) float smf[];
     float *sk = smf, *sv = sk + kRows * kPitch<D>, *sq = sv + kRows * kPitch<D>;
     float *sdo = sq + 32 * kPitch<D>, *sw = sdo + 32 * kPitch<D>;
@@ -331,8 +317,8 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const T *q, const T *k, const T *v,
     real_rows(p, seq, 0, p.Nq, rfirst, rlast);
     for (int gh = 0; gh < p.G; gh++) {
         const int h = hk * p.G + gh;
-        const T *qb = q + b * p.q.batch + h * p.q.head;
-        const T *db = dout + b * g.dout.batch + h * g.dout.head;
+        const float *qb = q + b * p.q.batch + h * p.q.head;
+        const float *db = dout + b * g.dout.batch + h * g.dout.head;
         const int64_t row = ((int64_t)b * p.H + h) * p.Nq;
         for (int i0 = first / 32 * 32; i0 < last; i0 += 32) {
             __syncthreads();
@@ -412,19 +398,19 @@ cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const
     return cudaGetLastError();
 }
 
-template <int D, typename T>
-cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const T *q, const T *k,
-                       const T *v, const float *lse, const float *delta, const T *dout,
-                       T *dq, T *dk, T *dv, cudaStream_t stream) {
-    cudaError_t e = allow_smem(simt_dq_kernel<D, T>, dq_smem<D>());
-    if (e == cudaSuccess) e = allow_smem(simt_dkv_kernel<D, T>, dkv_smem<D>());
+template <int D>
+cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
+                       const float *v, const float *lse, const float *delta, const float *dout,
+                       float *dq, float *dk, float *dv, cudaStream_t stream) {
+    cudaError_t e = allow_smem(simt_dq_kernel<D>, dq_smem<D>());
+    if (e == cudaSuccess) e = allow_smem(simt_dkv_kernel<D>, dkv_smem<D>());
     if (e != cudaSuccess) return e;
     const dim3 gq((p.Nq + kRows - 1) / kRows, p.B * p.H);
-    simt_dq_kernel<D, T><<<gq, 256, dq_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dq);
+    simt_dq_kernel<D><<<gq, 256, dq_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dq);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 gk((p.Nk + kRows - 1) / kRows, p.B * p.Hkv);
-    simt_dkv_kernel<D, T><<<gk, 256, dkv_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
+    simt_dkv_kernel<D><<<gk, 256, dkv_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
     return cudaGetLastError();
 }
 
@@ -437,22 +423,13 @@ cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, co
     return forward_d<128>(p, q, k, v, out, lse, stream);
 }
 
-template <typename T>
-cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const T *q, const T *k,
-                          const T *v, const float *lse, const float *delta, const T *dout, T *dq,
-                          T *dk, T *dv, cudaStream_t stream) {
+cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
+                          const float *v, const float *lse, const float *delta, const float *dout,
+                          float *dq, float *dk, float *dv, cudaStream_t stream) {
     if (p.d == 32) return backward_d<32>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
     if (p.d == 64) return backward_d<64>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
     return backward_d<128>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
 }
-template cudaError_t simt_backward<float>(const WinProblem &, const WinGrads &, const float *,
-                                          const float *, const float *, const float *,
-                                          const float *, const float *, float *, float *, float *,
-                                          cudaStream_t);
-template cudaError_t simt_backward<__nv_bfloat16>(
-    const WinProblem &, const WinGrads &, const __nv_bfloat16 *, const __nv_bfloat16 *,
-    const __nv_bfloat16 *, const float *, const float *, const __nv_bfloat16 *, __nv_bfloat16 *,
-    __nv_bfloat16 *, __nv_bfloat16 *, cudaStream_t);
 
 cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
                       const void *dout, float *delta, cudaStream_t stream) {
