@@ -22,6 +22,13 @@
 // memory, each half of the columns in its own place, so no warp waits for another
 // before it writes; a later product into the same columns follows in issue order.
 // In the dq kernel S has two buffers: dP(j+1) dQ(j) S(j+2) after dS(j).
+//
+// delta comes from out as the forward rounded it, an error of 2^-8 |dO.O| at most.  A
+// row of n keys of like weight has |O| of about n^(-1/2) |v|, so against dP it matters
+// for few keys only.  Query tiles of up to kExactTiles key tiles therefore first walk
+// their keys once for delta = sum P dP from the same products that form dS, and the dq
+// kernel runs first to hand it to the dk/dv kernel.  (Two padded causal
+// sequences of 1023 and 681 tokens, d = 64: dq is 2.6e-3 from 64 bits without it.)
 // Bound by the tensor pipe: 4 (3) products of 128 x 128 x d a tile against 16384
 // exponentials at 16 a clock.
 #include "window_tc.cuh"
@@ -32,6 +39,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 384;
+constexpr int kExactTiles = 3;
 
 // Shared memory: two fixed tiles of 128 rows, two stages of two streamed ones.
 template <int D> struct BwdLayout {
@@ -47,7 +55,8 @@ template <int D> struct BwdLayout {
 struct BwdArgs {
     WinProblem p;
     WinGrads g;
-    const float *lse, *delta;
+    const float *lse;
+    float *delta;   // of the rounded out; rows of few keys are written again (dq kernel)
     __nv_bfloat16 *dq, *dk, *dv;
     int *status;
     long long limit;
@@ -116,7 +125,7 @@ struct Bars {
     uint64_t *stats_full;    // [2 stages] (dkv)
     uint64_t *s_full;        // [2] S in tensor memory (dkv uses the first)
     uint64_t *dp_full;
-    uint64_t *p_full;        // 8 warps (dkv)
+    uint64_t *p_full;        // 8 warps (dkv; in dq the halves of delta, once)
     uint64_t *ds_full;       // 8 warps
     uint64_t *acc_full;      // the last products
     uint64_t *stall_bar;
@@ -401,6 +410,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = align1024(smem_raw);
     const Bars bar = make_bars(sm + L::kBar);
+    float *half_delta = reinterpret_cast<float *>(sm + L::kStats);   // [2 halves][128]
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the last tiles first: they see the most keys under a causal mask
@@ -408,7 +418,9 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int i0 = ((int)gridDim.x - 1 - (int)blockIdx.x) / (p.B * p.H) * 128;
     const Sequence seq = sequence(p, b);
     const KeyTiles kt = key_tiles<128>(p, seq, i0, i0 + 128);
-    const int n = kt.count();
+    const int nt = kt.count();
+    // the first n - nt steps only sum delta
+    const int n = nt <= kExactTiles ? 2 * nt : nt;
     __nv_bfloat16 *const dq = a.dq + b * a.g.dq.batch + h * a.g.dq.head;
 
     if (n == 0) {
@@ -438,7 +450,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
             const int st = i & 1;
             if (i >= 2 && !wait_warp(bar.stage_empty + st, ((i >> 1) - 1) & 1, w)) break;
             if (lane == 0) {
-                const int j0 = kt.tile(i) * 128;
+                const int j0 = kt.tile(i % nt) * 128;
                 uint8_t *dst = sm + L::kRing + st * 2 * kTile;
                 mbar_expect_tx(bar.first_full + st, kTile);
                 for (int pn = 0; pn < PN; pn++)
@@ -486,10 +498,10 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (!(ok = spin_warp(bar.ds_full, i & 1, w))) break;
             if (i + 1 < n && !(ok = issue_dp(i + 1))) break;
             tc_fence_after();
-            for (int hh = 0; hh < 2; hh++)
+            for (int hh = 0; hh < 2 && i >= n - nt; hh++)
                 mma4_ts_mn64(tmem + 384, tmem + 128 * st + 64 * hh,
                              dKt + st * kStageDesc + hh * kHalfDesc, idO,
-                             i > 0 || hh > 0 ? 1u : 0u);
+                             i > n - nt || hh > 0 ? 1u : 0u);
             mma_commit_warp(bar.stage_empty + st);
             if (i + 2 < n) ok = issue_s(i + 2);
         }
@@ -501,12 +513,12 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         const RowKeys rk = row_keys(p, seq, i);
         const int64_t at = ((int64_t)b * p.H + h) * p.Nq + i;
         const bool real = rk.hi > 0;
-        const float nl = real ? -a.lse[at] * kLog2e : 0.f, nd = real ? -a.delta[at] : 0.f;
+        const float nl = real ? -a.lse[at] * kLog2e : 0.f;
+        float nd = real && n == nt ? -a.delta[at] : 0.f;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
-        const uint64_t nd2 = f2_pack(nd, nd);
         bool ok = true;
         for (int it = 0; it < n; it++) {
-            const int st = it & 1, c0 = kt.tile(it) * 128 + 64 * half;
+            const int st = it & 1, c0 = kt.tile(it % nt) * 128 + 64 * half;
             if (!(ok = wait_warp(bar.s_full + st, (it >> 1) & 1, w))) break;
             tc_fence_after();
             float x[64];
@@ -524,15 +536,41 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                 x[k] = fast_exp2(lo);
                 x[k + 1] = fast_exp2(hi);
             }
-            if (kt.tile(it) * 128 + 128 > seq.len) {
+            if (kt.tile(it % nt) * 128 + 128 > seq.len) {
                 // keys past the sequence may hold anything, and 0 * NaN is NaN: they become
                 // zeros before the product over the keys (S of this tile is done with them)
-                zero_rows(sm + L::kRing + st * 2 * kTile, max(0, seq.len - kt.tile(it) * 128), 128,
+                zero_rows(sm + L::kRing + st * 2 * kTile, max(0, seq.len - kt.tile(it % nt) * 128), 128,
                           PN, kPanel, half * 128 + row, 256);
                 fence_proxy_async_smem();
             }
             if (!(ok = wait_warp(bar.dp_full, it & 1, w))) break;
             tc_fence_after();
+            if (it < n - nt) {
+                // this half's part of delta = sum P dP; the halves meet in shared memory
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float y[32];
+                    tmem_ld32f(tl + 256 + c, y);
+                    tmem_wait_ld();
+                    const uint32_t s = (uint32_t)(see >> c);
+#pragma unroll
+                    for (int k = 0; k < 32; k++)
+                        sum = fmaf((s >> k) & 1 ? x[c + k] : 0.f, (s >> k) & 1 ? y[k] : 0.f, sum);
+                }
+                nd -= sum;
+                if (it == n - nt - 1) {
+                    half_delta[half * 128 + row] = nd;
+                    mbar_arrive_warp(bar.p_full);
+                    if (!(ok = wait_warp(bar.p_full, 0, w))) break;
+                    nd = half_delta[row] + half_delta[128 + row];
+                    if (half == 0 && real) a.delta[at] = -nd;
+                }
+                tc_fence_before();
+                mbar_arrive_warp(bar.ds_full);
+                continue;
+            }
+            const uint64_t nd2 = f2_pack(nd, nd);
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
@@ -587,17 +625,18 @@ cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const 
     if (e != cudaSuccess) return e;
     const unsigned gk = (unsigned)p.B * p.Hkv * ((p.Nk + 127) / 128);
     const unsigned gq = (unsigned)p.B * p.H * ((p.Nq + 127) / 128);
-    tc_window_dkv_kernel<D><<<gk, kThreads, smem, stream>>>(mq, mk, mv, md, a);
+    // dq first: it completes delta
+    tc_window_dq_kernel<D><<<gq, kThreads, smem, stream>>>(mq, mk, mv, md, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    tc_window_dq_kernel<D><<<gq, kThreads, smem, stream>>>(mq, mk, mv, md, a);
+    tc_window_dkv_kernel<D><<<gk, kThreads, smem, stream>>>(mq, mk, mv, md, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
-                        const void *v, const float *lse, const float *delta, const void *dout,
+                        const void *v, const float *lse, float *delta, const void *dout,
                         void *dq, void *dk, void *dv, int *status, long long limit,
                         cudaStream_t stream) {
     BwdArgs a;

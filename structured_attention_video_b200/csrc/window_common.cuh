@@ -156,7 +156,7 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
                        float *lse, int *status, long long limit, cudaStream_t stream);
 
 cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
-                        const void *v, const float *lse, const float *delta, const void *dout,
+                        const void *v, const float *lse, float *delta, const void *dout,
                         void *dq, void *dk, void *dv, int *status, long long limit,
                         cudaStream_t stream);
 

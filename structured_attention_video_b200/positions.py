@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .window import _DTYPES, _LAYOUTS, _check, _fill, _index_tensor, _on_device, _strides
+from .window import _DTYPES, _LAYOUTS, _check, _fill, _index_tensor, _launch, _strides
 
 _STYLES = ("interleaved", "half")
 _SCALINGS = {None: _lib.ROTARY_PLAIN, "linear": _lib.ROTARY_LINEAR, "ntk": _lib.ROTARY_NTK,
@@ -44,8 +44,8 @@ def _run(q, k, freqs, dims, style, grid, positions, start, magnitude, layout, ou
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("expected 4-D tensors")
     if out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        q_out = torch.empty_like(q)
+        k_out = None if k is None else torch.empty_like(k)
     else:
         q_out, k_out = out
         if (k is None) != (k_out is None):
@@ -102,11 +102,9 @@ def _run(q, k, freqs, dims, style, grid, positions, start, magnitude, layout, ou
     if k is not None:
         _fill(desc.k, _strides(k, head, token, d))
         _fill(desc.k_out, _strides(k_out, head, token, d))
-    with _on_device(q.device):
-        _lib.check(_lib.monarch_rotary(
-            desc, q.data_ptr(), None if k is None else k.data_ptr(), freqs.data_ptr(),
-            q_out.data_ptr(), None if k is None else k_out.data_ptr(),
-            torch.cuda.current_stream(q.device).cuda_stream), "monarch_rotary")
+    _launch(q.device, _lib.monarch_rotary, "monarch_rotary", desc, q.data_ptr(),
+            None if k is None else k.data_ptr(), freqs.data_ptr(), q_out.data_ptr(),
+            None if k is None else k_out.data_ptr())
     return q_out, k_out
 
 

@@ -95,26 +95,30 @@ def _describe(q, k, v, out, window, sinks, frame, lengths, starts, scale, layout
 
 def _workspace(need, workspace, device):
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        # (at least a byte: where validation failed, the call itself says why)
+        return torch.empty(need or 1, dtype=torch.uint8, device=device)
     if workspace.device != device:
         raise ValueError("workspace must be on the inputs' device")
     return workspace
 
 
-class _on_device:
-    """Makes the tensors' device current for the launch where it is not."""
+# The handle of torch's current stream on a device: torch.cuda.current_stream() without
+# the Stream object (2.2 us a call, a tenth of a short call's host time).
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else \
-            torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(device, call, where, *args):
+    """call(*args, stream) on the device's current stream, with the tensors' device
+    current for the launch where it is not."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = call(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _stream(index))
+    if status:
+        _lib.check(status, where)
 
 
 def window_attention(q, k, v, *, window=(-1, 0), sinks=0, frame=1, lengths=None, starts=None,
@@ -130,19 +134,15 @@ def window_attention(q, k, v, *, window=(-1, 0), sinks=0, frame=1, lengths=None,
     newest tokens.  scale defaults to 1/sqrt(d).  Returns out, or (out, lse) with lse
     float32 [B, H, Nq] (natural logarithm, -inf in rows that see nothing)."""
     if out is None:
-        # q's own memory order, without the gaps that a slice would have
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     desc = _describe(q, k, v, out, window, sinks, frame, lengths, starts, scale, layout)
     lse = None
     if return_lse:
         lse = torch.empty((desc.B, desc.H, desc.Nq), dtype=torch.float32, device=q.device)
     ws = _workspace(_lib.monarch_window_attn_workspace_bytes(desc), workspace, q.device)
-    with _on_device(q.device):
-        _lib.check(_lib.monarch_window_attn_fwd_ws(
-            desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr() if return_lse else None, ws.data_ptr(),
-            ws.numel() * ws.element_size(), torch.cuda.current_stream(q.device).cuda_stream),
-            "monarch_window_attn_fwd_ws")
+    _launch(q.device, _lib.monarch_window_attn_fwd_ws, "monarch_window_attn_fwd_ws", desc,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size())
     return (out, lse) if return_lse else out
 
 
@@ -167,20 +167,16 @@ def window_attention_backward(q, k, v, out, lse, dout, *, window=(-1, 0), sinks=
     if lse.dtype != torch.float32 or lse.shape != (desc.B, desc.H, desc.Nq) or \
             lse.device != q.device or not lse.is_contiguous():
         raise ValueError("lse must be the forward's contiguous float32 [B, H, Nq]")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     head, token = (1, 2) if layout == "bhnd" else (2, 1)
     grads = _lib.WindowGrads()
     for field, t in ((grads.dout, dout), (grads.dq, dq), (grads.dk, dk), (grads.dv, dv)):
         _fill(field, _strides(t, head, token, desc.d))
     ws = _workspace(_lib.monarch_window_attn_bwd_workspace_bytes(desc), workspace, q.device)
-    with _on_device(q.device):
-        _lib.check(_lib.monarch_window_attn_bwd_ws(
-            desc, grads, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-            ws.data_ptr(), ws.numel() * ws.element_size(),
-            torch.cuda.current_stream(q.device).cuda_stream), "monarch_window_attn_bwd_ws")
+    _launch(q.device, _lib.monarch_window_attn_bwd_ws, "monarch_window_attn_bwd_ws", desc, grads,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size())
     return dq, dk, dv
 
 
@@ -201,7 +197,7 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, *, window=(-1, 0),
     if layout not in _LAYOUTS:
         raise ValueError("layout must be one of %s" % (list(_LAYOUTS),))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     _check(q, k_pages, v_pages, out)
     B, H, d = q.shape
     head, token = (1, 2) if layout == "bhnd" else (2, 1)
@@ -226,11 +222,8 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, *, window=(-1, 0),
     _fill(desc.v, _strides(v_pages, head, token, d))
     lse = torch.empty((B, H, 1), dtype=torch.float32, device=q.device) if return_lse else None
     ws = _workspace(_lib.monarch_paged_attn_workspace_bytes(desc), workspace, q.device)
-    with _on_device(q.device):
-        _lib.check(_lib.monarch_paged_attn_ws(
-            desc, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+    _launch(q.device, _lib.monarch_paged_attn_ws, "monarch_paged_attn_ws", desc, q.data_ptr(),
+            k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
             page_table.stride(0) if B > 1 else width, page, k_pages.shape[0], out.data_ptr(),
-            lse.data_ptr() if return_lse else None, ws.data_ptr(),
-            ws.numel() * ws.element_size(), torch.cuda.current_stream(q.device).cuda_stream),
-            "monarch_paged_attn_ws")
+            lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size())
     return (out, lse) if return_lse else out
