@@ -467,7 +467,7 @@ typedef struct {
 
 /*
  * Workspace bytes of monarch_window_attn_fwd_ws, or 0 if the arguments fail
- * validation (256 where none is needed).  Pure host function.
+ * validation; 256 where none is needed (workspace may then be NULL).  Pure host function.
  * Source: no counterpart in the pages (a property of this implementation).
  */
 MONARCH_API size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc);

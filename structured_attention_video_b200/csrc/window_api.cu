@@ -94,11 +94,16 @@ monarch_status run_token(const WinProblem &p, monarch_dtype dtype, const void *q
                          const void *v, void *out, float *lse, void *workspace, size_t ws_bytes,
                          cudaStream_t stream) {
     const win::TokenPlan plan = win::token_plan(p, dtype);
-    if (ws_bytes < at_least_256(plan.bytes)) return MONARCH_ERR_NO_MEMORY;
+    if (plan.bytes > 0) {
+        if (!workspace) return MONARCH_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return MONARCH_ERR_ALIGN;
+        if (ws_bytes < at_least_256(plan.bytes)) return MONARCH_ERR_NO_MEMORY;
+    }
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
     return status_of(
-        win::token_forward(p, dtype, plan, q, k, v, out, lse, workspace, status, stream));
+        win::token_forward(p, dtype, plan, q, k, v, out, lse, workspace, status,
+                           device_wait_limit(), stream));
 }
 
 // The page table's part of a paged call; p comes from validate_window.
@@ -138,14 +143,13 @@ monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc *desc, const
                                           const void *k, const void *v, void *out, float *lse,
                                           void *workspace, size_t ws_bytes,
                                           monarch_stream_t stream) {
-    if (!q || !k || !v || !out || !workspace) return MONARCH_ERR_INVALID_ARG;
+    if (!q || !k || !v || !out) return MONARCH_ERR_INVALID_ARG;
     WinProblem p;
     const monarch_status st = validate_window(desc, &p);
     if (st != MONARCH_OK) return st;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
-        !aligned4(lse) || !aligned4(p.lengths) || !aligned4(p.starts) || !aligned(workspace, 256))
+        !aligned4(lse) || !aligned4(p.lengths) || !aligned4(p.starts))
         return MONARCH_ERR_ALIGN;
-    if (ws_bytes < 256) return MONARCH_ERR_NO_MEMORY;
     const int path = choose(p, desc->dtype);
     cudaStream_t s = (cudaStream_t)stream;
     if (path == kPathToken)
@@ -213,7 +217,7 @@ monarch_status monarch_paged_attn_ws(const monarch_window_desc *desc, const void
                                      const int32_t *page_table, int64_t table_stride,
                                      int32_t page_size, int32_t num_pages, void *out, float *lse,
                                      void *workspace, size_t ws_bytes, monarch_stream_t stream) {
-    if (!q || !k_pages || !v_pages || !page_table || !out || !workspace)
+    if (!q || !k_pages || !v_pages || !page_table || !out)
         return MONARCH_ERR_INVALID_ARG;
     WinProblem p;
     const monarch_status st = validate_paged(desc, &p);
@@ -223,9 +227,8 @@ monarch_status monarch_paged_attn_ws(const monarch_window_desc *desc, const void
         return MONARCH_ERR_UNSUPPORTED;
     if (p.Nk % page_size || (p.B > 1 && table_stride < p.Nk / page_size)) return MONARCH_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-        !aligned4(page_table) || !aligned4(lse) || !aligned4(p.lengths) || !aligned(workspace, 256))
+        !aligned4(page_table) || !aligned4(lse) || !aligned4(p.lengths))
         return MONARCH_ERR_ALIGN;
-    if (ws_bytes < 256) return MONARCH_ERR_NO_MEMORY;
     p.table = page_table;
     p.table_stride = table_stride;
     p.page_shift = 0;

@@ -144,12 +144,13 @@ cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtyp
 struct TokenPlan {
     int row_tiles;   // tiles of 16 rows (query, head of the group) a key head
     int splits;      // parts of the visible keys
-    size_t bytes;    // workspace
+    int clusters;    // groups of parts that join inside a thread-block cluster
+    size_t bytes;    // workspace: none for one cluster
 };
 TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype);
 cudaError_t token_forward(const WinProblem &p, monarch_dtype dtype, const TokenPlan &plan,
                           const void *q, const void *k, const void *v, void *out, float *lse,
-                          void *workspace, int *status, cudaStream_t stream);
+                          void *workspace, int *status, long long limit, cudaStream_t stream);
 
 // Tensor-core kernels, bfloat16 (window_sm100.cu, window_bwd_sm100.cu).
 cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const void *v, void *out,

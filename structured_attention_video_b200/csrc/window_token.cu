@@ -3,39 +3,46 @@
 //
 // The work is reading the visible keys and values once, so the keys of one
 // (sequence, key head) are split over CTAs, each with its own running maximum, sum
-// and weighted values, and a second kernel joins the parts:
+// and weighted values, and joined:
 //   M = max_s m_s,  O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// Up to 8 parts form a thread-block cluster and join through distributed shared
+// memory: one launch and no workspace.  More parts (few key heads, long caches) are
+// several clusters, whose results a second kernel joins.  Every join adds the parts
+// in their order, so results do not depend on which CTA came first.
 // The rows of a key head (queries x heads of its group) form tiles of 16, the height
 // of mma.m16n8k16: every key is read once for all of them.  The split counts the
 // visible keys only (the sinks, then the window), from each sequence's own length,
 // so ragged batches and windows divide evenly.
 //
-// bfloat16: each warp takes groups of 16 keys; keys and values go from global
-// memory straight to the fragments.  The head dimension of the first product and the
-// columns of the second are permuted so that each lane's 16-byte loads are whole
-// fragments: lane (n, t) = (lane / 4, lane % 4) reads elements 32 kb + 8 t .. + 7 of
-// key n, four fragment registers of two K-steps, and elements 8 n .. + 7 (+ 64 h) of
-// the value rows 2 t and 2 t + 1, which byte permutes pair up along the keys.
+// bfloat16: one warp loads 64-key tiles of keys and values into a ring of stages (TMA;
+// behind a page table one copy a page, 128-byte swizzle), four warps take 16 keys of
+// each tile through ldmatrix and mma.sync.  The ring keeps the bytes in flight that
+// the memory's latency needs whatever the warps wait for; loading fragments straight
+// from global memory to registers reached 4.1 TB/s instead.  (The products need a tenth of
+// the legacy tensor rate here; tcgen05 would spend a 128-row tile on 16 rows.)
 // float32: FMA pipes, tiles of 32 keys through shared memory, one lane a key.
-#include "tc_primitives.cuh"
-#include "window_common.cuh"
+#include "window_tc.cuh"
+
+#include <cooperative_groups.h>
 
 namespace monarch {
 namespace win {
 namespace {
 
-using tc::fast_exp2;
-using tc::pack_bf16;
+namespace cg = cooperative_groups;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTokWarps = 4;
-constexpr int kTokThreads = kTokWarps * 32;
+constexpr int kTokWarps = 4;                       // of the arithmetic
+constexpr int kTokThreads = kTokWarps * 32;        // float32; one loading warp more for bfloat16
+constexpr int kMaxCluster = 8;
 
 struct TokenArgs {
     WinProblem p;
-    int row_tiles, splits;
-    float *part;   // [B * Hkv * row_tiles][splits][16][d + 2]: O, m, l (splits > 1)
+    int row_tiles, splits;   // splits: parts of the keys, `clusters` times the cluster size
+    int clusters;
+    float *part;   // [B * Hkv * row_tiles][clusters][16][d + 2]: O, m, l (clusters > 1)
     int *status;
+    long long limit;
 };
 
 // Where the rows of one key head lie: a contiguous cache, or behind the page table.
@@ -105,262 +112,367 @@ __device__ __forceinline__ TokenUnit token_unit(const TokenArgs &a) {
     return u;
 }
 
-// Row rr's part (16 rows of d values, then m and l) or, with one split, its output.
-__device__ __forceinline__ float *part_row(const TokenArgs &a, const TokenUnit &u, int r) {
-    const int64_t unit = ((int64_t)blockIdx.z * a.row_tiles + u.rt) * a.splits + u.split;
-    return a.part + (unit * 16 + r) * (a.p.d + 2);
-}
-
-template <typename T>
 __device__ __forceinline__ void write_lse(const WinProblem &p, float *lse, int b, int h, int i,
                                           float m, float l) {
     if (lse)
         lse[((int64_t)b * p.H + h) * p.Nq + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// ---------------------------------------------------------------- bfloat16
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16 *p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
+// ---------------------------------------------------------------- join in a cluster
+// One CTA's part of a row tile in shared memory: row r at r * (d + 4), its maximum and
+// sum (log2 units) behind the rows.
+template <int D> struct Part {
+    static constexpr int kPitch = D + 4;
+    static constexpr int kFloats = 16 * kPitch + 32;
+};
+
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
 }
-__device__ __forceinline__ uint2 load8(const __nv_bfloat16 *p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(r.x), "=r"(r.y)
-                 : "l"(p));
-    return r;
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
 }
 
-// c += a b: a 16 x 16 (row), b 16 x 8 (column), bfloat16 with float32 sums.
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <int D>
-__global__ void __launch_bounds__(kTokThreads)
-token_bf16_kernel(TokenArgs a, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                  const __nv_bfloat16 *v, __nv_bfloat16 *out, float *lse) {
-    constexpr int KB = D / 32;                // 32-element blocks of the head dimension
-    constexpr int E = D >= 64 ? 8 : 4;        // value elements a lane reads at once
-    constexpr int VH = D / (8 * E);           // such reads a row
-    constexpr int VW = E / 2;                 // registers of one
-    __shared__ float so[kTokWarps][16][D + 4];
-    __shared__ float sml[kTokWarps][16][2];
+// Joins the parts of the cluster's CTAs (a CTA alone: its own) and writes the rows, or
+// with several clusters their part to the workspace.  The CTAs share the elements out.
+template <int D, typename T>
+__device__ __forceinline__ void join_cluster(const TokenArgs &a, const TokenUnit &u, float *part,
+                                             T *out, float *lse) {
+    constexpr int kPitch = Part<D>::kPitch;
     const WinProblem &p = a.p;
-    const TokenUnit u = token_unit<16>(a);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
-    const int rows = p.Nq * p.G;
-    const __nv_bfloat16 *kb = k + u.hk * p.k.head + (p.table ? 0 : u.b * p.k.batch);
-    const __nv_bfloat16 *vb = v + u.hk * p.v.head + (p.table ? 0 : u.b * p.v.batch);
-    const KeyPlace kp = key_place(p, u.b, p.k.token, p.k.batch, a.status);
-    const KeyPlace vp = key_place(p, u.b, p.v.token, p.v.batch, a.status);
-
-    uint4 qf[2][KB];
-    RowKeys rk[2];
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-        const int rr = u.rt * 16 + n + 8 * x;
-        rk[x] = RowKeys{0, 0, 0};
-        const bool real = rr < rows;
-        const int i = rr / p.G, h = u.hk * p.G + rr % p.G;
-        if (real) rk[x] = row_keys(p, u.seq, i);
-#pragma unroll
-        for (int c = 0; c < KB; c++) {
-            qf[x][c] = make_uint4(0, 0, 0, 0);
-            if (real && rk[x].hi > 0)
-                qf[x][c] = load16(q + u.b * p.q.batch + h * p.q.head + i * p.q.token + c * 32 + t * 8);
-        }
-    }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[VH][E][4];
-#pragma unroll
-    for (int x = 0; x < VH; x++)
-#pragma unroll
-        for (int e = 0; e < E; e++)
-#pragma unroll
-            for (int c = 0; c < 4; c++) o[x][e][c] = 0.f;
-
-    uint4 kf[2][KB];
-    uint32_t vf[2][2][VH][VW];   // [8-key tile][key 2t or 2t + 1]
-    bool there[2];               // the tile's page exists (load_k)
-    auto load_k = [&](int g) {
-        const int j0 = u.kt.tile(g) * 16;
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-            const int j = j0 + 8 * x + n;
-            // (pages hold at least 8 keys: the table has an entry for all 8 or none)
-            const int64_t at = u.meets(j0 + 8 * x, 8) ? kp.at(j) : -1;
-            there[x] = at >= 0;
-#pragma unroll
-            for (int c = 0; c < KB; c++) {
-                kf[x][c] = make_uint4(0, 0, 0, 0);
-                if (at >= 0 && j < u.seq.len) kf[x][c] = load16(kb + at + c * 32 + t * 8);
-            }
-        }
-    };
-    auto load_v = [&](int g) {
-        const int j0 = u.kt.tile(g) * 16;
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-            const int j = j0 + 8 * x + 2 * t;
-            const int64_t at = u.meets(j0 + 8 * x, 8) ? vp.at(j) : -1;
-#pragma unroll
-            for (int y = 0; y < 2; y++)   // a value that no row sees is not read: 0 * NaN is NaN
-#pragma unroll
-                for (int c = 0; c < VH; c++) {
-                    uint32_t *r = vf[x][y][c];
-                    const __nv_bfloat16 *src = vb + at + y * p.v.token + c * 64 + n * E;
-                    const bool read = at >= 0 && u.any.sees(j + y);
-                    if (E == 8) {
-                        const uint4 w = read ? load16(src) : make_uint4(0, 0, 0, 0);
-                        r[0] = w.x, r[1] = w.y, r[VW - 2] = w.z, r[VW - 1] = w.w;
-                    } else {
-                        const uint2 w = read ? load8(src) : make_uint2(0, 0);
-                        r[0] = w.x, r[1] = w.y;
-                    }
-                }
-        }
-    };
-
-    int g = u.g0 + warp;
-    if (g < u.g1) {
-        load_k(g);
-        load_v(g);
-    }
-    for (; g < u.g1; g += kTokWarps) {
-        const int j0 = u.kt.tile(g) * 16;
-        const bool next = g + kTokWarps < u.g1;
-        float s[2][4];
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-#pragma unroll
-            for (int c = 0; c < 4; c++) s[x][c] = 0.f;
-#pragma unroll
-            for (int c = 0; c < KB; c++) {
-                mma16816(s[x], qf[0][c].x, qf[1][c].x, qf[0][c].y, qf[1][c].y, kf[x][c].x, kf[x][c].y);
-                mma16816(s[x], qf[0][c].z, qf[1][c].z, qf[0][c].w, qf[1][c].w, kf[x][c].z, kf[x][c].w);
-            }
-        }
-        const bool th0 = there[0], th1 = there[1];
-        if (next) load_k(g + kTokWarps);
-        // s[x][2 y + c]: row n + 8 y, key j0 + 8 x + 2 t + c
-        float alpha[2];
-        bool moved = false;
-#pragma unroll
-        for (int y = 0; y < 2; y++) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    float &z = s[x][2 * y + c];
-                    const bool see = rk[y].sees(j0 + 8 * x + 2 * t + c) && (x ? th1 : th0);
-                    z = see ? z * p.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, z);
-                }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mx = fmaxf(mx, m[y]);
-            const float safe = mx == -INFINITY ? 0.f : mx;
-            alpha[y] = fast_exp2(m[y] - safe);
-            moved |= mx > m[y];
-            m[y] = mx;
-            float sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    float &z = s[x][2 * y + c];
-                    z = fast_exp2(z - safe);
-                    sum += z;
-                }
-            l[y] = l[y] * alpha[y] + sum;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-            for (int x = 0; x < VH; x++)
-#pragma unroll
-                for (int e = 0; e < E; e++)
-#pragma unroll
-                    for (int c = 0; c < 4; c++) o[x][e][c] *= alpha[c >> 1];
-        }
-        const uint32_t p0 = pack_bf16(s[0][0], s[0][1]), p1 = pack_bf16(s[0][2], s[0][3]);
-        const uint32_t p2 = pack_bf16(s[1][0], s[1][1]), p3 = pack_bf16(s[1][2], s[1][3]);
-#pragma unroll
-        for (int x = 0; x < VH; x++)
-#pragma unroll
-            for (int w = 0; w < VW; w++) {
-                // elements 2w and 2w + 1 of the two keys of each 8-key tile
-                const uint32_t a0 = vf[0][0][x][w], a1 = vf[0][1][x][w];
-                const uint32_t b0 = vf[1][0][x][w], b1 = vf[1][1][x][w];
-                mma16816(o[x][2 * w], p0, p1, p2, p3, __byte_perm(a0, a1, 0x5410),
-                         __byte_perm(b0, b1, 0x5410));
-                mma16816(o[x][2 * w + 1], p0, p1, p2, p3, __byte_perm(a0, a1, 0x7632),
-                         __byte_perm(b0, b1, 0x7632));
-            }
-        if (next) load_v(g + kTokWarps);
-    }
-
-    // the warps' parts meet in shared memory.  o[x][e][2 y + c] is row n + 8 y, column
-    // 64 x + (2 t + c) E + e.
-#pragma unroll
-    for (int y = 0; y < 2; y++) {
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-        const int r = n + 8 * y;
-        if (t == 0) {
-            sml[warp][r][0] = m[y];
-            sml[warp][r][1] = l[y];
-        }
-#pragma unroll
-        for (int x = 0; x < VH; x++)
-#pragma unroll
-            for (int c = 0; c < 2; c++)
-#pragma unroll
-                for (int e = 0; e < E; e += 4)
-                    *reinterpret_cast<float4 *>(&so[warp][r][64 * x + (2 * t + c) * E + e]) =
-                        make_float4(o[x][e][2 * y + c], o[x][e + 1][2 * y + c],
-                                    o[x][e + 2][2 * y + c], o[x][e + 3][2 * y + c]);
-    }
-    __syncthreads();
-    for (int at = threadIdx.x; at < 16 * (D / 4); at += kTokThreads) {
+    const int rows = min(16, p.Nq * p.G - u.rt * 16);
+    const int parts = a.splits / a.clusters;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = parts > 1 ? (int)cluster.block_rank() : 0;
+    if (parts > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    for (int at = rank * blockDim.x + threadIdx.x; at < rows * (D / 4); at += parts * blockDim.x) {
         const int r = at / (D / 4), c = at % (D / 4) * 4;
-        const int rr = u.rt * 16 + r;
-        if (rr >= rows) continue;
-        float mx = -INFINITY;
+        if (c >= p.d) continue;
+        const float *src[kMaxCluster];
+        float m[kMaxCluster], mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kTokWarps; w++) mx = fmaxf(mx, sml[w][r][0]);
+        for (int s = 0; s < kMaxCluster; s++) {
+            if (s >= parts) break;
+            src[s] = parts > 1 ? cluster.map_shared_rank(part, s) : part;
+            m[s] = src[s][16 * kPitch + r];
+            mx = fmaxf(mx, m[s]);
+        }
         const float safe = mx == -INFINITY ? 0.f : mx;
         float sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kTokWarps; w++) {
-            const float f = fast_exp2(sml[w][r][0] - safe);
-            const float4 x = *reinterpret_cast<const float4 *>(&so[w][r][c]);
-            sum += f * sml[w][r][1];
-            acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+        for (int s = 0; s < kMaxCluster; s++) {
+            if (s >= parts) break;
+            const float f = exp2f(m[s] - safe);
+            const float4 x = *reinterpret_cast<const float4 *>(src[s] + r * kPitch + c);
+            sum = fmaf(f, src[s][16 * kPitch + 16 + r], sum);
+            acc.x = fmaf(f, x.x, acc.x);
+            acc.y = fmaf(f, x.y, acc.y);
+            acc.z = fmaf(f, x.z, acc.z);
+            acc.w = fmaf(f, x.w, acc.w);
         }
-        if (a.splits > 1) {
-            float *dst = part_row(a, u, r);
+        if (a.clusters > 1) {
+            const int64_t unit = ((int64_t)blockIdx.z * a.row_tiles + u.rt) * a.clusters;
+            float *dst = a.part + ((unit + u.split / parts) * 16 + r) * (p.d + 2);
             *reinterpret_cast<float2 *>(dst + c) = make_float2(acc.x, acc.y);
             *reinterpret_cast<float2 *>(dst + c + 2) = make_float2(acc.z, acc.w);
-            if (c == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, sum);
+            if (c == 0) *reinterpret_cast<float2 *>(dst + p.d) = make_float2(mx, sum);
         } else {
-            const int i = rr / p.G, h = u.hk * p.G + rr % p.G;
+            const int rr = u.rt * 16 + r, i = rr / p.G, h = u.hk * p.G + rr % p.G;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2 *>(out + u.b * p.o.batch + h * p.o.head + i * p.o.token + c) =
-                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-            if (c == 0) write_lse<float>(p, lse, u.b, h, i, mx, sum);
+            store4(out + u.b * p.o.batch + h * p.o.head + i * p.o.token + c, acc.x * inv,
+                   acc.y * inv, acc.z * inv, acc.w * inv);
+            if (c == 0) write_lse(p, lse, u.b, h, i, mx, sum);
         }
     }
+    if (parts > 1) cluster.sync();   // the others have read this CTA's part
+}
+
+// ---------------------------------------------------------------- bfloat16
+// c += a b: a 16 x 16 (row), b 16 x 8 (column), bfloat16 with float32 sums.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Ring of kStages tiles of 64 keys and values: 96 KB at d = 128, so two CTAs fit on an
+// SM and keep up to 192 KB in flight.
+template <int D> struct Ring {
+    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr uint32_t kPanelBytes = 64 * 128;               // 64 rows of 64 columns
+    static constexpr uint32_t kHalf = (D / 64) * kPanelBytes;       // keys, then values
+    static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr uint32_t kBars = kStages * kStage;             // full, empty, good, abort
+    static constexpr uint32_t kSmem = kBars + 128 + 1024;           // + slack to align the base
+    // after the last tile the ring holds the four warps' parts and the CTA's
+    static_assert(5 * Part<D>::kFloats * 4 <= kBars, "parts fit the ring");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTokThreads + 32)
+token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, TokenArgs a, int box,
+                  const __nv_bfloat16 *q, __nv_bfloat16 *out, float *lse) {
+    using R = Ring<D>;
+    constexpr int NS = R::kStages, PN = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = align1024(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + R::kBars);
+    uint64_t *empty = full + NS;
+    // [stage]: bit g: the page of the tile's keys 8 g .. 8 g + 7 exists
+    volatile uint32_t *good = reinterpret_cast<volatile uint32_t *>(empty + NS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + NS) + NS;
+    const WinProblem &p = a.p;
+    const TokenUnit u = token_unit<64>(a);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
+    const int rows = p.Nq * p.G;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; s++) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, kTokWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const WaitCtx w{a.limit, a.status, abort_flag};
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int x = 0; x < D / 8; x++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[x][c] = 0.f;
+
+    if (warp == kTokWarps) {
+        // ---------------- loads
+        int issued = 0;
+        for (int g = u.g0; g < u.g1; g++) {
+            const int it = g - u.g0, st = it % NS, j0 = u.kt.tile(g) * 64;
+            if (it >= NS && !wait_warp(empty + st, (it / NS - 1) & 1, w)) break;
+            uint8_t *dst = sm + st * R::kStage;
+            if (p.table) {
+                // one box of min(page, 64) keys a lane; pages that hold no visible key, or
+                // are not in the pool, read zeros (a coordinate past the last page)
+                const int jb = j0 + lane * box;
+                const bool mine = lane * box < 64;
+                int pg = p.num_pages;
+                bool bad = false;
+                if (mine && u.meets(jb, box)) {
+                    pg = p.table[u.b * p.table_stride + (jb >> p.page_shift)];
+                    bad = pg < 0 || pg >= p.num_pages;
+                    if (bad) {
+                        record_status(a.status, MONARCH_ERR_INVALID_ARG);
+                        pg = p.num_pages;
+                    }
+                }
+                uint32_t bits = __ballot_sync(0xffffffffu, bad), absent = 0;
+                for (int x = 0; bits && x < 8; x++) absent |= ((bits >> (8 * x / box)) & 1) << x;
+                if (lane == 0) {
+                    good[st] = ~absent;
+                    mbar_expect_tx(full + st, R::kStage);
+                }
+                __syncwarp();
+                if (mine) {
+                    const int row = jb & ((1 << p.page_shift) - 1);
+                    uint8_t *at = dst + lane * box * 128;
+                    for (int pn = 0; pn < PN; pn++) {
+                        tma_load_4d(at + pn * R::kPanelBytes, &tmK, pn * 64, row, u.hk, pg, full + st);
+                        tma_load_4d(at + R::kHalf + pn * R::kPanelBytes, &tmV, pn * 64, row, u.hk, pg,
+                                    full + st);
+                    }
+                }
+            } else if (lane == 0) {
+                good[st] = ~0u;
+                mbar_expect_tx(full + st, R::kStage);
+                for (int pn = 0; pn < PN; pn++) {
+                    tma_load_4d(dst + pn * R::kPanelBytes, &tmK, pn * 64, j0, u.hk, u.b, full + st);
+                    tma_load_4d(dst + R::kHalf + pn * R::kPanelBytes, &tmV, pn * 64, j0, u.hk, u.b,
+                                full + st);
+                }
+            }
+            issued++;
+        }
+        // every issued copy lands before the ring is used for the parts
+        if (lane == 0)
+            for (int it = max(0, issued - NS); it < issued; it++)
+                wait_phase_cleanup(full + it % NS, (it / NS) & 1, kCleanupPolls);
+    } else {
+        // ---------------- rows n and n + 8 of the tile; keys 16 warp .. + 15 of each tile
+        uint32_t qf[D / 16][4];
+        RowKeys rk[2];
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            const int rr = u.rt * 16 + n + 8 * y, i = rr / p.G;
+            rk[y] = RowKeys{0, 0, 0};
+            if (rr < rows) rk[y] = row_keys(p, u.seq, i);
+            const __nv_bfloat16 *src =
+                q + u.b * p.q.batch + (u.hk * p.G + rr % p.G) * p.q.head + i * p.q.token + 2 * t;
+#pragma unroll
+            for (int x = 0; x < D / 16; x++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const bool in = rr < rows && rk[y].hi > 0 && x * 16 + c * 8 < p.d;
+                    qf[x][y + 2 * c] =
+                        in ? *reinterpret_cast<const uint32_t *>(src + x * 16 + c * 8) : 0u;
+                }
+        }
+        // this lane's row of an 8 x 8 matrix: key r8 (+ 8) of the 16, 16-byte column c
+        const int r8 = lane & 7, mi = lane >> 3;
+        const uint32_t base = smem_u32(sm) + warp * 16 * 128;
+        for (int g = u.g0; g < u.g1; g++) {
+            const int it = g - u.g0, st = it % NS, j0 = u.kt.tile(g) * 64 + warp * 16;
+            if (!wait_warp(full + st, (it / NS) & 1, w)) break;
+            if (u.meets(j0, 16)) {
+                const uint32_t kt = base + st * R::kStage, vt = kt + R::kHalf;
+                const uint32_t bits = good[st] >> (2 * warp);
+                float s[2][4];
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+#pragma unroll
+                    for (int c = 0; c < 4; c++) s[x][c] = 0.f;
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; kk++) {
+                        const int c = kk * 4 + mi;
+                        uint32_t b[4];
+                        ldmatrix4(b, kt + (c >> 3) * R::kPanelBytes + (8 * x + r8) * 128 +
+                                         (((c & 7) ^ r8) << 4));
+                        mma16816(s[x], qf[2 * kk], b[0], b[1]);
+                        mma16816(s[x], qf[2 * kk + 1], b[2], b[3]);
+                    }
+                }
+                // s[x][2 y + c]: row n + 8 y, key j0 + 8 x + 2 t + c
+                float alpha[2];
+                bool moved = false;
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            float &z = s[x][2 * y + c];
+                            const bool see = rk[y].sees(j0 + 8 * x + 2 * t + c) && ((bits >> x) & 1);
+                            z = see ? z * p.scale_log2 : -INFINITY;
+                            mx = fmaxf(mx, z);
+                        }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    mx = fmaxf(mx, m[y]);
+                    const float safe = mx == -INFINITY ? 0.f : mx;
+                    alpha[y] = fast_exp2(m[y] - safe);
+                    moved |= mx > m[y];
+                    m[y] = mx;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            float &z = s[x][2 * y + c];
+                            z = fast_exp2(z - safe);
+                            sum += z;
+                        }
+                    l[y] = l[y] * alpha[y] + sum;
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int x = 0; x < D / 8; x++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) o[x][c] *= alpha[c >> 1];
+                }
+                const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
+                                        pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+                // values that no row sees may be NaN, and 0 * NaN is NaN: they count as 0
+                const bool whole = u.any.sees(j0) && u.any.sees(j0 + 15) &&
+                                   (j0 >= u.any.lo || j0 + 15 < u.any.sink);
+                uint32_t keep[2] = {~0u, ~0u};
+                if (!whole)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int j = j0 + 8 * x + 2 * t;
+                        keep[x] = (u.any.sees(j) ? 0xFFFFu : 0u) |
+                                  (u.any.sees(j + 1) ? 0xFFFF0000u : 0u);
+                    }
+#pragma unroll
+                for (int dd = 0; dd < D / 16; dd++) {
+                    const int c = dd * 2 + (mi >> 1);
+                    uint32_t b[4];
+                    ldmatrix4_trans(b, vt + (c >> 3) * R::kPanelBytes +
+                                           ((mi & 1) * 8 + r8) * 128 + (((c & 7) ^ r8) << 4));
+                    mma16816(o[2 * dd], pf, b[0] & keep[0], b[1] & keep[1]);
+                    mma16816(o[2 * dd + 1], pf, b[2] & keep[0], b[3] & keep[1]);
+                }
+            }
+            mbar_arrive_warp(empty + st);
+        }
+    }
+
+    // the four warps' parts, then the CTA's, in the ring's memory
+    __syncthreads();
+    constexpr int kPitch = Part<D>::kPitch, kFloats = Part<D>::kFloats;
+    float *part = reinterpret_cast<float *>(sm);
+    if (warp < kTokWarps) {
+        float *mine = part + (1 + warp) * kFloats;
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+            const int r = n + 8 * y;
+            if (t == 0) {
+                mine[16 * kPitch + r] = m[y];
+                mine[16 * kPitch + 16 + r] = l[y];
+            }
+#pragma unroll
+            for (int x = 0; x < D / 8; x++)
+                *reinterpret_cast<float2 *>(mine + r * kPitch + x * 8 + 2 * t) =
+                    make_float2(o[x][2 * y], o[x][2 * y + 1]);
+        }
+    }
+    __syncthreads();
+    const int real = min(16, rows - u.rt * 16);
+    for (int at = threadIdx.x; at < real * (D / 4); at += blockDim.x) {
+        const int r = at / (D / 4), c = at % (D / 4) * 4;
+        const float *src = part + kFloats;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kTokWarps; x++) mx = fmaxf(mx, src[x * kFloats + 16 * kPitch + r]);
+        const float safe = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kTokWarps; x++) {
+            const float *s = src + x * kFloats;
+            const float f = exp2f(s[16 * kPitch + r] - safe);
+            const float4 y = *reinterpret_cast<const float4 *>(s + r * kPitch + c);
+            sum = fmaf(f, s[16 * kPitch + 16 + r], sum);
+            acc.x = fmaf(f, y.x, acc.x);
+            acc.y = fmaf(f, y.y, acc.y);
+            acc.z = fmaf(f, y.z, acc.z);
+            acc.w = fmaf(f, y.w, acc.w);
+        }
+        *reinterpret_cast<float4 *>(part + r * kPitch + c) = acc;
+        if (c == 0) part[16 * kPitch + r] = mx, part[16 * kPitch + 16 + r] = sum;
+    }
+    join_cluster<D>(a, u, part, out, lse);
 }
 
 // ---------------------------------------------------------------- float32
@@ -371,9 +483,9 @@ __global__ void __launch_bounds__(kTokThreads)
 token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, float *out,
                  float *lse) {
     constexpr int P = D + 4;
-    __shared__ __align__(16) float sq[16 * D];
-    __shared__ __align__(16) float sk[32 * P];
-    __shared__ __align__(16) float sv[32 * D];
+    __shared__ __align__(16) float buf[16 * D + 32 * P + 32 * D];
+    static_assert(Part<D>::kFloats <= 16 * D + 32 * P + 32 * D, "the part fits the buffer");
+    float *sq = buf, *sk = sq + 16 * D, *sv = sk + 32 * P;
     const WinProblem &p = a.p;
     const TokenUnit u = token_unit<32>(a);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -456,32 +568,26 @@ token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, fl
             }
         }
     }
+    // the CTA's part over the tile buffer (every warp is done with it)
+    __syncthreads();
+    float *part = buf;
+    constexpr int kPitch = Part<D>::kPitch;
 #pragma unroll
     for (int x = 0; x < 4; x++) {
-        const int r = warp + 4 * x, rr = u.rt * 16 + r;
-        if (rr >= rows) continue;
+        const int r = warp + 4 * x;
+        if (u.rt * 16 + r >= rows) continue;
         float sum = l[x];
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        if (a.splits > 1) {
-            float *dst = part_row(a, u, r);
 #pragma unroll
-            for (int c = 0; c < D / 32; c++) dst[c * 32 + lane] = o[x][c];
-            if (lane == 0) dst[D] = m[x], dst[D + 1] = sum;
-        } else {
-            const int i = rr / p.G, h = u.hk * p.G + rr % p.G;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            float *dst = out + u.b * p.o.batch + h * p.o.head + i * p.o.token;
-#pragma unroll
-            for (int c = 0; c < D / 32; c++) dst[c * 32 + lane] = o[x][c] * inv;
-            if (lane == 0) write_lse<float>(p, lse, u.b, h, i, m[x], sum);
-        }
+        for (int c = 0; c < D / 32; c++) part[r * kPitch + c * 32 + lane] = o[x][c];
+        if (lane == 0) part[16 * kPitch + r] = m[x], part[16 * kPitch + 16 + r] = sum;
     }
+    join_cluster<D>(a, u, part, out, lse);
 }
 
-// ---------------------------------------------------------------- join
-// One warp a row (query, head): the parts of its splits in order, so the result does
-// not depend on which CTA came first.
+// ---------------------------------------------------------------- join of clusters
+// One warp a row (query, head).
 template <typename T>
 __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, float *lse) {
     const WinProblem &p = a.p;
@@ -493,15 +599,15 @@ __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, fl
     const int b = (int)(bh / p.Hkv), hk = (int)(bh % p.Hkv);
     const int d2 = p.d + 2;
     const float *part =
-        a.part + ((bh * a.row_tiles + rr / 16) * a.splits * 16 + rr % 16) * (int64_t)d2;
+        a.part + ((bh * a.row_tiles + rr / 16) * a.clusters * 16 + rr % 16) * (int64_t)d2;
     const int64_t step = 16 * (int64_t)d2;
     float mx = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, part[s * step + p.d]);
+    for (int s = lane; s < a.clusters; s += 32) mx = fmaxf(mx, part[s * step + p.d]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float safe = mx == -INFINITY ? 0.f : mx;
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-    for (int s = 0; s < a.splits; s++) {
+    for (int s = 0; s < a.clusters; s++) {
         const float *src = part + s * step;
         const float f = exp2f(src[p.d] - safe);
         sum = fmaf(f, src[p.d + 1], sum);
@@ -515,7 +621,7 @@ __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, fl
 #pragma unroll
     for (int c = 0; c < 4; c++)
         if (c * 32 < p.d) dst[c * 32 + lane] = from_f32<T>(acc[c] * inv);
-    if (lane == 0) write_lse<T>(p, lse, b, h, i, mx, sum);
+    if (lane == 0) write_lse(p, lse, b, h, i, mx, sum);
 }
 
 template <typename T>
@@ -527,9 +633,9 @@ cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
 
 }  // namespace
 
-// Splits: enough CTAs for the 148 SMs several times over (the loads in flight of about
-// eight warps an SM cover the memory's latency), and no part below four groups of keys
-// a warp, where the join would cost more than the split saves.
+// Parts: about three CTAs an SM (two at a time of the bfloat16 kernel's, whose ring holds
+// what the memory's latency needs), none below two tiles of keys.  Up to 8 parts are
+// one cluster; more make clusters of one size each.
 TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
     TokenPlan t;
     t.row_tiles = (p.Nq * p.G + 15) / 16;
@@ -540,42 +646,78 @@ TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
         const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + p.Nq + p.frame;
         most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
     }
-    const int64_t group = dtype == MONARCH_BF16 ? 64 : 32;   // keys of one step of a CTA
-    const int64_t want = (148 * 8 + units - 1) / units;
-    const int64_t room = max((int64_t)1, most / (group * 2));
-    t.splits = (int)max((int64_t)1, min(min(want, room), (int64_t)1024));
-    t.bytes = t.splits > 1 ? (size_t)units * t.splits * 16 * (p.d + 2) * sizeof(float) : 0;
+    const int64_t tile = dtype == MONARCH_BF16 ? 64 : 32;
+    const int64_t want = (148 * 3 + units - 1) / units;
+    const int64_t room = max((int64_t)1, most / (tile * 2));
+    const int64_t parts = max((int64_t)1, min(min(want, room), (int64_t)1024));
+    t.clusters = (int)((parts + kMaxCluster - 1) / kMaxCluster);
+    t.splits = (int)((parts + t.clusters - 1) / t.clusters) * t.clusters;
+    t.bytes = t.clusters > 1 ? (size_t)units * t.clusters * 16 * (p.d + 2) * sizeof(float) : 0;
     return t;
 }
 
+namespace {
+
+// A launch of grid.x / parts clusters of `parts` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_parts(void (*kernel)(Params...), const TokenArgs &a, const dim3 &grid, int threads,
+                         uint32_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.splits / a.clusters;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t launch_f32(const TokenArgs &a, const dim3 &grid, const void *q, const void *k,
+                       const void *v, void *out, float *lse, cudaStream_t stream) {
+    return launch_parts(token_f32_kernel<D>, a, grid, kTokThreads, 0, stream, a, (const float *)q,
+                        (const float *)k, (const float *)v, (float *)out, lse);
+}
+
+template <int D>
+cudaError_t launch_bf16(const TokenArgs &a, const dim3 &grid, const void *q, const void *k,
+                        const void *v, void *out, float *lse, cudaStream_t stream) {
+    const WinProblem &p = a.p;
+    const int page = 1 << p.page_shift, box = p.table ? min(page, 64) : 64;
+    const int tokens = p.table ? page : p.Nk, batches = p.table ? p.num_pages : p.B;
+    CUtensorMap mk, mv;
+    if (!map_tokens(&mk, k, p.k, batches, p.Hkv, tokens, p.d, (uint32_t)box) ||
+        !map_tokens(&mv, v, p.v, batches, p.Hkv, tokens, p.d, (uint32_t)box))
+        return cudaErrorInvalidValue;
+    cudaError_t e = tcs::set_smem(token_bf16_kernel<D>, Ring<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_parts(token_bf16_kernel<D>, a, grid, kTokThreads + 32, Ring<D>::kSmem, stream, mk,
+                        mv, a, box, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, lse);
+}
+
+}  // namespace
+
 cudaError_t token_forward(const WinProblem &p, monarch_dtype dtype, const TokenPlan &plan,
                           const void *q, const void *k, const void *v, void *out, float *lse,
-                          void *workspace, int *status, cudaStream_t stream) {
-    TokenArgs a{p, plan.row_tiles, plan.splits, (float *)workspace, status};
+                          void *workspace, int *status, long long limit, cudaStream_t stream) {
+    const TokenArgs a{p, plan.row_tiles, plan.splits, plan.clusters, (float *)workspace, status, limit};
     const dim3 grid(plan.splits, plan.row_tiles, p.B * p.Hkv);
-    if (dtype == MONARCH_F32) {
-        const float *qf = (const float *)q, *kf = (const float *)k, *vf = (const float *)v;
-        float *of = (float *)out;
-        if (p.d == 32)
-            token_f32_kernel<32><<<grid, kTokThreads, 0, stream>>>(a, qf, kf, vf, of, lse);
-        else if (p.d == 64)
-            token_f32_kernel<64><<<grid, kTokThreads, 0, stream>>>(a, qf, kf, vf, of, lse);
-        else
-            token_f32_kernel<128><<<grid, kTokThreads, 0, stream>>>(a, qf, kf, vf, of, lse);
-        cudaError_t e = cudaGetLastError();
-        return e != cudaSuccess || plan.splits == 1 ? e : join<float>(a, of, lse, stream);
-    }
-    const __nv_bfloat16 *qb = (const __nv_bfloat16 *)q, *kb = (const __nv_bfloat16 *)k;
-    const __nv_bfloat16 *vb = (const __nv_bfloat16 *)v;
-    __nv_bfloat16 *ob = (__nv_bfloat16 *)out;
-    if (p.d == 32)
-        token_bf16_kernel<32><<<grid, kTokThreads, 0, stream>>>(a, qb, kb, vb, ob, lse);
-    else if (p.d == 64)
-        token_bf16_kernel<64><<<grid, kTokThreads, 0, stream>>>(a, qb, kb, vb, ob, lse);
+    cudaError_t e;
+    if (dtype == MONARCH_F32)
+        e = p.d == 32   ? launch_f32<32>(a, grid, q, k, v, out, lse, stream)
+            : p.d == 64 ? launch_f32<64>(a, grid, q, k, v, out, lse, stream)
+                        : launch_f32<128>(a, grid, q, k, v, out, lse, stream);
     else
-        token_bf16_kernel<128><<<grid, kTokThreads, 0, stream>>>(a, qb, kb, vb, ob, lse);
-    cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess || plan.splits == 1 ? e : join<__nv_bfloat16>(a, ob, lse, stream);
+        e = p.d == 128 ? launch_bf16<128>(a, grid, q, k, v, out, lse, stream)
+                       : launch_bf16<64>(a, grid, q, k, v, out, lse, stream);
+    if (e != cudaSuccess || plan.clusters == 1) return e;
+    return dtype == MONARCH_F32 ? join(a, (float *)out, lse, stream)
+                                : join(a, (__nv_bfloat16 *)out, lse, stream);
 }
 
 }  // namespace win

@@ -94,12 +94,15 @@ def _describe(q, k, v, out, window, sinks, frame, lengths, starts, scale, layout
 
 
 def _workspace(need, workspace, device):
+    """(pointer, bytes, the tensor that owns them).  None where the call needs none (256),
+    or where validation failed (0) and the call itself says why."""
+    if need <= 256:
+        return None, 0, None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        # (at least a byte: where validation failed, the call itself says why)
-        return torch.empty(need or 1, dtype=torch.uint8, device=device)
-    if workspace.device != device:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
         raise ValueError("workspace must be on the inputs' device")
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 # The handle of torch's current stream on a device: torch.cuda.current_stream() without
@@ -139,10 +142,11 @@ def window_attention(q, k, v, *, window=(-1, 0), sinks=0, frame=1, lengths=None,
     lse = None
     if return_lse:
         lse = torch.empty((desc.B, desc.H, desc.Nq), dtype=torch.float32, device=q.device)
-    ws = _workspace(_lib.monarch_window_attn_workspace_bytes(desc), workspace, q.device)
+    ws, size, _owner = _workspace(_lib.monarch_window_attn_workspace_bytes(desc), workspace,
+                                  q.device)
     _launch(q.device, _lib.monarch_window_attn_fwd_ws, "monarch_window_attn_fwd_ws", desc,
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size())
+            lse.data_ptr() if return_lse else None, ws, size)
     return (out, lse) if return_lse else out
 
 
@@ -172,11 +176,11 @@ def window_attention_backward(q, k, v, out, lse, dout, *, window=(-1, 0), sinks=
     grads = _lib.WindowGrads()
     for field, t in ((grads.dout, dout), (grads.dq, dq), (grads.dk, dk), (grads.dv, dv)):
         _fill(field, _strides(t, head, token, desc.d))
-    ws = _workspace(_lib.monarch_window_attn_bwd_workspace_bytes(desc), workspace, q.device)
+    need = max(257, _lib.monarch_window_attn_bwd_workspace_bytes(desc))   # always used
+    ws, size, _owner = _workspace(need, workspace, q.device)
     _launch(q.device, _lib.monarch_window_attn_bwd_ws, "monarch_window_attn_bwd_ws", desc, grads,
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
-            ws.numel() * ws.element_size())
+            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, size)
     return dq, dk, dv
 
 
@@ -221,9 +225,10 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, *, window=(-1, 0),
     _fill(desc.k, _strides(k_pages, head, token, d))
     _fill(desc.v, _strides(v_pages, head, token, d))
     lse = torch.empty((B, H, 1), dtype=torch.float32, device=q.device) if return_lse else None
-    ws = _workspace(_lib.monarch_paged_attn_workspace_bytes(desc), workspace, q.device)
+    ws, size, _owner = _workspace(_lib.monarch_paged_attn_workspace_bytes(desc), workspace,
+                                  q.device)
     _launch(q.device, _lib.monarch_paged_attn_ws, "monarch_paged_attn_ws", desc, q.data_ptr(),
             k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
             page_table.stride(0) if B > 1 else width, page, k_pages.shape[0], out.data_ptr(),
-            lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel() * ws.element_size())
+            lse.data_ptr() if return_lse else None, ws, size)
     return (out, lse) if return_lse else out

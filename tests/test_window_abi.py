@@ -62,12 +62,12 @@ def test_window_pointers_and_workspace():
         assert fwd(d, *x) == INVALID
         x[i] = P + 8
         assert fwd(d, *x) == ALIGN
-    assert fwd(d, ws=None) == INVALID and fwd(d, ws=P + 16) == ALIGN
     assert fwd(d, lse=P + 2) == ALIGN and fwd(desc(lengths=P + 1)) == ALIGN
-    assert fwd(d, n=255) == NO_MEMORY
+    assert _lib.monarch_window_attn_workspace_bytes(d) == 256   # none needed
     token = desc(Nq=1, Nk=100000, left=-1)
     need = _lib.monarch_window_attn_workspace_bytes(token)
     assert need > 256 and fwd(token, n=need - 1) == NO_MEMORY
+    assert fwd(token, ws=None) == INVALID and fwd(token, ws=P + 16) == ALIGN
     assert fwd(None) == INVALID
     g = _lib.WindowGrads()
     back = lambda *x: _lib.monarch_window_attn_bwd_ws(d, *x, 1 << 40, None)   # noqa: E731
