@@ -10,22 +10,26 @@
 //   tc_window_dkv_kernel  128 keys of one key head against the 128-query tiles of
 //                         every head of its group that see them;
 //   tc_window_dq_kernel   128 queries of one head against their 128-key tiles.
-// 384 threads a CTA, one CTA an SM: warps 0-7 the elementwise work (two warps a group
-// of 32 tensor-memory lanes, each half of the 128 columns), warp 8 loads (TMA), warp 9
-// issues the products, warp 10 stages lse and delta.
+// 384 threads a CTA, one CTA an SM: warps 0-7 the elementwise work, warp 8 loads
+// (TMA), warp 9 issues the products, warp 10 stages lse and delta.
 //
-// Order of the products (dkv), chosen so that the tensor pipe always has one that
-// does not wait for the elementwise work on the previous one:
-//   S(0) dP(0)  |  dV(i) S(i+1) dK(i) dP(i+1)  |  ...
-// While the warps form P(i + 1) the pipe runs dK(i) and dP(i + 1), while they form
-// dS(i) it runs dV(i) and S(i + 1).  P overwrites S and dS overwrites dP in tensor
-// memory, each half of the columns in its own place, so no warp waits for another
-// before it writes; a later product into the same columns follows in issue order.
-// In the dq kernel S has two buffers: dP(j+1) dQ(j) S(j+2) after dS(j).
+// The streamed side goes in blocks of 64 rows (queries in dkv, keys in dq).  Blocks u
+// with u % 2 = h belong to warps 4 h .. 4 h + 3 (thread = tensor-memory lane = row of the
+// fixed tile) and to half h of the tensor-memory columns, so the two groups work on
+// different blocks at different times and the tensor pipe has the products of one
+// while the other computes.  Order of the products (fixed, so the sums are too):
+//   dkv:  dV(u) S(u+2) after P(u);  dK(u) dP(u+2) after dS(u)
+//   dq:   dP(u+2) dQ(u) S(u+3) after dS(u)   (S has four buffers)
+// P overwrites S and dS overwrites dP (S in dq) in tensor memory; a later product into
+// the same columns follows in issue order.
+// The blocks go through two rings of their own, as many as shared memory holds.  A
+// block is needed about a block's work after its predecessor, and a load takes about as
+// long as a block (16 KB a tensor): with two stages of 128 rows the tensor pipe
+// waited for loads and a 128 x 128 tile took 5100 clocks in dkv and 3460 in dq.
 //
 // delta comes from out as the forward rounded it, an error of 2^-8 |dO.O| at most.  A
 // row of n keys of like weight has |O| of about n^(-1/2) |v|, so against dP it matters
-// for few keys only.  Query tiles of up to kExactTiles key tiles therefore first walk
+// for few keys only.  Query tiles of up to kExactBlocks key blocks therefore first walk
 // their keys once for delta = sum P dP from the same products that form dS, and the dq
 // kernel runs first to hand it to the dk/dv kernel.  (Two padded causal
 // sequences of 1023 and 681 tokens, d = 64: dq is 2.6e-3 from 64 bits without it.)
@@ -39,16 +43,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 384;
-constexpr int kExactTiles = 3;
+constexpr int kExactBlocks = 6;
 
-// Shared memory: two fixed tiles of 128 rows, two stages of two streamed ones.
+// Shared memory: two fixed tiles of 128 rows, two rings of 64-row blocks, and per slot of
+// the first ring -lse and -delta of its 64 queries (dkv).
 template <int D> struct BwdLayout {
     static constexpr uint32_t kTile = (D / 64) * kPanel;
+    static constexpr uint32_t kBlock = kTile / 2;             // panels of 64 rows
+    static constexpr uint32_t kBlockPanel = 64 * 128;
+    static constexpr int kBlocks = 10;
     static constexpr uint32_t kFix = 0;                       // K, V (dkv) or Q, dO (dq)
-    static constexpr uint32_t kRing = 2 * kTile;              // stage s: 2 tiles
-    static constexpr uint32_t kStats = kRing + 4 * kTile;     // [stage][-lse | -delta][128] floats
-    static constexpr uint32_t kBar = kStats + 2 * 2 * 512;
-    static constexpr uint32_t kSmem = kBar + 256 + 1024;      // + slack to align the base
+    static constexpr uint32_t kRing = 2 * kTile;
+    static constexpr uint32_t kStats = kRing + kBlocks * kBlock;
+    static constexpr uint32_t kBar = kStats + 5 * 512;
+    static constexpr uint32_t kSmem = kBar + 512;   // the base is 1024-aligned (checked)
     static_assert(kSmem <= (uint32_t)kMaxSmem, "window backward shared memory");
 };
 
@@ -116,60 +124,109 @@ __device__ __forceinline__ void probabilities(float (&x)[64], float c, const flo
     }
 }
 
-// Everything one CTA's roles share.
-struct Bars {
-    uint64_t *fix_full;      // the fixed tiles
-    uint64_t *first_full;    // [2 stages]: Q (dkv) or K (dq)
-    uint64_t *second_full;   // [2 stages]: dO or V
-    uint64_t *stage_empty;   // [2 stages]: the products have read the stage
-    uint64_t *stats_full;    // [2 stages] (dkv)
-    uint64_t *s_full;        // [2] S in tensor memory (dkv uses the first)
-    uint64_t *dp_full;
-    uint64_t *p_full;        // 8 warps (dkv; in dq the halves of delta, once)
-    uint64_t *ds_full;       // 8 warps
-    uint64_t *acc_full;      // the last products
-    uint64_t *stall_bar;
-    uint32_t *tmem_slot;
-    volatile int *abort_flag;
+// Barriers of one CTA.  N1, N2: blocks of the two rings; NS: S buffers.
+template <int N1, int N2, int NS> struct Bars {
+    uint64_t fix_full;                  // the fixed tiles
+    uint64_t full1[N1], empty1[N1];     // Q (dkv) or K (dq)
+    uint64_t full2[N2], empty2[N2];     // dO or V
+    uint64_t stats_full[N1];            // dkv
+    uint64_t s_full[NS];                // S in tensor memory
+    uint64_t dp_full[2];
+    uint64_t p_full[2], ds_full[2];     // one arrival a warp of the half
+    uint64_t delta_bar;                 // the halves' parts of delta (dq), once
+    uint64_t acc_full;                  // the last products
+    uint64_t stall_bar;                 // never completed (fault injection)
+    uint32_t tmem_slot;
+    int abort_flag;
+
+    __device__ __forceinline__ void init() {
+        mbar_init(&fix_full, 1);
+        for (int i = 0; i < N1; i++) {
+            mbar_init(full1 + i, 1);
+            mbar_init(empty1 + i, 1);
+            mbar_init(stats_full + i, 1);
+        }
+        for (int i = 0; i < N2; i++) {
+            mbar_init(full2 + i, 1);
+            mbar_init(empty2 + i, 1);
+        }
+        for (int i = 0; i < NS; i++) mbar_init(s_full + i, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(dp_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(ds_full + i, 4);
+        }
+        mbar_init(&delta_bar, 8);
+        mbar_init(&acc_full, 1);
+        mbar_init(&stall_bar, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    // Every issued copy lands before the CTA may exit (an aborted CTA may not have
+    // waited for the last ones).
+    __device__ __forceinline__ void drain(int issued1, int issued2) {
+        wait_phase_cleanup(&fix_full, 0, kCleanupPolls);
+        for (int u = max(0, issued1 - N1); u < issued1; u++)
+            wait_phase_cleanup(full1 + u % N1, (u / N1) & 1, kCleanupPolls);
+        for (int u = max(0, issued2 - N2); u < issued2; u++)
+            wait_phase_cleanup(full2 + u % N2, (u / N2) & 1, kCleanupPolls);
+    }
 };
 
-__device__ __forceinline__ Bars make_bars(uint8_t *at) {
-    uint64_t *b = reinterpret_cast<uint64_t *>(at);
-    return {b, b + 1, b + 3, b + 5, b + 7, b + 9, b + 11, b + 12, b + 13, b + 14, b + 15,
-            reinterpret_cast<uint32_t *>(b + 16), reinterpret_cast<volatile int *>(b + 17)};
-}
-__device__ __forceinline__ void init_bars(const Bars &b) {
-    for (int i = 0; i < 2; i++) {
-        mbar_init(b.first_full + i, 1);
-        mbar_init(b.second_full + i, 1);
-        mbar_init(b.stage_empty + i, 1);
-        mbar_init(b.stats_full + i, 1);
-        mbar_init(b.s_full + i, 1);
+// One CTA's loads: the fixed tiles, then the blocks of both rings in the order in which
+// the products need them.  coords(u, h, row): head and first row of block u.
+template <int D, typename B, int N1, int N2, typename Coords>
+__device__ __forceinline__ void load_all(uint8_t *sm, B *bar, const CUtensorMap *fix_a,
+                                         const CUtensorMap *fix_b, int fix_row, int fix_head,
+                                         const CUtensorMap *ring1, const CUtensorMap *ring2, int b,
+                                         int n, const Coords &coords, const WaitCtx &w, int lane) {
+    using L = BwdLayout<D>;
+    constexpr int PN = D / 64;
+    if (lane == 0) {
+        mbar_expect_tx(&bar->fix_full, 2 * L::kTile);
+        for (int pn = 0; pn < PN; pn++) {
+            tma_load_4d(sm + L::kFix + pn * kPanel, fix_a, pn * 64, fix_row, fix_head, b,
+                        &bar->fix_full);
+            tma_load_4d(sm + L::kFix + L::kTile + pn * kPanel, fix_b, pn * 64, fix_row, fix_head, b,
+                        &bar->fix_full);
+        }
     }
-    mbar_init(b.fix_full, 1);
-    mbar_init(b.dp_full, 1);
-    mbar_init(b.p_full, 8);
-    mbar_init(b.ds_full, 8);
-    mbar_init(b.acc_full, 1);
-    mbar_init(b.stall_bar, 1);
-    *b.abort_flag = 0;
-    fence_mbar_init();
+    int issued1 = 0, issued2 = 0;
+    for (int u = 0; u < n; u++) {
+        int h, row;
+        coords(u, h, row);
+        const int s1 = u % N1, s2 = u % N2;
+        if (u >= N1 && !wait_warp(bar->empty1 + s1, (u / N1 - 1) & 1, w)) break;
+        if (lane == 0) {
+            uint8_t *dst = sm + L::kRing + s1 * L::kBlock;
+            mbar_expect_tx(bar->full1 + s1, L::kBlock);
+            for (int pn = 0; pn < PN; pn++)
+                tma_load_4d(dst + pn * L::kBlockPanel, ring1, pn * 64, row, h, b, bar->full1 + s1);
+        }
+        issued1++;
+        if (u >= N2 && !wait_warp(bar->empty2 + s2, (u / N2 - 1) & 1, w)) break;
+        if (lane == 0) {
+            uint8_t *dst = sm + L::kRing + (N1 + s2) * L::kBlock;
+            mbar_expect_tx(bar->full2 + s2, L::kBlock);
+            for (int pn = 0; pn < PN; pn++)
+                tma_load_4d(dst + pn * L::kBlockPanel, ring2, pn * 64, row, h, b, bar->full2 + s2);
+        }
+        issued2++;
+    }
+    if (lane == 0) bar->drain(issued1, issued2);
 }
 
-// Every issued copy lands before the CTA may exit (an aborted CTA may not have
-// waited for the last ones).
-__device__ __forceinline__ void drain_loads(const Bars &b, const int (&issued)[2]) {
-    wait_phase_cleanup(b.fix_full, 0, kCleanupPolls);
-    for (int s = 0; s < 2; s++)
-        if (issued[s] > 0) {
-            wait_phase_cleanup(b.first_full + s, (issued[s] - 1) & 1, kCleanupPolls);
-            wait_phase_cleanup(b.second_full + s, (issued[s] - 1) & 1, kCleanupPolls);
-        }
+// The SW128 tiles need a 1024-byte aligned base; the layout leaves no room to align by
+// hand, so a misaligned base is reported, not worked around.
+__device__ __forceinline__ bool base_aligned(const uint8_t *sm, int *status) {
+    if ((smem_u32(sm) & 1023u) == 0) return true;
+    if (threadIdx.x == 0) record_status(status, MONARCH_ERR_CUDA);
+    return false;
 }
 
 // ---------------------------------------------------------------- dk, dv
-// Tensor memory: S^T at 0, dP^T at 128, dV at 256, dK at 384.  P^T of the half h of
-// the queries lies at 64 h, dS^T at 128 + 64 h (32 columns each).
+// Tensor memory, half h: S^T at 64 h (P^T over its first 32 columns), dP^T at 128 + 64 h
+// (dS^T over it); dV at 256, dK at 384.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -177,12 +234,15 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDo, BwdArgs a) {
     using L = BwdLayout<D>;
-    constexpr int PN = D / 64;
-    constexpr uint32_t kTile = L::kTile;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = align1024(smem_raw);
-    const Bars bar = make_bars(sm + L::kBar);
-    float *stats = reinterpret_cast<float *>(sm + L::kStats);   // [stage][2][128]
+    constexpr int PN = D / 64, N1 = 5, N2 = 5;
+    static_assert(N1 + N2 == L::kBlocks, "ring slots");
+    using B = Bars<N1, N2, 2>;
+    static_assert(sizeof(B) <= 512, "barriers");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = smem_raw;
+    if (!base_aligned(sm, a.status)) return;
+    B *bar = reinterpret_cast<B *>(sm + L::kBar);
+    float *stats = reinterpret_cast<float *>(sm + L::kStats);   // [slot][-lse | -delta][64]
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (the first key tiles first: they are seen by the most queries under a causal mask)
@@ -191,8 +251,8 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
     const Sequence seq = sequence(p, b);
     int first, last;
     query_rows(p, seq, j0, j0 + 128, first, last);
-    const int t0 = first / 128, nt = last > first ? (last + 127) / 128 - t0 : 0;
-    const int n = nt * p.G;   // query tiles over the group's heads
+    const int t0 = first / 64, nt = last > first ? (last + 63) / 64 - t0 : 0;
+    const int n = nt * p.G;   // query blocks over the group's heads
 
     if (n == 0) {             // no query sees these keys (the same for the whole CTA)
         const int j = j0 + threadIdx.x;
@@ -202,118 +262,95 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         return;
     }
-    if (threadIdx.x == 0) init_bars(bar);
-    if (warp == 9) tmem_alloc(bar.tmem_slot, 512);
+    if (threadIdx.x == 0) bar->init();
+    if (warp == 9) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *bar.tmem_slot;
-    const WaitCtx w{a.limit, a.status, bar.abort_flag};
+    const uint32_t tmem = bar->tmem_slot;
+    const WaitCtx w{a.limit, a.status, &bar->abort_flag};
+    auto coords = [&](int u, int &h, int &row) {
+        h = hk * p.G + u / nt;
+        row = (t0 + u % nt) * 64;
+    };
 
     if (warp == 8) {
-        // ---------------- loads
-        int issued[2] = {0, 0};
-        if (lane == 0) {
-            mbar_expect_tx(bar.fix_full, 2 * kTile);
-            for (int pn = 0; pn < PN; pn++) {
-                tma_load_4d(sm + L::kFix + pn * kPanel, &tmK, pn * 64, j0, hk, b, bar.fix_full);
-                tma_load_4d(sm + L::kFix + kTile + pn * kPanel, &tmV, pn * 64, j0, hk, b,
-                            bar.fix_full);
-            }
-        }
-        for (int i = 0; i < n; i++) {
-            const int st = i & 1;
-            if (i >= 2 && !wait_warp(bar.stage_empty + st, ((i >> 1) - 1) & 1, w)) break;
-            if (lane == 0) {
-                const int h = hk * p.G + i / nt, i0 = (t0 + i % nt) * 128;
-                uint8_t *dst = sm + L::kRing + st * 2 * kTile;
-                mbar_expect_tx(bar.first_full + st, kTile);
-                for (int pn = 0; pn < PN; pn++)
-                    tma_load_4d(dst + pn * kPanel, &tmQ, pn * 64, i0, h, b, bar.first_full + st);
-                mbar_expect_tx(bar.second_full + st, kTile);
-                for (int pn = 0; pn < PN; pn++)
-                    tma_load_4d(dst + kTile + pn * kPanel, &tmDo, pn * 64, i0, h, b,
-                                bar.second_full + st);
-            }
-            issued[st]++;
-        }
-        if (lane == 0) drain_loads(bar, issued);
+        load_all<D, B, N1, N2>(sm, bar, &tmK, &tmV, j0, hk, &tmQ, &tmDo, b, n, coords, w, lane);
     } else if (warp == 9) {
+        if (elect_one()) {
         // ---------------- products
-        constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kStageDesc = 2 * kTile >> 4, kHalfDesc = 64 * 128 >> 4;
+        constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
+        constexpr uint32_t kBlockDesc = L::kBlock >> 4;
+        const uint32_t ring = smem_u32(sm + L::kRing);
         const uint64_t dK = smem_desc_sw128(smem_u32(sm + L::kFix), 16, 1024);
-        const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kFix + kTile), 16, 1024);
-        const uint64_t dQ = smem_desc_sw128(smem_u32(sm + L::kRing), 16, 1024);
-        const uint64_t dO = smem_desc_sw128(smem_u32(sm + L::kRing + kTile), 16, 1024);
-        const uint64_t dQt = smem_desc_sw128(smem_u32(sm + L::kRing), kPanel, 1024);
-        const uint64_t dOt = smem_desc_sw128(smem_u32(sm + L::kRing + kTile), kPanel, 1024);
-        auto issue_s = [&](int i) -> bool {
-            const int st = i & 1;
-            if (!spin_warp(bar.first_full + st, (i >> 1) & 1, w)) return false;
+        const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kFix + L::kTile), 16, 1024);
+        const uint64_t dQ = smem_desc_sw128(ring, 16, 1024);
+        const uint64_t dO = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
+        const uint64_t dQt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
+        const uint64_t dOt = smem_desc_sw128(ring + N1 * L::kBlock, L::kBlockPanel, 1024);
+        auto issue_s = [&](int u) -> bool {
+            if (!spin_phase(bar->full1 + u % N1, (u / N1) & 1, w)) return false;
             tc_fence_after();
-            mma_ss_head<D>(tmem, dK, dQ + st * kStageDesc, idS);
-            mma_commit_warp(bar.s_full);
+            mma_head<D, 64>(tmem + 64 * (u & 1), dK, dQ + u % N1 * kBlockDesc, idS);
+            mma_commit(bar->s_full + (u & 1));
             return true;
         };
-        auto issue_dp = [&](int i) -> bool {
-            const int st = i & 1;
-            if (!spin_warp(bar.second_full + st, (i >> 1) & 1, w)) return false;
+        auto issue_dp = [&](int u) -> bool {
+            if (!spin_phase(bar->full2 + u % N2, (u / N2) & 1, w)) return false;
             tc_fence_after();
-            mma_ss_head<D>(tmem + 128, dV, dO + st * kStageDesc, idS);
-            mma_commit_warp(bar.dp_full);
+            mma_head<D, 64>(tmem + 128 + 64 * (u & 1), dV, dO + u % N2 * kBlockDesc, idS);
+            mma_commit(bar->dp_full + (u & 1));
             return true;
         };
-        bool ok = (!a.stall || spin_warp(bar.stall_bar, 0, w)) && spin_warp(bar.fix_full, 0, w);
-        ok = ok && issue_s(0) && issue_dp(0);
-        for (int i = 0; ok && i < n; i++) {
-            const int st = i & 1;
-            if (!(ok = spin_warp(bar.p_full, i & 1, w))) break;
+        bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
+        for (int u = 0; ok && u < 2 && u < n; u++) ok = issue_s(u) && issue_dp(u);
+        for (int u = 0; ok && u < n; u++) {
+            const int h = u & 1, ph = (u >> 1) & 1;
+            if (!(ok = spin_phase(bar->p_full + h, ph, w))) break;
             tc_fence_after();
-            for (int h = 0; h < 2; h++)
-                mma4_ts_mn64(tmem + 256, tmem + 64 * h, dOt + st * kStageDesc + h * kHalfDesc, idO,
-                             i > 0 || h > 0 ? 1u : 0u);
-            if (i + 1 < n && !(ok = issue_s(i + 1))) break;
-            if (!(ok = spin_warp(bar.ds_full, i & 1, w))) break;
+            mma_block64(tmem + 256, tmem + 64 * h, dOt + u % N2 * kBlockDesc, idO, u > 0 ? 1u : 0u);
+            mma_commit(bar->empty2 + u % N2);
+            if (u + 2 < n && !(ok = issue_s(u + 2))) break;
+            if (!(ok = spin_phase(bar->ds_full + h, ph, w))) break;
             tc_fence_after();
-            for (int h = 0; h < 2; h++)
-                mma4_ts_mn64(tmem + 384, tmem + 128 + 64 * h,
-                             dQt + st * kStageDesc + h * kHalfDesc, idO, i > 0 || h > 0 ? 1u : 0u);
-            mma_commit_warp(bar.stage_empty + st);
-            if (i + 1 < n) ok = issue_dp(i + 1);
+            mma_block64(tmem + 384, tmem + 128 + 64 * h, dQt + u % N1 * kBlockDesc, idO,
+                         u > 0 ? 1u : 0u);
+            mma_commit(bar->empty1 + u % N1);
+            if (u + 2 < n) ok = issue_dp(u + 2);
         }
-        mma_commit_warp(bar.acc_full);
-        wait_phase_cleanup(bar.acc_full, 0, kCleanupPolls);
+        mma_commit(&bar->acc_full);
+        wait_phase_cleanup(&bar->acc_full, 0, kCleanupPolls);
+        }
+        __syncwarp();
     } else if (warp == 10) {
-        // ---------------- lse (in log2 units) and delta of each tile's queries, negated
-        for (int i = 0; i < n; i++) {
-            const int st = i & 1;
-            if (i >= 2 && !wait_warp(bar.stage_empty + st, ((i >> 1) - 1) & 1, w)) break;
-            const int h = hk * p.G + i / nt, i0 = (t0 + i % nt) * 128;
+        // ---------------- lse (in log2 units) and delta of each block's queries, negated
+        for (int u = 0; u < n; u++) {
+            if (u >= N1 && !wait_warp(bar->empty1 + u % N1, (u / N1 - 1) & 1, w)) break;
+            int h, i0;
+            coords(u, h, i0);
             const int64_t row = ((int64_t)b * p.H + h) * p.Nq;
-            float *dst = stats + st * 256;
+            float *dst = stats + u % N1 * 128;
 #pragma unroll
-            for (int x = lane; x < 128; x += 32) {
+            for (int x = lane; x < 64; x += 32) {
                 const bool in = i0 + x < p.Nq;
                 dst[x] = in ? -a.lse[row + i0 + x] * kLog2e : 0.f;
-                dst[128 + x] = in ? -a.delta[row + i0 + x] : 0.f;
+                dst[64 + x] = in ? -a.delta[row + i0 + x] : 0.f;
             }
-            mbar_arrive_warp(bar.stats_full + st);
+            mbar_arrive_warp(bar->stats_full + u % N1);
         }
     } else if (warp < 8) {
-        // ---------------- elementwise: key row j, queries of one half of the tile
+        // ---------------- elementwise: key row j, the queries of the half's blocks
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, j = j0 + row;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
         int ilo, ihi, rfirst, rlast;
         query_rows(p, seq, j, j + 1, ilo, ihi);   // the queries that see this key
         real_rows(p, seq, 0, p.Nq, rfirst, rlast);
         bool ok = true;
-        for (int i = 0; i < n; i++) {
-            const int st = i & 1, i0 = (t0 + i % nt) * 128, c0 = i0 + 64 * half;
-            const float *nl = stats + st * 256 + 64 * half, *nd = nl + 128;
-            if (!(ok = wait_warp(bar.s_full, i & 1, w) &&
-                       wait_warp(bar.stats_full + st, (i >> 1) & 1, w)))
+        for (int u = half; u < n; u += 2) {
+            const int ph = (u >> 1) & 1, s1 = u % N1, s2 = u % N2, c0 = (t0 + u % nt) * 64;
+            const float *nl = stats + s1 * 128, *nd = nl + 64;
+            if (!(ok = wait_warp(bar->s_full + half, ph, w) &&
+                       wait_warp(bar->stats_full + s1, (u / N1) & 1, w)))
                 break;
             tc_fence_after();
             float x[64];
@@ -327,24 +364,22 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
             for (int k = 0; k < 32; k++) pk[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
             tmem_st32(tl, pk);
-            const int rl = min(rlast, p.Nq), rf = rfirst;
-            if (i0 < rf || (rl < p.Nq && i0 + 128 > rl)) {
+            if (c0 < rfirst || (rlast < p.Nq && c0 + 64 > rlast)) {
                 // rows that are not real may hold anything, and 0 * NaN is NaN: they become
                 // zeros before the products over the queries
-                if (!(ok = wait_warp(bar.second_full + st, (i >> 1) & 1, w))) break;
-                uint8_t *tile = sm + L::kRing + st * 2 * kTile;
-                const int za = min(max(rf - i0, 0), 128), zb = min(max(rl - i0, 0), 128);
-                const int id = half * 128 + row;
-                zero_rows(tile, 0, za, PN, kPanel, id, 256);
-                zero_rows(tile, zb, 128, PN, kPanel, id, 256);
-                zero_rows(tile + kTile, 0, za, PN, kPanel, id, 256);
-                zero_rows(tile + kTile, zb, 128, PN, kPanel, id, 256);
+                if (!(ok = wait_warp(bar->full2 + s2, (u / N2) & 1, w))) break;
+                const int za = min(max(rfirst - c0, 0), 64), zb = min(max(rlast - c0, 0), 64);
+                for (int x2 = 0; x2 < 2; x2++) {
+                    uint8_t *blk = sm + L::kRing + (x2 ? N1 + s2 : s1) * L::kBlock;
+                    zero_rows(blk, 0, za, PN, L::kBlockPanel, row, 128);
+                    zero_rows(blk, zb, 64, PN, L::kBlockPanel, row, 128);
+                }
                 fence_proxy_async_smem();
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive_warp(bar.p_full);
-            if (!(ok = wait_warp(bar.dp_full, i & 1, w))) break;
+            mbar_arrive_warp(bar->p_full + half);
+            if (!(ok = wait_warp(bar->dp_full + half, ph, w))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
@@ -354,12 +389,12 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(nd + c + k);
-                    const uint64_t u = f2_mul(f2_add(f2_pack(y[k], y[k + 1]), d2.x),
+                    const uint64_t e = f2_mul(f2_add(f2_pack(y[k], y[k + 1]), d2.x),
                                               f2_pack(x[c + k], x[c + k + 1]));
-                    const uint64_t v = f2_mul(f2_add(f2_pack(y[k + 2], y[k + 3]), d2.y),
+                    const uint64_t f = f2_mul(f2_add(f2_pack(y[k + 2], y[k + 3]), d2.y),
                                               f2_pack(x[c + k + 2], x[c + k + 3]));
-                    f2_unpack(u, y[k], y[k + 1]);
-                    f2_unpack(v, y[k + 2], y[k + 3]);
+                    f2_unpack(e, y[k], y[k + 1]);
+                    f2_unpack(f, y[k + 2], y[k + 3]);
                 }
                 if (!all) {
                     const uint32_t s = (uint32_t)(see >> c);
@@ -372,9 +407,9 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             tmem_st32(tl + 128, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive_warp(bar.ds_full);
+            mbar_arrive_warp(bar->ds_full + half);
         }
-        if (ok && wait_warp(bar.acc_full, 0, w)) {
+        if (ok && wait_warp(&bar->acc_full, 0, w)) {
             tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (D / 2);
             const int64_t x = half * (D / 2);
@@ -396,8 +431,8 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
 }
 
 // ---------------------------------------------------------------- dq
-// Tensor memory: S at 0 and 128 (two buffers; dS over S, half h at + 64 h), dP at 256,
-// dQ at 384.
+// Tensor memory: S of block u at 64 (u % 4) (dS over its first 32 columns), dP of half h
+// at 256 + 64 h, dQ at 384.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -405,11 +440,15 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmDo, BwdArgs a) {
     using L = BwdLayout<D>;
-    constexpr int PN = D / 64;
-    constexpr uint32_t kTile = L::kTile;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = align1024(smem_raw);
-    const Bars bar = make_bars(sm + L::kBar);
+    // a key block stays from S(u) to dQ(u), three blocks; a value block for dP(u) alone
+    constexpr int PN = D / 64, N1 = 6, N2 = 4;
+    static_assert(N1 + N2 == L::kBlocks, "ring slots");
+    using B = Bars<N1, N2, 4>;
+    static_assert(sizeof(B) <= 512, "barriers");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = smem_raw;
+    if (!base_aligned(sm, a.status)) return;
+    B *bar = reinterpret_cast<B *>(sm + L::kBar);
     float *half_delta = reinterpret_cast<float *>(sm + L::kStats);   // [2 halves][128]
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -417,10 +456,10 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int unit = blockIdx.x % (p.B * p.H), h = unit % p.H, b = unit / p.H;
     const int i0 = ((int)gridDim.x - 1 - (int)blockIdx.x) / (p.B * p.H) * 128;
     const Sequence seq = sequence(p, b);
-    const KeyTiles kt = key_tiles<128>(p, seq, i0, i0 + 128);
+    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + 128);
     const int nt = kt.count();
-    // the first n - nt steps only sum delta
-    const int n = nt <= kExactTiles ? 2 * nt : nt;
+    // the first n - nt blocks only sum delta
+    const int n = nt <= kExactBlocks ? 2 * nt : nt;
     __nv_bfloat16 *const dq = a.dq + b * a.g.dq.batch + h * a.g.dq.head;
 
     if (n == 0) {
@@ -428,102 +467,92 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (threadIdx.x < 128 && i < p.Nq) zero_row(dq + (int64_t)i * a.g.dq.token, p.d);
         return;
     }
-    if (threadIdx.x == 0) init_bars(bar);
-    if (warp == 9) tmem_alloc(bar.tmem_slot, 512);
+    if (threadIdx.x == 0) bar->init();
+    if (warp == 9) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *bar.tmem_slot;
-    const WaitCtx w{a.limit, a.status, bar.abort_flag};
+    const uint32_t tmem = bar->tmem_slot;
+    const WaitCtx w{a.limit, a.status, &bar->abort_flag};
 
     if (warp == 8) {
-        int issued[2] = {0, 0};
-        if (lane == 0) {
-            mbar_expect_tx(bar.fix_full, 2 * kTile);
-            for (int pn = 0; pn < PN; pn++) {
-                tma_load_4d(sm + L::kFix + pn * kPanel, &tmQ, pn * 64, i0, h, b, bar.fix_full);
-                tma_load_4d(sm + L::kFix + kTile + pn * kPanel, &tmDo, pn * 64, i0, h, b,
-                            bar.fix_full);
-            }
-        }
-        for (int i = 0; i < n; i++) {
-            const int st = i & 1;
-            if (i >= 2 && !wait_warp(bar.stage_empty + st, ((i >> 1) - 1) & 1, w)) break;
-            if (lane == 0) {
-                const int j0 = kt.tile(i % nt) * 128;
-                uint8_t *dst = sm + L::kRing + st * 2 * kTile;
-                mbar_expect_tx(bar.first_full + st, kTile);
-                for (int pn = 0; pn < PN; pn++)
-                    tma_load_4d(dst + pn * kPanel, &tmK, pn * 64, j0, h / p.G, b,
-                                bar.first_full + st);
-                mbar_expect_tx(bar.second_full + st, kTile);
-                for (int pn = 0; pn < PN; pn++)
-                    tma_load_4d(dst + kTile + pn * kPanel, &tmV, pn * 64, j0, h / p.G, b,
-                                bar.second_full + st);
-            }
-            issued[st]++;
-        }
-        if (lane == 0) drain_loads(bar, issued);
+        auto coords = [&](int u, int &head, int &row) {
+            head = h / p.G;
+            row = kt.tile(u % nt) * 64;
+        };
+        load_all<D, B, N1, N2>(sm, bar, &tmQ, &tmDo, i0, h, &tmK, &tmV, b, n, coords, w, lane);
     } else if (warp == 9) {
-        constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kStageDesc = 2 * kTile >> 4, kHalfDesc = 64 * 128 >> 4;
+        if (elect_one()) {
+        constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
+        constexpr uint32_t kBlockDesc = L::kBlock >> 4;
+        const uint32_t ring = smem_u32(sm + L::kRing);
         const uint64_t dQ = smem_desc_sw128(smem_u32(sm + L::kFix), 16, 1024);
-        const uint64_t dO = smem_desc_sw128(smem_u32(sm + L::kFix + kTile), 16, 1024);
-        const uint64_t dK = smem_desc_sw128(smem_u32(sm + L::kRing), 16, 1024);
-        const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kRing + kTile), 16, 1024);
-        const uint64_t dKt = smem_desc_sw128(smem_u32(sm + L::kRing), kPanel, 1024);
-        auto issue_s = [&](int i) -> bool {
-            const int st = i & 1;
-            if (!spin_warp(bar.first_full + st, (i >> 1) & 1, w)) return false;
+        const uint64_t dO = smem_desc_sw128(smem_u32(sm + L::kFix + L::kTile), 16, 1024);
+        const uint64_t dK = smem_desc_sw128(ring, 16, 1024);
+        const uint64_t dV = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
+        const uint64_t dKt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
+        auto issue_s = [&](int u) -> bool {
+            if (!spin_phase(bar->full1 + u % N1, (u / N1) & 1, w)) return false;
             tc_fence_after();
-            mma_ss_head<D>(tmem + 128 * st, dQ, dK + st * kStageDesc, idS);
-            mma_commit_warp(bar.s_full + st);
+            mma_head<D, 64>(tmem + 64 * (u & 3), dQ, dK + u % N1 * kBlockDesc, idS);
+            mma_commit(bar->s_full + (u & 3));
             return true;
         };
-        auto issue_dp = [&](int i) -> bool {
-            const int st = i & 1;
-            if (!spin_warp(bar.second_full + st, (i >> 1) & 1, w)) return false;
+        auto issue_dp = [&](int u) -> bool {
+            if (!spin_phase(bar->full2 + u % N2, (u / N2) & 1, w)) return false;
             tc_fence_after();
-            mma_ss_head<D>(tmem + 256, dO, dV + st * kStageDesc, idS);
-            mma_commit_warp(bar.dp_full);
+            mma_head<D, 64>(tmem + 256 + 64 * (u & 1), dO, dV + u % N2 * kBlockDesc, idS);
+            mma_commit(bar->dp_full + (u & 1));
+            mma_commit(bar->empty2 + u % N2);
             return true;
         };
-        bool ok = (!a.stall || spin_warp(bar.stall_bar, 0, w)) && spin_warp(bar.fix_full, 0, w);
-        ok = ok && issue_s(0) && issue_dp(0);
-        if (ok && n > 1) ok = issue_s(1);
-        for (int i = 0; ok && i < n; i++) {
-            const int st = i & 1;
-            // dS(i) is written: dP's columns have been read too
-            if (!(ok = spin_warp(bar.ds_full, i & 1, w))) break;
-            if (i + 1 < n && !(ok = issue_dp(i + 1))) break;
+        bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
+        for (int u = 0; ok && u < 2 && u < n; u++) ok = issue_s(u) && issue_dp(u);
+        if (ok && n > 2) ok = issue_s(2);
+        for (int u = 0; ok && u < n; u++) {
+            // dS(u) is written: the half's dP columns have been read too
+            if (!(ok = spin_phase(bar->ds_full + (u & 1), (u >> 1) & 1, w))) break;
+            if (u + 2 < n && !(ok = issue_dp(u + 2))) break;
             tc_fence_after();
-            for (int hh = 0; hh < 2 && i >= n - nt; hh++)
-                mma4_ts_mn64(tmem + 384, tmem + 128 * st + 64 * hh,
-                             dKt + st * kStageDesc + hh * kHalfDesc, idO,
-                             i > n - nt || hh > 0 ? 1u : 0u);
-            mma_commit_warp(bar.stage_empty + st);
-            if (i + 2 < n) ok = issue_s(i + 2);
+            if (u >= n - nt)
+                mma_block64(tmem + 384, tmem + 64 * (u & 3), dKt + u % N1 * kBlockDesc, idO,
+                             u > n - nt ? 1u : 0u);
+            mma_commit(bar->empty1 + u % N1);
+            if (u + 3 < n) ok = issue_s(u + 3);
         }
-        mma_commit_warp(bar.acc_full);
-        wait_phase_cleanup(bar.acc_full, 0, kCleanupPolls);
+        mma_commit(&bar->acc_full);
+        wait_phase_cleanup(&bar->acc_full, 0, kCleanupPolls);
+        }
+        __syncwarp();
     } else if (warp < 8) {
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, i = i0 + row;
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const RowKeys rk = row_keys(p, seq, i);
         const int64_t at = ((int64_t)b * p.H + h) * p.Nq + i;
         const bool real = rk.hi > 0;
         const float nl = real ? -a.lse[at] * kLog2e : 0.f;
         float nd = real && n == nt ? -a.delta[at] : 0.f;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
-        bool ok = true;
-        for (int it = 0; it < n; it++) {
-            const int st = it & 1, c0 = kt.tile(it % nt) * 128 + 64 * half;
-            if (!(ok = wait_warp(bar.s_full + st, (it >> 1) & 1, w))) break;
+        bool ok = true, summed = n == nt;
+        // (a group without a block of its own still joins delta)
+        auto join_delta = [&]() -> bool {
+            half_delta[half * 128 + row] = nd;
+            mbar_arrive_warp(&bar->delta_bar);
+            if (!wait_warp(&bar->delta_bar, 0, w)) return false;
+            nd = half_delta[row] + half_delta[128 + row];
+            if (half == 0 && real) a.delta[at] = -nd;
+            summed = true;
+            return true;
+        };
+        for (int u = half; u < n; u += 2) {
+            const int ph = (u >> 1) & 1, c0 = kt.tile(u % nt) * 64;
+            if (!summed && u >= n - nt && !(ok = join_delta())) break;
+            if (!(ok = wait_warp(bar->s_full + (u & 3), (u >> 2) & 1, w))) break;
             tc_fence_after();
+            const uint32_t ts = tl + 64 * (u & 3), td = tl + 256 + 64 * half;
             float x[64];
-            tmem_ld32f(tl + 128 * st, &x[0]);
-            tmem_ld32f(tl + 128 * st + 32, &x[32]);
+            tmem_ld32f(ts, &x[0]);
+            tmem_ld32f(ts + 32, &x[32]);
             tmem_wait_ld();
             const bool all = __all_sync(0xffffffffu, c0 + 64 <= rk.hi &&
                                                          (c0 >= rk.lo || c0 + 64 <= rk.sink));
@@ -536,22 +565,22 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                 x[k] = fast_exp2(lo);
                 x[k + 1] = fast_exp2(hi);
             }
-            if (kt.tile(it % nt) * 128 + 128 > seq.len) {
+            if (c0 + 64 > seq.len) {
                 // keys past the sequence may hold anything, and 0 * NaN is NaN: they become
-                // zeros before the product over the keys (S of this tile is done with them)
-                zero_rows(sm + L::kRing + st * 2 * kTile, max(0, seq.len - kt.tile(it % nt) * 128), 128,
-                          PN, kPanel, half * 128 + row, 256);
+                // zeros before the product over the keys (S of this block is done with them)
+                zero_rows(sm + L::kRing + u % N1 * L::kBlock, max(0, seq.len - c0), 64, PN,
+                          L::kBlockPanel, row, 128);
                 fence_proxy_async_smem();
             }
-            if (!(ok = wait_warp(bar.dp_full, it & 1, w))) break;
+            if (!(ok = wait_warp(bar->dp_full + half, ph, w))) break;
             tc_fence_after();
-            if (it < n - nt) {
-                // this half's part of delta = sum P dP; the halves meet in shared memory
+            if (u < n - nt) {
+                // this group's part of delta = sum P dP
                 float sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     float y[32];
-                    tmem_ld32f(tl + 256 + c, y);
+                    tmem_ld32f(td + c, y);
                     tmem_wait_ld();
                     const uint32_t s = (uint32_t)(see >> c);
 #pragma unroll
@@ -559,15 +588,8 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                         sum = fmaf((s >> k) & 1 ? x[c + k] : 0.f, (s >> k) & 1 ? y[k] : 0.f, sum);
                 }
                 nd -= sum;
-                if (it == n - nt - 1) {
-                    half_delta[half * 128 + row] = nd;
-                    mbar_arrive_warp(bar.p_full);
-                    if (!(ok = wait_warp(bar.p_full, 0, w))) break;
-                    nd = half_delta[row] + half_delta[128 + row];
-                    if (half == 0 && real) a.delta[at] = -nd;
-                }
                 tc_fence_before();
-                mbar_arrive_warp(bar.ds_full);
+                mbar_arrive_warp(bar->ds_full + half);
                 continue;
             }
             const uint64_t nd2 = f2_pack(nd, nd);
@@ -575,7 +597,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
                 float y[32];
-                tmem_ld32f(tl + 256 + c, y);
+                tmem_ld32f(td + c, y);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; k += 2)
@@ -590,16 +612,17 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                 for (int k = 0; k < 16; k++) pk[c / 2 + k] = pack_bf16(y[2 * k], y[2 * k + 1]);
             }
-            tmem_st32(tl + 128 * st, pk);
+            tmem_st32(ts, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive_warp(bar.ds_full);
+            mbar_arrive_warp(bar->ds_full + half);
         }
-        if (ok && wait_warp(bar.acc_full, 0, w)) {
+        if (ok && !summed) ok = join_delta();
+        if (ok && wait_warp(&bar->acc_full, 0, w)) {
             tc_fence_after();
             const int x = half * (D / 2);
-            store_row<D / 2>(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 384 + x,
-                             dq + (int64_t)i * a.g.dq.token + x, p.scale, p.d - x, i < p.Nq);
+            store_row<D / 2>(tl + 384 + x, dq + (int64_t)i * a.g.dq.token + x, p.scale, p.d - x,
+                             i < p.Nq);
         }
     }
     tc_fence_before();
@@ -613,11 +636,16 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
 template <int D>
 cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
                    const void *v, const void *dout, const BwdArgs &a, cudaStream_t stream) {
-    CUtensorMap mq, mk, mv, md;
-    if (!map_tokens(&mq, q, p.q, p.B, p.H, p.Nq, p.d, 128) ||
-        !map_tokens(&mk, k, p.k, p.B, p.Hkv, p.Nk, p.d, 128) ||
-        !map_tokens(&mv, v, p.v, p.B, p.Hkv, p.Nk, p.d, 128) ||
-        !map_tokens(&md, dout, g.dout, p.B, p.H, p.Nq, p.d, 128))
+    // the fixed tiles have 128 rows, the streamed blocks 64
+    CUtensorMap q128, k128, v128, d128, q64, k64, v64, d64;
+    if (!map_tokens(&q128, q, p.q, p.B, p.H, p.Nq, p.d, 128) ||
+        !map_tokens(&q64, q, p.q, p.B, p.H, p.Nq, p.d, 64) ||
+        !map_tokens(&d128, dout, g.dout, p.B, p.H, p.Nq, p.d, 128) ||
+        !map_tokens(&d64, dout, g.dout, p.B, p.H, p.Nq, p.d, 64) ||
+        !map_tokens(&k128, k, p.k, p.B, p.Hkv, p.Nk, p.d, 128) ||
+        !map_tokens(&k64, k, p.k, p.B, p.Hkv, p.Nk, p.d, 64) ||
+        !map_tokens(&v128, v, p.v, p.B, p.Hkv, p.Nk, p.d, 128) ||
+        !map_tokens(&v64, v, p.v, p.B, p.Hkv, p.Nk, p.d, 64))
         return cudaErrorInvalidValue;
     constexpr uint32_t smem = BwdLayout<D>::kSmem;
     cudaError_t e = tcs::set_smem(tc_window_dkv_kernel<D>, smem);
@@ -626,10 +654,10 @@ cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const 
     const unsigned gk = (unsigned)p.B * p.Hkv * ((p.Nk + 127) / 128);
     const unsigned gq = (unsigned)p.B * p.H * ((p.Nq + 127) / 128);
     // dq first: it completes delta
-    tc_window_dq_kernel<D><<<gq, kThreads, smem, stream>>>(mq, mk, mv, md, a);
+    tc_window_dq_kernel<D><<<gq, kThreads, smem, stream>>>(q128, k64, v64, d128, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    tc_window_dkv_kernel<D><<<gk, kThreads, smem, stream>>>(mq, mk, mv, md, a);
+    tc_window_dkv_kernel<D><<<gk, kThreads, smem, stream>>>(q64, k128, v128, d64, a);
     return cudaGetLastError();
 }
 

@@ -362,25 +362,58 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
 }
 
 // ---------------------------------------------------------------- delta
-// One warp a row; rows without keys get 0 (their dO may be anything).  Bound by
-// memory: dO and O are read once.
-template <typename T>
+// 16-byte loads, d / (elements of 16 bytes) lanes a row; rows without keys get 0 (their
+// dO may be anything).  Bound by memory: dO and O are read once.
+__device__ __forceinline__ float dot16(const float *a, const float *b) {
+    const float4 x = *reinterpret_cast<const float4 *>(a), y = *reinterpret_cast<const float4 *>(b);
+    return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+}
+__device__ __forceinline__ float dot16(const __nv_bfloat16 *a, const __nv_bfloat16 *b) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(a), y = *reinterpret_cast<const uint4 *>(b);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
+        sum = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), sum);
+    }
+    return sum;
+}
+
+template <typename T, int D>
 __global__ void __launch_bounds__(256)
 row_delta_kernel(WinProblem p, WinGrads g, const T *out, const T *dout, float *delta) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (int64_t)p.B * p.H * p.Nq) return;
-    const int i = (int)(row % p.Nq), h = (int)(row / p.Nq % p.H), b = (int)(row / p.Nq / p.H);
-    const Sequence seq = sequence(p, b);
+    constexpr int V = 16 / sizeof(T), LANES = D / V, ROWS = 256 / LANES;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+    const int x = threadIdx.x % LANES * V;
     float sum = 0.f;
-    if (row_keys(p, seq, i).hi > 0) {
-        const T *o = out + b * p.o.batch + h * p.o.head + i * p.o.token;
-        const T *d = dout + b * g.dout.batch + h * g.dout.head + i * g.dout.token;
-        for (int x = lane; x < p.d; x += 32) sum = fmaf(to_f32(o[x]), to_f32(d[x]), sum);
+    if (row < (int64_t)p.B * p.H * p.Nq) {
+        const int i = (int)(row % p.Nq), bh = (int)(row / p.Nq), h = bh % p.H, b = bh / p.H;
+        const Sequence seq = sequence(p, b);
+        const int64_t pos = seq.start + i;
+        if (pos >= 0 && pos < seq.len)   // a real row
+            sum = dot16(out + b * p.o.batch + h * p.o.head + i * p.o.token + x,
+                        dout + b * g.dout.batch + h * g.dout.head + i * g.dout.token + x);
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (lane == 0) delta[row] = sum;
+    for (int m = LANES / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (x == 0 && row < (int64_t)p.B * p.H * p.Nq) delta[row] = sum;
+}
+
+template <typename T>
+cudaError_t run_delta(const WinProblem &p, const WinGrads &g, const void *out, const void *dout,
+                      float *delta, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.B * p.H * p.Nq;
+    const int per = 256 / (p.d * (int)sizeof(T) / 16);
+    const unsigned grid = (unsigned)((rows + per - 1) / per);
+    const T *o = (const T *)out, *d = (const T *)dout;
+    if (p.d == 32)
+        row_delta_kernel<T, 32><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
+    else if (p.d == 64)
+        row_delta_kernel<T, 64><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
+    else
+        row_delta_kernel<T, 128><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
+    return cudaGetLastError();
 }
 
 template <typename K>
@@ -433,15 +466,8 @@ cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q
 
 cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
                       const void *dout, float *delta, cudaStream_t stream) {
-    const int64_t rows = (int64_t)p.B * p.H * p.Nq;
-    const unsigned grid = (unsigned)((rows + 7) / 8);
-    if (dtype == MONARCH_F32)
-        row_delta_kernel<float><<<grid, 256, 0, stream>>>(p, g, (const float *)out,
-                                                          (const float *)dout, delta);
-    else
-        row_delta_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
-            p, g, (const __nv_bfloat16 *)out, (const __nv_bfloat16 *)dout, delta);
-    return cudaGetLastError();
+    return dtype == MONARCH_F32 ? run_delta<float>(p, g, out, dout, delta, stream)
+                                : run_delta<__nv_bfloat16>(p, g, out, dout, delta, stream);
 }
 
 }  // namespace win

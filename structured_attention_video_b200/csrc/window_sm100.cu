@@ -221,6 +221,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             // tile t uses S buffer hc & 1.  Order: S of the first two halves, then per
             // half PV(hc), S(hc + 2).  S(hc + 2) overwrites the columns that PV(hc)
             // reads as P: one thread's products execute in issue order.
+            if (elect_one()) {
             const int t = warp == 13 ? 0 : 1;
             constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0);
             constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
@@ -229,7 +230,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kV), kPanel, 1024);
             constexpr uint32_t kTileDesc = kTile >> 4, kHalfDesc = 64 * 128 >> 4;
             const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
-            bool ok = !a.stall || spin_warp(stall_bar, 0, w);
+            bool ok = !a.stall || spin_phase(stall_bar, 0, w);
             struct Cursor {
                 int pi, pc, i, hc, jc0;
                 FwdProblem pr;
@@ -253,29 +254,29 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             };
             auto issue_s = [&](const Cursor &c) -> bool {
                 const int jc = c.jc0 + (c.i >> 1), sk = jc & 1, kh = c.i & 1, b = c.hc & 1;
-                if (c.i == 0 && !spin_warp(q_full + t, c.pc & 1, w)) return false;
-                if (kh == 0 && !spin_warp(k_full + sk, (jc >> 1) & 1, w)) return false;
+                if (c.i == 0 && !spin_phase(q_full + t, c.pc & 1, w)) return false;
+                if (kh == 0 && !spin_phase(k_full + sk, (jc >> 1) & 1, w)) return false;
                 tc_fence_after();
-                mma_ss_head<D>(tS + b * 64, dQ, dK + sk * kTileDesc + kh * kHalfDesc, idS);
-                mma_commit_warp(s_full + 2 * t + b);
+                mma_head<D, 128>(tS + b * 64, dQ, dK + sk * kTileDesc + kh * kHalfDesc, idS);
+                mma_commit(s_full + 2 * t + b);
                 const bool last = c.i == c.pr.nh - 1;
-                if (kh == 1 || last) mma_commit_warp(k_empty + sk);
-                if (last) mma_commit_warp(q_empty + t);
+                if (kh == 1 || last) mma_commit(k_empty + sk);
+                if (last) mma_commit(q_empty + t);
                 return true;
             };
             auto issue_pv = [&](const Cursor &c) -> bool {
                 const int jc = c.jc0 + (c.i >> 1), st = jc & 1, kh = c.i & 1, b = c.hc & 1;
-                if (kh == 0 && !spin_warp(v_full + st, (jc >> 1) & 1, w)) return false;
-                if (!spin_warp(p_full + 2 * t + b, (c.hc >> 1) & 1, w)) return false;
+                if (kh == 0 && !spin_phase(v_full + st, (jc >> 1) & 1, w)) return false;
+                if (!spin_phase(p_full + 2 * t + b, (c.hc >> 1) & 1, w)) return false;
                 // the first PV of a problem overwrites O: the epilogue must have read it
-                if (c.i == 0 && c.pc > 0 && !spin_warp(o_free + t, (c.pc - 1) & 1, w)) return false;
+                if (c.i == 0 && c.pc > 0 && !spin_phase(o_free + t, (c.pc - 1) & 1, w)) return false;
                 tc_fence_after();
-                mma4_ts_mn64(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
+                mma_block64(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
                              c.i > 0 ? 1u : 0u);
-                mma_commit_warp(pv_done + t);
+                mma_commit(pv_done + t);
                 const bool last = c.i == c.pr.nh - 1;
-                if (kh == 1 || last) mma_commit_warp(v_empty + st);
-                if (last) mma_commit_warp(o_full + t);
+                if (kh == 1 || last) mma_commit(v_empty + st);
+                if (last) mma_commit(o_full + t);
                 return true;
             };
             Cursor cs{0, 0, 0, 0, 0, {}};   // next S to issue
@@ -291,8 +292,10 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 if (more) advance(cs);
                 advance(cp);
             }
-            mma_commit_warp(mma_done);
+            mma_commit(mma_done);
             wait_phase_cleanup(mma_done, 0, kCleanupPolls);
+            }
+            __syncwarp();
         }
     } else if (warp >= 8) {
         // ---------------- epilogue: O / l to bfloat16 rows

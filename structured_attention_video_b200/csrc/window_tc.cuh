@@ -15,33 +15,48 @@ using tcs::kMaxSmem;
 using tcs::kPanel;
 using tcs::wait_warp;
 
-// Four K-steps (K = 64) of D (+)= A B^T, both operands one K-major 128-byte swizzled
-// panel of 64 columns: K-step k starts 32 k bytes into the panel.
-__device__ __forceinline__ void mma4_ss_k64(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                            uint32_t idesc, uint32_t acc0) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred e, p0;\n\t"
-        ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.and.b32 p0, %4, 0, e;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc0)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_one_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 
-// D = A B^T over a head of D elements: panels of 64 columns, 16 KB apart (128 rows each).
-template <int D>
-__device__ __forceinline__ void mma_ss_head(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                            uint32_t idesc) {
-    if (D == 128)
-        mma8_ss_k128(d_tmem, a, b, idesc, 0u);
-    else
-        mma4_ss_k64(d_tmem, a, b, idesc, 0u);
+// D = A B^T over a head of HD elements: A a 128-row tile, B of BROWS rows, both K-major
+// 128-byte swizzled panels of 64 columns (a K-step of 16 is 32 bytes inside a panel).
+template <int HD, int BROWS>
+__device__ __forceinline__ void mma_head(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < HD / 16; k++)
+        mma_one(d_tmem, a + (k >> 2) * (kPanel >> 4) + (k & 3) * 2,
+                b + (k >> 2) * (BROWS * 128 >> 4) + (k & 3) * 2, idesc, k > 0);
+}
+
+// D (+)= A B over 64 keys or queries: A bfloat16 pairs in tensor memory (8 columns a
+// K-step), B an MN-major swizzled block (16 rows = 2 KB a K-step).
+__device__ __forceinline__ void mma_block64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                            uint32_t idesc, uint32_t acc) {
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        mma_one_ts(d_tmem, a_tmem + 8 * k, b + 128 * k, idesc, k > 0 ? 1u : acc);
 }
 
 // Rows [first, last) of a tile of 64-column panels (128-byte rows, panel_bytes apart)
