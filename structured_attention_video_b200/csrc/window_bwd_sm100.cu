@@ -124,6 +124,16 @@ __device__ __forceinline__ void probabilities(float (&x)[64], float c, const flo
     }
 }
 
+// A position in a ring of N blocks: slot and phase of its barriers, without divisions
+// (the issuing thread has nothing to hide their latency behind).
+template <int N> struct Slot {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) s = 0, ph ^= 1;
+    }
+};
+
 // Barriers of one CTA.  N1, N2: blocks of the two rings; NS: S buffers.
 template <int N1, int N2, int NS> struct Bars {
     uint64_t fix_full;                  // the fixed tiles
@@ -192,26 +202,29 @@ __device__ __forceinline__ void load_all(uint8_t *sm, B *bar, const CUtensorMap 
         }
     }
     int issued1 = 0, issued2 = 0;
+    Slot<N1> r1;
+    Slot<N2> r2;
     for (int u = 0; u < n; u++) {
         int h, row;
         coords(u, h, row);
-        const int s1 = u % N1, s2 = u % N2;
-        if (u >= N1 && !wait_warp(bar->empty1 + s1, (u / N1 - 1) & 1, w)) break;
+        if (u >= N1 && !wait_warp(bar->empty1 + r1.s, r1.ph ^ 1, w)) break;
         if (lane == 0) {
-            uint8_t *dst = sm + L::kRing + s1 * L::kBlock;
-            mbar_expect_tx(bar->full1 + s1, L::kBlock);
+            uint8_t *dst = sm + L::kRing + r1.s * L::kBlock;
+            mbar_expect_tx(bar->full1 + r1.s, L::kBlock);
             for (int pn = 0; pn < PN; pn++)
-                tma_load_4d(dst + pn * L::kBlockPanel, ring1, pn * 64, row, h, b, bar->full1 + s1);
+                tma_load_4d(dst + pn * L::kBlockPanel, ring1, pn * 64, row, h, b, bar->full1 + r1.s);
         }
         issued1++;
-        if (u >= N2 && !wait_warp(bar->empty2 + s2, (u / N2 - 1) & 1, w)) break;
+        r1.next();
+        if (u >= N2 && !wait_warp(bar->empty2 + r2.s, r2.ph ^ 1, w)) break;
         if (lane == 0) {
-            uint8_t *dst = sm + L::kRing + (N1 + s2) * L::kBlock;
-            mbar_expect_tx(bar->full2 + s2, L::kBlock);
+            uint8_t *dst = sm + L::kRing + (N1 + r2.s) * L::kBlock;
+            mbar_expect_tx(bar->full2 + r2.s, L::kBlock);
             for (int pn = 0; pn < PN; pn++)
-                tma_load_4d(dst + pn * L::kBlockPanel, ring2, pn * 64, row, h, b, bar->full2 + s2);
+                tma_load_4d(dst + pn * L::kBlockPanel, ring2, pn * 64, row, h, b, bar->full2 + r2.s);
         }
         issued2++;
+        r2.next();
     }
     if (lane == 0) bar->drain(issued1, issued2);
 }
@@ -288,18 +301,22 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint64_t dO = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
         const uint64_t dQt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
         const uint64_t dOt = smem_desc_sw128(ring + N1 * L::kBlock, L::kBlockPanel, 1024);
-        auto issue_s = [&](int u) -> bool {
-            if (!spin_phase(bar->full1 + u % N1, (u / N1) & 1, w)) return false;
+        Slot<N1> next_s, cur_q;    // of the next S; of block u
+        Slot<N2> next_dp, cur_do;
+        auto issue_s = [&](int h) -> bool {
+            if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
             tc_fence_after();
-            mma_head<D, 64>(tmem + 64 * (u & 1), dK, dQ + u % N1 * kBlockDesc, idS);
-            mma_commit(bar->s_full + (u & 1));
+            mma_head<D, 64>(tmem + 64 * h, dK, dQ + next_s.s * kBlockDesc, idS);
+            mma_commit(bar->s_full + h);
+            next_s.next();
             return true;
         };
-        auto issue_dp = [&](int u) -> bool {
-            if (!spin_phase(bar->full2 + u % N2, (u / N2) & 1, w)) return false;
+        auto issue_dp = [&](int h) -> bool {
+            if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
             tc_fence_after();
-            mma_head<D, 64>(tmem + 128 + 64 * (u & 1), dV, dO + u % N2 * kBlockDesc, idS);
-            mma_commit(bar->dp_full + (u & 1));
+            mma_head<D, 64>(tmem + 128 + 64 * h, dV, dO + next_dp.s * kBlockDesc, idS);
+            mma_commit(bar->dp_full + h);
+            next_dp.next();
             return true;
         };
         bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
@@ -308,15 +325,17 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             const int h = u & 1, ph = (u >> 1) & 1;
             if (!(ok = spin_phase(bar->p_full + h, ph, w))) break;
             tc_fence_after();
-            mma_block64(tmem + 256, tmem + 64 * h, dOt + u % N2 * kBlockDesc, idO, u > 0 ? 1u : 0u);
-            mma_commit(bar->empty2 + u % N2);
-            if (u + 2 < n && !(ok = issue_s(u + 2))) break;
+            mma_block64(tmem + 256, tmem + 64 * h, dOt + cur_do.s * kBlockDesc, idO, u > 0 ? 1u : 0u);
+            mma_commit(bar->empty2 + cur_do.s);
+            cur_do.next();
+            if (u + 2 < n && !(ok = issue_s(h))) break;
             if (!(ok = spin_phase(bar->ds_full + h, ph, w))) break;
             tc_fence_after();
-            mma_block64(tmem + 384, tmem + 128 + 64 * h, dQt + u % N1 * kBlockDesc, idO,
-                         u > 0 ? 1u : 0u);
-            mma_commit(bar->empty1 + u % N1);
-            if (u + 2 < n) ok = issue_dp(u + 2);
+            mma_block64(tmem + 384, tmem + 128 + 64 * h, dQt + cur_q.s * kBlockDesc, idO,
+                        u > 0 ? 1u : 0u);
+            mma_commit(bar->empty1 + cur_q.s);
+            cur_q.next();
+            if (u + 2 < n) ok = issue_dp(h);
         }
         mma_commit(&bar->acc_full);
         wait_phase_cleanup(&bar->acc_full, 0, kCleanupPolls);
@@ -491,19 +510,23 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint64_t dK = smem_desc_sw128(ring, 16, 1024);
         const uint64_t dV = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
         const uint64_t dKt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
+        Slot<N1> next_s, cur_k;    // of the next S; of block u
+        Slot<N2> next_dp;
         auto issue_s = [&](int u) -> bool {
-            if (!spin_phase(bar->full1 + u % N1, (u / N1) & 1, w)) return false;
+            if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
             tc_fence_after();
-            mma_head<D, 64>(tmem + 64 * (u & 3), dQ, dK + u % N1 * kBlockDesc, idS);
+            mma_head<D, 64>(tmem + 64 * (u & 3), dQ, dK + next_s.s * kBlockDesc, idS);
             mma_commit(bar->s_full + (u & 3));
+            next_s.next();
             return true;
         };
         auto issue_dp = [&](int u) -> bool {
-            if (!spin_phase(bar->full2 + u % N2, (u / N2) & 1, w)) return false;
+            if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
             tc_fence_after();
-            mma_head<D, 64>(tmem + 256 + 64 * (u & 1), dO, dV + u % N2 * kBlockDesc, idS);
+            mma_head<D, 64>(tmem + 256 + 64 * (u & 1), dO, dV + next_dp.s * kBlockDesc, idS);
             mma_commit(bar->dp_full + (u & 1));
-            mma_commit(bar->empty2 + u % N2);
+            mma_commit(bar->empty2 + next_dp.s);
+            next_dp.next();
             return true;
         };
         bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
@@ -512,12 +535,13 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int u = 0; ok && u < n; u++) {
             // dS(u) is written: the half's dP columns have been read too
             if (!(ok = spin_phase(bar->ds_full + (u & 1), (u >> 1) & 1, w))) break;
-            if (u + 2 < n && !(ok = issue_dp(u + 2))) break;
+            if (u + 2 < n && !(ok = issue_dp(u))) break;   // of block u + 2
             tc_fence_after();
             if (u >= n - nt)
-                mma_block64(tmem + 384, tmem + 64 * (u & 3), dKt + u % N1 * kBlockDesc, idO,
-                             u > n - nt ? 1u : 0u);
-            mma_commit(bar->empty1 + u % N1);
+                mma_block64(tmem + 384, tmem + 64 * (u & 3), dKt + cur_k.s * kBlockDesc, idO,
+                            u > n - nt ? 1u : 0u);
+            mma_commit(bar->empty1 + cur_k.s);
+            cur_k.next();
             if (u + 3 < n) ok = issue_s(u + 3);
         }
         mma_commit(&bar->acc_full);
