@@ -10,22 +10,26 @@
 //   tc_window_dkv_kernel  128 keys of one key head against the 128-query tiles of
 //                         every head of its group that see them;
 //   tc_window_dq_kernel   128 queries of one head against their 128-key tiles.
-// 384 threads a CTA, one CTA an SM: warps 0-7 the elementwise work, warp 8 loads
-// (TMA), warp 9 issues the products, warp 10 stages lse and delta.
+// 608 threads a CTA, one CTA an SM: warps 0-15 the elementwise work, warp 16 loads, one
+// thread of warp 17 issues every product, warp 18 stages lse and delta (dkv).
 //
 // The streamed side goes in blocks of 64 rows (queries in dkv, keys in dq).  Blocks u
-// with u % 2 = h belong to warps 4 h .. 4 h + 3 (thread = tensor-memory lane = row of the
-// fixed tile) and to half h of the tensor-memory columns, so the two groups work on
-// different blocks at different times and the tensor pipe has the products of one
-// while the other computes.  Order of the products (fixed, so the sums are too):
+// with u % 2 = h belong to warps 8 h .. 8 h + 7 (a thread has 32 columns of one row, its
+// tensor-memory lane, of the fixed tile), so the two groups work on different blocks at
+// different times and the tensor pipe has the products of one while the other computes.
+// Order of the products (fixed, so the sums are too):
 //   dkv:  dV(u) S(u+2) after P(u);  dK(u) dP(u+2) after dS(u)
-//   dq:   dP(u+2) dQ(u) S(u+3) after dS(u)   (S has four buffers)
-// P overwrites S and dS overwrites dP (S in dq) in tensor memory; a later product into
-// the same columns follows in issue order.
-// The blocks go through two rings of their own, as many as shared memory holds.  A
-// block is needed about a block's work after its predecessor, and a load takes about as
-// long as a block (16 KB a tensor): with two stages of 128 rows the tensor pipe
-// waited for loads and a 128 x 128 tile took 5100 clocks in dkv and 3460 in dq.
+//   dq:   S(u+2) once S(u) is read;  dQ(u) dP(u+2) after dS(u)
+// P lies over S and dS over dP in tensor memory; a later product into the same columns
+// follows in issue order.  What shaped this (d = 128, nine 480p frames):
+//  - Two stages of 128 rows with 128-column products, all warps in step: dkv 1107 us, dq
+//    787; the pipe waited for loads and for the elementwise work in turn.
+//  - Two or three issuing threads, to fill the gaps at one's barrier polls: dkv 915-932,
+//    dq 600-620.  Where a product has to follow another thread's, the commit, the wait and
+//    the pipe's latency cost about 700 clocks, and interleaved streams run slower.
+//  - M = 128, N = 64 reads 4 KB of A and 2 KB of B a K-step, 48 clocks of shared memory's
+//    128 bytes a clock against 32 of the tensor pipe: Q and dO live in tensor memory in dq
+//    (648 -> 624); in dkv the accumulators leave no room.
 //
 // delta comes from out as the forward rounded it, an error of 2^-8 |dO.O| at most.  A
 // row of n keys of like weight has |O| of about n^(-1/2) |v|, so against dP it matters
@@ -42,20 +46,21 @@ namespace win {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 384;
+constexpr int kThreads = 608;
+constexpr int kLoadWarp = 16, kIssueWarp = 17, kStatsWarp = 18;
 constexpr int kExactBlocks = 6;
+constexpr int kDkvRing1 = 5, kDkvRing2 = 5, kDqRing1 = 8, kDqRing2 = 6;
 
-// Shared memory: two fixed tiles of 128 rows, two rings of 64-row blocks, and per slot of
-// the first ring -lse and -delta of its 64 queries (dkv).
-template <int D> struct BwdLayout {
+// Shared memory: FIX fixed tiles of 128 rows (K and V of dkv), two rings of N1 and N2
+// 64-row blocks, then per slot of the first ring -lse and -delta of its 64 queries (dkv) or the
+// warps' parts of delta (dq).
+template <int D, int FIX, int N1, int N2> struct BwdLayout {
     static constexpr uint32_t kTile = (D / 64) * kPanel;
     static constexpr uint32_t kBlock = kTile / 2;             // panels of 64 rows
     static constexpr uint32_t kBlockPanel = 64 * 128;
-    static constexpr int kBlocks = 10;
-    static constexpr uint32_t kFix = 0;                       // K, V (dkv) or Q, dO (dq)
-    static constexpr uint32_t kRing = 2 * kTile;
-    static constexpr uint32_t kStats = kRing + kBlocks * kBlock;
-    static constexpr uint32_t kBar = kStats + 5 * 512;
+    static constexpr uint32_t kRing = FIX * kTile;
+    static constexpr uint32_t kStats = kRing + (N1 + N2) * kBlock;
+    static constexpr uint32_t kBar = kStats + (FIX ? N1 * 512 : 2048);
     static constexpr uint32_t kSmem = kBar + 512;   // the base is 1024-aligned (checked)
     static_assert(kSmem <= (uint32_t)kMaxSmem, "window backward shared memory");
 };
@@ -65,30 +70,30 @@ struct BwdArgs {
     WinGrads g;
     const float *lse;
     float *delta;   // of the rounded out; rows of few keys are written again (dq kernel)
+    const __nv_bfloat16 *q, *dout;
     __nv_bfloat16 *dq, *dk, *dv;
     int *status;
     long long limit;
     int stall;
 };
 
-// 32-bit pieces of a 64-bit mask: bit k says whether element first + k of [lo, hi)
-// counts.
-__device__ __forceinline__ uint64_t below(int n) {
-    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+// The lowest n bits, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t below(int n) {
+    return n >= 32 ? ~0u : (1u << max(n, 0)) - 1;
 }
 
-// 64 columns of an accumulator row to bfloat16 in global memory (columns below d).
+// N columns of an accumulator row to bfloat16 in global memory (columns below d).
 template <int N>
 __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16 *dst, float scale, int d,
                                           bool real) {
 #pragma unroll 1
-    for (int c = 0; c < N; c += 32) {
-        float o[32];
-        tmem_ld32f(taddr + c, o);
+    for (int c = 0; c < N; c += 16) {
+        float o[16];
+        tmem_ld16f(taddr + c, o);
         tmem_wait_ld();
         if (!real || c >= d) continue;
 #pragma unroll
-        for (int e = 0; e < 4; e++)
+        for (int e = 0; e < 2; e++)
             *reinterpret_cast<uint4 *>(dst + c + 8 * e) =
                 make_uint4(pack_bf16(o[8 * e] * scale, o[8 * e + 1] * scale),
                            pack_bf16(o[8 * e + 2] * scale, o[8 * e + 3] * scale),
@@ -100,28 +105,20 @@ __device__ __forceinline__ void zero_row(__nv_bfloat16 *dst, int n) {
     for (int c = 0; c < n; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
 }
 
-// P of 64 columns: x = exp2(c x + nl[column]), masked by `see`.  nl in shared memory.
-__device__ __forceinline__ void probabilities(float (&x)[64], float c, const float *nl,
-                                              bool all, uint64_t see) {
-    const uint64_t c2 = f2_pack(c, c);
+// Elements whose bit of `see` is 0 become 0, whatever they were.
+__device__ __forceinline__ void keep_seen(float (&x)[32], uint32_t see) {
 #pragma unroll
-    for (int k = 0; k < 64; k += 4) {
-        const ulonglong2 n2 = *reinterpret_cast<const ulonglong2 *>(nl + k);
-        const uint64_t a = f2_fma(f2_pack(x[k], x[k + 1]), c2, n2.x);
-        const uint64_t b = f2_fma(f2_pack(x[k + 2], x[k + 3]), c2, n2.y);
-        f2_unpack(a, x[k], x[k + 1]);
-        f2_unpack(b, x[k + 2], x[k + 3]);
+    for (int k = 0; k < 32; k++) x[k] = (see >> k) & 1 ? x[k] : 0.f;
+}
+
+// 32 columns as bfloat16 pairs over 16 columns of tensor memory.
+__device__ __forceinline__ void pack_to_tmem(uint32_t taddr, const float (&x)[32]) {
+    uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 4; e++) x[k + e] = fast_exp2(x[k + e]);
-    }
-    if (!all) {
-        const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
-#pragma unroll
-        for (int k = 0; k < 32; k++) {
-            x[k] = (s0 >> k) & 1 ? x[k] : 0.f;
-            x[k + 32] = (s1 >> k) & 1 ? x[k + 32] : 0.f;
-        }
-    }
+    for (int k = 0; k < 16; k++) pk[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
+    tmem_st8(taddr, *reinterpret_cast<const uint32_t(*)[8]>(&pk[0]));
+    tmem_st8(taddr + 8, *reinterpret_cast<const uint32_t(*)[8]>(&pk[8]));
+    tmem_wait_st();
 }
 
 // A position in a ring of N blocks: slot and phase of its barriers, without divisions
@@ -134,23 +131,25 @@ template <int N> struct Slot {
     }
 };
 
-// Barriers of one CTA.  N1, N2: blocks of the two rings; NS: S buffers.
-template <int N1, int N2, int NS> struct Bars {
+// Barriers of one CTA.  N1, N2: blocks of the two rings.
+template <int N1, int N2> struct Bars {
     uint64_t fix_full;                  // the fixed tiles
+    uint64_t tmem_full;                 // Q and dO in tensor memory (dq), 8 warps
     uint64_t full1[N1], empty1[N1];     // Q (dkv) or K (dq)
     uint64_t full2[N2], empty2[N2];     // dO or V
     uint64_t stats_full[N1];            // dkv
-    uint64_t s_full[NS];                // S in tensor memory
-    uint64_t dp_full[2];
-    uint64_t p_full[2], ds_full[2];     // one arrival a warp of the half
-    uint64_t delta_bar;                 // the halves' parts of delta (dq), once
-    uint64_t acc_full;                  // the last products
+    uint64_t s_full[2], dp_full[2];     // products in tensor memory, per half
+    uint64_t s_free[2];                 // S is read (dq), the half's 8 warps
+    uint64_t p_full[2], ds_full[2];     // the half's 8 warps
+    uint64_t delta_bar;                 // the parts of delta (dq), 16 warps, once
+    uint64_t done;                      // the last products
     uint64_t stall_bar;                 // never completed (fault injection)
     uint32_t tmem_slot;
     int abort_flag;
 
     __device__ __forceinline__ void init() {
         mbar_init(&fix_full, 1);
+        mbar_init(&tmem_full, 8);
         for (int i = 0; i < N1; i++) {
             mbar_init(full1 + i, 1);
             mbar_init(empty1 + i, 1);
@@ -160,14 +159,15 @@ template <int N1, int N2, int NS> struct Bars {
             mbar_init(full2 + i, 1);
             mbar_init(empty2 + i, 1);
         }
-        for (int i = 0; i < NS; i++) mbar_init(s_full + i, 1);
         for (int i = 0; i < 2; i++) {
+            mbar_init(s_full + i, 1);
             mbar_init(dp_full + i, 1);
-            mbar_init(p_full + i, 4);
-            mbar_init(ds_full + i, 4);
+            mbar_init(s_free + i, 8);
+            mbar_init(p_full + i, 8);
+            mbar_init(ds_full + i, 8);
         }
-        mbar_init(&delta_bar, 8);
-        mbar_init(&acc_full, 1);
+        mbar_init(&delta_bar, 16);
+        mbar_init(&done, 1);
         mbar_init(&stall_bar, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -175,7 +175,6 @@ template <int N1, int N2, int NS> struct Bars {
     // Every issued copy lands before the CTA may exit (an aborted CTA may not have
     // waited for the last ones).
     __device__ __forceinline__ void drain(int issued1, int issued2) {
-        wait_phase_cleanup(&fix_full, 0, kCleanupPolls);
         for (int u = max(0, issued1 - N1); u < issued1; u++)
             wait_phase_cleanup(full1 + u % N1, (u / N1) & 1, kCleanupPolls);
         for (int u = max(0, issued2 - N2); u < issued2; u++)
@@ -183,24 +182,26 @@ template <int N1, int N2, int NS> struct Bars {
     }
 };
 
-// One CTA's loads: the fixed tiles, then the blocks of both rings in the order in which
-// the products need them.  coords(u, h, row): head and first row of block u.
-template <int D, typename B, int N1, int N2, typename Coords>
-__device__ __forceinline__ void load_all(uint8_t *sm, B *bar, const CUtensorMap *fix_a,
-                                         const CUtensorMap *fix_b, int fix_row, int fix_head,
-                                         const CUtensorMap *ring1, const CUtensorMap *ring2, int b,
-                                         int n, const Coords &coords, const WaitCtx &w, int lane) {
-    using L = BwdLayout<D>;
-    constexpr int PN = D / 64;
-    if (lane == 0) {
-        mbar_expect_tx(&bar->fix_full, 2 * L::kTile);
-        for (int pn = 0; pn < PN; pn++) {
-            tma_load_4d(sm + L::kFix + pn * kPanel, fix_a, pn * 64, fix_row, fix_head, b,
-                        &bar->fix_full);
-            tma_load_4d(sm + L::kFix + L::kTile + pn * kPanel, fix_b, pn * 64, fix_row, fix_head, b,
-                        &bar->fix_full);
-        }
+// A role of one thread of a warp: waits and issues until body() is done or gives up,
+// then waits for its own products, which the CTA's exit must not overtake.
+template <typename Body>
+__device__ __forceinline__ void issuer(uint64_t *done, const Body &body) {
+    if (elect_one()) {
+        body();
+        mma_commit(done);
+        wait_phase_cleanup(done, 0, kCleanupPolls);
     }
+    __syncwarp();
+}
+
+// One CTA's loads of the blocks of both rings, in the order in which the products need
+// them.  coords(u, h, row): head and first row of block u.
+template <int D, typename L, int N1, int N2, typename Coords>
+__device__ __forceinline__ void load_blocks(uint8_t *sm, Bars<N1, N2> *bar,
+                                            const CUtensorMap *ring1, const CUtensorMap *ring2,
+                                            int b, int n, const Coords &coords, const WaitCtx &w,
+                                            int lane) {
+    constexpr int PN = D / 64;
     int issued1 = 0, issued2 = 0;
     Slot<N1> r1;
     Slot<N2> r2;
@@ -238,18 +239,17 @@ __device__ __forceinline__ bool base_aligned(const uint8_t *sm, int *status) {
 }
 
 // ---------------------------------------------------------------- dk, dv
-// Tensor memory, half h: S^T at 64 h (P^T over its first 32 columns), dP^T at 128 + 64 h
-// (dS^T over it); dV at 256, dK at 384.
+// Tensor memory: S^T of half h at 64 h, dP^T at 128 + 64 h, dV at 256, dK at 384.  P^T and
+// dS^T of each 32 columns lie over the first 16 of them.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDo, BwdArgs a) {
-    using L = BwdLayout<D>;
-    constexpr int PN = D / 64, N1 = 5, N2 = 5;
-    static_assert(N1 + N2 == L::kBlocks, "ring slots");
-    using B = Bars<N1, N2, 2>;
+    constexpr int PN = D / 64, N1 = kDkvRing1, N2 = kDkvRing2;
+    using L = BwdLayout<D, 2, N1, N2>;
+    using B = Bars<N1, N2>;
     static_assert(sizeof(B) <= 512, "barriers");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = smem_raw;
@@ -276,7 +276,7 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         return;
     }
     if (threadIdx.x == 0) bar->init();
-    if (warp == 9) tmem_alloc(&bar->tmem_slot, 512);
+    if (warp == kIssueWarp) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -287,188 +287,200 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         row = (t0 + u % nt) * 64;
     };
 
-    if (warp == 8) {
-        load_all<D, B, N1, N2>(sm, bar, &tmK, &tmV, j0, hk, &tmQ, &tmDo, b, n, coords, w, lane);
-    } else if (warp == 9) {
-        if (elect_one()) {
-        // ---------------- products
-        constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kBlockDesc = L::kBlock >> 4;
-        const uint32_t ring = smem_u32(sm + L::kRing);
-        const uint64_t dK = smem_desc_sw128(smem_u32(sm + L::kFix), 16, 1024);
-        const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kFix + L::kTile), 16, 1024);
-        const uint64_t dQ = smem_desc_sw128(ring, 16, 1024);
-        const uint64_t dO = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
-        const uint64_t dQt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
-        const uint64_t dOt = smem_desc_sw128(ring + N1 * L::kBlock, L::kBlockPanel, 1024);
-        Slot<N1> next_s, cur_q;    // of the next S; of block u
-        Slot<N2> next_dp, cur_do;
-        auto issue_s = [&](int h) -> bool {
-            if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
-            tc_fence_after();
-            mma_head<D, 64>(tmem + 64 * h, dK, dQ + next_s.s * kBlockDesc, idS);
-            mma_commit(bar->s_full + h);
-            next_s.next();
-            return true;
-        };
-        auto issue_dp = [&](int h) -> bool {
-            if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
-            tc_fence_after();
-            mma_head<D, 64>(tmem + 128 + 64 * h, dV, dO + next_dp.s * kBlockDesc, idS);
-            mma_commit(bar->dp_full + h);
-            next_dp.next();
-            return true;
-        };
-        bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
-        for (int u = 0; ok && u < 2 && u < n; u++) ok = issue_s(u) && issue_dp(u);
-        for (int u = 0; ok && u < n; u++) {
-            const int h = u & 1, ph = (u >> 1) & 1;
-            if (!(ok = spin_phase(bar->p_full + h, ph, w))) break;
-            tc_fence_after();
-            mma_block64(tmem + 256, tmem + 64 * h, dOt + cur_do.s * kBlockDesc, idO, u > 0 ? 1u : 0u);
-            mma_commit(bar->empty2 + cur_do.s);
-            cur_do.next();
-            if (u + 2 < n && !(ok = issue_s(h))) break;
-            if (!(ok = spin_phase(bar->ds_full + h, ph, w))) break;
-            tc_fence_after();
-            mma_block64(tmem + 384, tmem + 128 + 64 * h, dQt + cur_q.s * kBlockDesc, idO,
-                        u > 0 ? 1u : 0u);
-            mma_commit(bar->empty1 + cur_q.s);
-            cur_q.next();
-            if (u + 2 < n) ok = issue_dp(h);
+    constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
+    constexpr uint32_t kBlockDesc = L::kBlock >> 4;
+    const uint32_t ring = smem_u32(sm + L::kRing);
+    const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kTile), 16, 1024);
+    const uint64_t dQ = smem_desc_sw128(ring, 16, 1024);
+    const uint64_t dO = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
+    const uint64_t dQt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
+    const uint64_t dOt = smem_desc_sw128(ring + N1 * L::kBlock, L::kBlockPanel, 1024);
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            mbar_expect_tx(&bar->fix_full, 2 * L::kTile);
+            for (int pn = 0; pn < PN; pn++) {
+                tma_load_4d(sm + pn * kPanel, &tmK, pn * 64, j0, hk, b, &bar->fix_full);
+                tma_load_4d(sm + L::kTile + pn * kPanel, &tmV, pn * 64, j0, hk, b, &bar->fix_full);
+            }
         }
-        mma_commit(&bar->acc_full);
-        wait_phase_cleanup(&bar->acc_full, 0, kCleanupPolls);
-        }
-        __syncwarp();
-    } else if (warp == 10) {
-        // ---------------- lse (in log2 units) and delta of each block's queries, negated
+        load_blocks<D, L>(sm, bar, &tmQ, &tmDo, b, n, coords, w, lane);
+        if (lane == 0) wait_phase_cleanup(&bar->fix_full, 0, kCleanupPolls);
+    } else if (warp == kStatsWarp) {
+        // -lse (in log2 units) and -delta of each block's queries.  (A warp of its own: in
+        // the loading warp, its global reads held up the copies, 722 -> 915 us.)
+        Slot<N1> cur;
         for (int u = 0; u < n; u++) {
-            if (u >= N1 && !wait_warp(bar->empty1 + u % N1, (u / N1 - 1) & 1, w)) break;
             int h, i0;
             coords(u, h, i0);
-            const int64_t row = ((int64_t)b * p.H + h) * p.Nq;
-            float *dst = stats + u % N1 * 128;
+            const int64_t at = ((int64_t)b * p.H + h) * p.Nq + i0;
+            float2 st[2];
 #pragma unroll
-            for (int x = lane; x < 64; x += 32) {
-                const bool in = i0 + x < p.Nq;
-                dst[x] = in ? -a.lse[row + i0 + x] * kLog2e : 0.f;
-                dst[64 + x] = in ? -a.delta[row + i0 + x] : 0.f;
+            for (int x = 0; x < 2; x++) {
+                const int i = lane + 32 * x;
+                st[x] = i0 + i < p.Nq ? make_float2(-a.lse[at + i] * kLog2e, -a.delta[at + i])
+                                      : make_float2(0.f, 0.f);
             }
-            mbar_arrive_warp(bar->stats_full + u % N1);
+            if (u >= N1 && !wait_warp(bar->empty1 + cur.s, cur.ph ^ 1, w)) break;
+            float *dst = stats + cur.s * 128;
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                dst[lane + 32 * x] = st[x].x;
+                dst[64 + lane + 32 * x] = st[x].y;
+            }
+            mbar_arrive_warp(bar->stats_full + cur.s);
+            cur.next();
         }
-    } else if (warp < 8) {
-        // ---------------- elementwise: key row j, the queries of the half's blocks
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane, j = j0 + row;
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
+    } else if (warp == kIssueWarp) {
+        issuer(&bar->done, [&]() {
+            if ((a.stall && !spin_phase(&bar->stall_bar, 0, w)) || !spin_phase(&bar->fix_full, 0, w))
+                return;
+            Slot<N1> next_s, cur_q;    // of the next S; of block u
+            Slot<N2> next_dp, cur_do;
+            auto issue_s = [&](int h) -> bool {
+                if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
+                tc_fence_after();
+                mma_head<D, 64>(tmem + 64 * h, dK, dQ + next_s.s * kBlockDesc, idS);
+                mma_commit(bar->s_full + h);
+                next_s.next();
+                return true;
+            };
+            auto issue_dp = [&](int h) -> bool {
+                if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
+                tc_fence_after();
+                mma_head<D, 64>(tmem + 128 + 64 * h, dV, dO + next_dp.s * kBlockDesc, idS);
+                mma_commit(bar->dp_full + h);
+                next_dp.next();
+                return true;
+            };
+            for (int u = 0; u < 2 && u < n; u++)
+                if (!issue_s(u) || !issue_dp(u)) return;
+            for (int u = 0; u < n; u++) {
+                const int h = u & 1, ph = (u >> 1) & 1;
+                if (!spin_phase(bar->p_full + h, ph, w)) return;
+                tc_fence_after();
+                mma_block64<32>(tmem + 256, tmem + 64 * h, dOt + cur_do.s * kBlockDesc, idO, u > 0);
+                mma_commit(bar->empty2 + cur_do.s);   // (dP(u), issued before, read it too)
+                cur_do.next();
+                if (u + 2 < n && !issue_s(h)) return;
+                if (!spin_phase(bar->ds_full + h, ph, w)) return;
+                tc_fence_after();
+                mma_block64<32>(tmem + 384, tmem + 128 + 64 * h, dQt + cur_q.s * kBlockDesc, idO, u > 0);
+                mma_commit(bar->empty1 + cur_q.s);
+                cur_q.next();
+                if (u + 2 < n && !issue_dp(h)) return;
+            }
+        });
+    } else if (warp < kLoadWarp) {
+        // ---------------- elementwise: key row j, 32 queries of each of the half's blocks
+        const int half = warp >> 3, part = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        const int j = j0 + row;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lanes + 64 * half, td = ts + 128;
         int ilo, ihi, rfirst, rlast;
         query_rows(p, seq, j, j + 1, ilo, ihi);   // the queries that see this key
         real_rows(p, seq, 0, p.Nq, rfirst, rlast);
+        const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
         bool ok = true;
+        int x0 = half % nt;   // block of its head
         for (int u = half; u < n; u += 2) {
-            const int ph = (u >> 1) & 1, s1 = u % N1, s2 = u % N2, c0 = (t0 + u % nt) * 64;
-            const float *nl = stats + s1 * 128, *nd = nl + 64;
-            if (!(ok = wait_warp(bar->s_full + half, ph, w) &&
-                       wait_warp(bar->stats_full + s1, (u / N1) & 1, w)))
+            const int ph = (u >> 1) & 1, s1 = u % N1, c0 = (t0 + x0) * 64 + 32 * part;
+            x0 += 2;
+            while (x0 >= nt) x0 -= nt;
+            const float *nl = stats + s1 * 128 + 32 * part, *nd = nl + 64;
+            const bool all = __all_sync(0xffffffffu, c0 >= ilo && c0 + 32 <= ihi);
+            const uint32_t see = below(ihi - c0) & ~below(ilo - c0);
+            if (!(ok = wait_warp(bar->stats_full + s1, (u / N1) & 1, w) &&
+                       wait_warp(bar->s_full + half, ph, w)))
                 break;
             tc_fence_after();
-            float x[64];
-            tmem_ld32f(tl, &x[0]);
-            tmem_ld32f(tl + 32, &x[32]);
+            float x[32];
+            tmem_ld32f(ts + 32 * part, x);
             tmem_wait_ld();
-            const bool all = __all_sync(0xffffffffu, c0 >= ilo && c0 + 64 <= ihi);
-            const uint64_t see = below(ihi - c0) & ~below(ilo - c0);
-            probabilities(x, p.scale_log2, nl, all, see);
-            uint32_t pk[32];
 #pragma unroll
-            for (int k = 0; k < 32; k++) pk[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
-            tmem_st32(tl, pk);
-            if (c0 < rfirst || (rlast < p.Nq && c0 + 64 > rlast)) {
+            for (int k = 0; k < 32; k += 4) {
+                const ulonglong2 n2 = *reinterpret_cast<const ulonglong2 *>(nl + k);
+                f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), c2, n2.x), x[k], x[k + 1]);
+                f2_unpack(f2_fma(f2_pack(x[k + 2], x[k + 3]), c2, n2.y), x[k + 2], x[k + 3]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) x[k + e] = fast_exp2(x[k + e]);
+            }
+            if (!all) keep_seen(x, see);
+            pack_to_tmem(ts + 32 * part, x);   // over the part's own columns of S
+            if (c0 < rfirst || (rlast < p.Nq && c0 + 32 > rlast)) {
                 // rows that are not real may hold anything, and 0 * NaN is NaN: they become
                 // zeros before the products over the queries
+                const int s2 = u % N2;
                 if (!(ok = wait_warp(bar->full2 + s2, (u / N2) & 1, w))) break;
-                const int za = min(max(rfirst - c0, 0), 64), zb = min(max(rlast - c0, 0), 64);
+                const int za = min(max(rfirst - c0, 0), 32), zb = min(max(rlast - c0, 0), 32);
                 for (int x2 = 0; x2 < 2; x2++) {
-                    uint8_t *blk = sm + L::kRing + (x2 ? N1 + s2 : s1) * L::kBlock;
+                    uint8_t *blk = sm + L::kRing + (x2 ? N1 + s2 : s1) * L::kBlock + part * 32 * 128;
                     zero_rows(blk, 0, za, PN, L::kBlockPanel, row, 128);
-                    zero_rows(blk, zb, 64, PN, L::kBlockPanel, row, 128);
+                    zero_rows(blk, zb, 32, PN, L::kBlockPanel, row, 128);
                 }
                 fence_proxy_async_smem();
             }
-            tmem_wait_st();
             tc_fence_before();
             mbar_arrive_warp(bar->p_full + half);
             if (!(ok = wait_warp(bar->dp_full + half, ph, w))) break;
             tc_fence_after();
+            float y[32];
+            tmem_ld32f(td + 32 * part, y);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                float y[32];
-                tmem_ld32f(tl + 128 + c, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(nd + c + k);
-                    const uint64_t e = f2_mul(f2_add(f2_pack(y[k], y[k + 1]), d2.x),
-                                              f2_pack(x[c + k], x[c + k + 1]));
-                    const uint64_t f = f2_mul(f2_add(f2_pack(y[k + 2], y[k + 3]), d2.y),
-                                              f2_pack(x[c + k + 2], x[c + k + 3]));
-                    f2_unpack(e, y[k], y[k + 1]);
-                    f2_unpack(f, y[k + 2], y[k + 3]);
-                }
-                if (!all) {
-                    const uint32_t s = (uint32_t)(see >> c);
-#pragma unroll
-                    for (int k = 0; k < 32; k++) y[k] = (s >> k) & 1 ? y[k] : 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < 16; k++) pk[c / 2 + k] = pack_bf16(y[2 * k], y[2 * k + 1]);
+            for (int k = 0; k < 32; k += 4) {
+                const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(nd + k);
+                f2_unpack(f2_mul(f2_add(f2_pack(y[k], y[k + 1]), d2.x), f2_pack(x[k], x[k + 1])),
+                          y[k], y[k + 1]);
+                f2_unpack(f2_mul(f2_add(f2_pack(y[k + 2], y[k + 3]), d2.y),
+                                 f2_pack(x[k + 2], x[k + 3])),
+                          y[k + 2], y[k + 3]);
             }
-            tmem_st32(tl + 128, pk);
-            tmem_wait_st();
+            if (!all) keep_seen(y, see);
+            pack_to_tmem(td + 32 * part, y);
             tc_fence_before();
             mbar_arrive_warp(bar->ds_full + half);
         }
-        if (ok && wait_warp(&bar->acc_full, 0, w)) {
+        if (ok && wait_warp(&bar->done, 0, w)) {
             tc_fence_after();
-            const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (D / 2);
-            const int64_t x = half * (D / 2);
+            // a quarter of the head's columns, of dV and dK, for each group of four warps
+            constexpr int W = D / 4;
+            const int64_t x = (half * 2 + part) * W;
             const bool real = j < p.Nk;
-            store_row<D / 2>(ta + 256,
-                             a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
-                             p.d - (int)x, real);
-            store_row<D / 2>(ta + 384,
-                             a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x,
-                             p.scale, p.d - (int)x, real);
+            store_row<W>(lanes + 256 + x,
+                         a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
+                         p.d - (int)x, real);
+            store_row<W>(lanes + 384 + x,
+                         a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x, p.scale,
+                         p.d - (int)x, real);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssueWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
 // ---------------------------------------------------------------- dq
-// Tensor memory: S of block u at 64 (u % 4) (dS over its first 32 columns), dP of half h
-// at 256 + 64 h, dQ at 384.
+// Tensor memory: S of half h at 64 h, dP at 128 + 64 h (dS of each 32 columns over the
+// first 16), dQ at 256, Q at 384, dO at 448.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
-                    const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmDo, BwdArgs a) {
-    using L = BwdLayout<D>;
-    // a key block stays from S(u) to dQ(u), three blocks; a value block for dP(u) alone
-    constexpr int PN = D / 64, N1 = 6, N2 = 4;
-    static_assert(N1 + N2 == L::kBlocks, "ring slots");
-    using B = Bars<N1, N2, 4>;
+tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, BwdArgs a) {
+    // a key block stays from S(u) to dQ(u), a value block for dP(u) alone
+    constexpr int PN = D / 64, N1 = kDqRing1, N2 = kDqRing2;
+    using L = BwdLayout<D, 0, N1, N2>;
+    using B = Bars<N1, N2>;
     static_assert(sizeof(B) <= 512, "barriers");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = smem_raw;
     if (!base_aligned(sm, a.status)) return;
     B *bar = reinterpret_cast<B *>(sm + L::kBar);
-    float *half_delta = reinterpret_cast<float *>(sm + L::kStats);   // [2 halves][128]
+    float *part_delta = reinterpret_cast<float *>(sm + L::kStats);   // [half, part][128]
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the last tiles first: they see the most keys under a causal mask
@@ -487,70 +499,82 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         return;
     }
     if (threadIdx.x == 0) bar->init();
-    if (warp == 9) tmem_alloc(&bar->tmem_slot, 512);
+    if (warp == kIssueWarp) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_slot;
     const WaitCtx w{a.limit, a.status, &bar->abort_flag};
 
-    if (warp == 8) {
+    constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
+    constexpr uint32_t kBlockDesc = L::kBlock >> 4;
+    const uint32_t ring = smem_u32(sm + L::kRing);
+    const uint64_t dK = smem_desc_sw128(ring, 16, 1024);
+    const uint64_t dV = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
+    const uint64_t dKt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
+
+    if (warp == kLoadWarp) {
         auto coords = [&](int u, int &head, int &row) {
             head = h / p.G;
             row = kt.tile(u % nt) * 64;
         };
-        load_all<D, B, N1, N2>(sm, bar, &tmQ, &tmDo, i0, h, &tmK, &tmV, b, n, coords, w, lane);
-    } else if (warp == 9) {
-        if (elect_one()) {
-        constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kBlockDesc = L::kBlock >> 4;
-        const uint32_t ring = smem_u32(sm + L::kRing);
-        const uint64_t dQ = smem_desc_sw128(smem_u32(sm + L::kFix), 16, 1024);
-        const uint64_t dO = smem_desc_sw128(smem_u32(sm + L::kFix + L::kTile), 16, 1024);
-        const uint64_t dK = smem_desc_sw128(ring, 16, 1024);
-        const uint64_t dV = smem_desc_sw128(ring + N1 * L::kBlock, 16, 1024);
-        const uint64_t dKt = smem_desc_sw128(ring, L::kBlockPanel, 1024);
-        Slot<N1> next_s, cur_k;    // of the next S; of block u
-        Slot<N2> next_dp;
-        auto issue_s = [&](int u) -> bool {
-            if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
-            tc_fence_after();
-            mma_head<D, 64>(tmem + 64 * (u & 3), dQ, dK + next_s.s * kBlockDesc, idS);
-            mma_commit(bar->s_full + (u & 3));
-            next_s.next();
-            return true;
-        };
-        auto issue_dp = [&](int u) -> bool {
-            if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
-            tc_fence_after();
-            mma_head<D, 64>(tmem + 256 + 64 * (u & 1), dO, dV + next_dp.s * kBlockDesc, idS);
-            mma_commit(bar->dp_full + (u & 1));
-            mma_commit(bar->empty2 + next_dp.s);
-            next_dp.next();
-            return true;
-        };
-        bool ok = (!a.stall || spin_phase(&bar->stall_bar, 0, w)) && spin_phase(&bar->fix_full, 0, w);
-        for (int u = 0; ok && u < 2 && u < n; u++) ok = issue_s(u) && issue_dp(u);
-        if (ok && n > 2) ok = issue_s(2);
-        for (int u = 0; ok && u < n; u++) {
-            // dS(u) is written: the half's dP columns have been read too
-            if (!(ok = spin_phase(bar->ds_full + (u & 1), (u >> 1) & 1, w))) break;
-            if (u + 2 < n && !(ok = issue_dp(u))) break;   // of block u + 2
-            tc_fence_after();
-            if (u >= n - nt)
-                mma_block64(tmem + 384, tmem + 64 * (u & 3), dKt + cur_k.s * kBlockDesc, idO,
-                            u > n - nt ? 1u : 0u);
-            mma_commit(bar->empty1 + cur_k.s);
-            cur_k.next();
-            if (u + 3 < n) ok = issue_s(u + 3);
+        load_blocks<D, L>(sm, bar, &tmK, &tmV, b, n, coords, w, lane);
+    } else if (warp == kIssueWarp) {
+        issuer(&bar->done, [&]() {
+            if ((a.stall && !spin_phase(&bar->stall_bar, 0, w)) || !spin_phase(&bar->tmem_full, 0, w))
+                return;
+            Slot<N1> next_s, cur_k;    // of the next S; of block u
+            Slot<N2> next_dp;
+            auto issue_s = [&](int h) -> bool {
+                if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
+                tc_fence_after();
+                mma_head_ts<D, 64>(tmem + 64 * h, tmem + 384, dK + next_s.s * kBlockDesc, idS);
+                mma_commit(bar->s_full + h);
+                next_s.next();
+                return true;
+            };
+            auto issue_dp = [&](int h) -> bool {
+                if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
+                tc_fence_after();
+                mma_head_ts<D, 64>(tmem + 128 + 64 * h, tmem + 448, dV + next_dp.s * kBlockDesc, idS);
+                mma_commit(bar->dp_full + h);
+                mma_commit(bar->empty2 + next_dp.s);
+                next_dp.next();
+                return true;
+            };
+            for (int u = 0; u < 2 && u < n; u++)
+                if (!issue_s(u) || !issue_dp(u)) return;
+            for (int v = 0; v <= n; v++) {
+                // S(v + 2) once S(v) is read, which comes before dS(v - 1) is written
+                if (v + 2 < n && (!spin_phase(bar->s_free + (v & 1), (v >> 1) & 1, w) ||
+                                  !issue_s(v & 1)))
+                    return;
+                if (v == 0) continue;
+                const int u = v - 1, h = u & 1;
+                if (!spin_phase(bar->ds_full + h, (u >> 1) & 1, w)) return;
+                tc_fence_after();
+                if (u >= n - nt)
+                    mma_block64<32>(tmem + 256, tmem + 128 + 64 * h, dKt + cur_k.s * kBlockDesc, idO,
+                                    u > n - nt);
+                mma_commit(bar->empty1 + cur_k.s);
+                cur_k.next();
+                if (u + 2 < n && !issue_dp(h)) return;
+            }
+        });
+    } else if (warp < kLoadWarp) {
+        // ---------------- elementwise: query row i, 32 keys of each of the half's blocks
+        const int half = warp >> 3, part = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        const int i = i0 + row;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lanes + 64 * half + 32 * part, td = ts + 128;
+        if (half == 0) {   // Q's rows to tensor memory (warps 0-3) and dO's (warps 4-7)
+            row_to_tmem<D>(lanes + 384 + 64 * part,
+                           part ? a.dout + b * a.g.dout.batch + h * a.g.dout.head + i * a.g.dout.token
+                                : a.q + b * p.q.batch + h * p.q.head + i * p.q.token,
+                           p.d, i < p.Nq);
+            tc_fence_before();
+            mbar_arrive_warp(&bar->tmem_full);
         }
-        mma_commit(&bar->acc_full);
-        wait_phase_cleanup(&bar->acc_full, 0, kCleanupPolls);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane, i = i0 + row;
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const RowKeys rk = row_keys(p, seq, i);
         const int64_t at = ((int64_t)b * p.H + h) * p.Nq + i;
         const bool real = rk.hi > 0;
@@ -558,100 +582,81 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
         float nd = real && n == nt ? -a.delta[at] : 0.f;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
         bool ok = true, summed = n == nt;
-        // (a group without a block of its own still joins delta)
+        // (warps without a block of their own still join delta)
         auto join_delta = [&]() -> bool {
-            half_delta[half * 128 + row] = nd;
+            part_delta[(warp >> 2) * 128 + row] = nd;
             mbar_arrive_warp(&bar->delta_bar);
             if (!wait_warp(&bar->delta_bar, 0, w)) return false;
-            nd = half_delta[row] + half_delta[128 + row];
-            if (half == 0 && real) a.delta[at] = -nd;
+            nd = (part_delta[row] + part_delta[128 + row]) +
+                 (part_delta[256 + row] + part_delta[384 + row]);
+            if (warp < 4 && real) a.delta[at] = -nd;
             summed = true;
             return true;
         };
         for (int u = half; u < n; u += 2) {
-            const int ph = (u >> 1) & 1, c0 = kt.tile(u % nt) * 64;
-            if (!summed && u >= n - nt && !(ok = join_delta())) break;
-            if (!(ok = wait_warp(bar->s_full + (u & 3), (u >> 2) & 1, w))) break;
-            tc_fence_after();
-            const uint32_t ts = tl + 64 * (u & 3), td = tl + 256 + 64 * half;
-            float x[64];
-            tmem_ld32f(ts, &x[0]);
-            tmem_ld32f(ts + 32, &x[32]);
-            tmem_wait_ld();
-            const bool all = __all_sync(0xffffffffu, c0 + 64 <= rk.hi &&
-                                                         (c0 >= rk.lo || c0 + 64 <= rk.sink));
-            const uint64_t see =
+            const int ph = (u >> 1) & 1, c0 = kt.tile(u < nt ? u : u - nt) * 64 + 32 * part;
+            const bool all = __all_sync(0xffffffffu, c0 + 32 <= rk.hi &&
+                                                         (c0 >= rk.lo || c0 + 32 <= rk.sink));
+            const uint32_t see =
                 below(rk.hi - c0) & (~below(rk.lo - c0) | below(rk.sink - c0));
+            if (!summed && u >= n - nt && !(ok = join_delta())) break;
+            if (!(ok = wait_warp(bar->s_full + half, ph, w))) break;
+            tc_fence_after();
+            float x[32];
+            tmem_ld32f(ts, x);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive_warp(bar->s_free + half);
 #pragma unroll
-            for (int k = 0; k < 64; k += 2) {
+            for (int k = 0; k < 32; k += 2) {
                 float lo, hi;
                 f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), c2, nl2), lo, hi);
                 x[k] = fast_exp2(lo);
                 x[k + 1] = fast_exp2(hi);
             }
-            if (c0 + 64 > seq.len) {
+            if (c0 + 32 > seq.len) {
                 // keys past the sequence may hold anything, and 0 * NaN is NaN: they become
                 // zeros before the product over the keys (S of this block is done with them)
-                zero_rows(sm + L::kRing + u % N1 * L::kBlock, max(0, seq.len - c0), 64, PN,
-                          L::kBlockPanel, row, 128);
+                zero_rows(sm + L::kRing + u % N1 * L::kBlock + part * 32 * 128, max(0, seq.len - c0),
+                          32, PN, L::kBlockPanel, row, 128);
                 fence_proxy_async_smem();
             }
             if (!(ok = wait_warp(bar->dp_full + half, ph, w))) break;
             tc_fence_after();
+            float y[32];
+            tmem_ld32f(td, y);
+            tmem_wait_ld();
             if (u < n - nt) {
-                // this group's part of delta = sum P dP
+                // this part of delta = sum P dP
                 float sum = 0.f;
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float y[32];
-                    tmem_ld32f(td + c, y);
-                    tmem_wait_ld();
-                    const uint32_t s = (uint32_t)(see >> c);
-#pragma unroll
-                    for (int k = 0; k < 32; k++)
-                        sum = fmaf((s >> k) & 1 ? x[c + k] : 0.f, (s >> k) & 1 ? y[k] : 0.f, sum);
-                }
+                for (int k = 0; k < 32; k++)
+                    sum = fmaf((see >> k) & 1 ? x[k] : 0.f, (see >> k) & 1 ? y[k] : 0.f, sum);
                 nd -= sum;
-                tc_fence_before();
-                mbar_arrive_warp(bar->ds_full + half);
-                continue;
-            }
-            const uint64_t nd2 = f2_pack(nd, nd);
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                float y[32];
-                tmem_ld32f(td + c, y);
-                tmem_wait_ld();
+            } else {
+                const uint64_t nd2 = f2_pack(nd, nd);
 #pragma unroll
                 for (int k = 0; k < 32; k += 2)
-                    f2_unpack(f2_mul(f2_add(f2_pack(y[k], y[k + 1]), nd2),
-                                     f2_pack(x[c + k], x[c + k + 1])),
+                    f2_unpack(f2_mul(f2_add(f2_pack(y[k], y[k + 1]), nd2), f2_pack(x[k], x[k + 1])),
                               y[k], y[k + 1]);
-                if (!all) {
-                    const uint32_t s = (uint32_t)(see >> c);
-#pragma unroll
-                    for (int k = 0; k < 32; k++) y[k] = (s >> k) & 1 ? y[k] : 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < 16; k++) pk[c / 2 + k] = pack_bf16(y[2 * k], y[2 * k + 1]);
+                if (!all) keep_seen(y, see);
+                pack_to_tmem(td, y);
             }
-            tmem_st32(ts, pk);
-            tmem_wait_st();
             tc_fence_before();
             mbar_arrive_warp(bar->ds_full + half);
         }
         if (ok && !summed) ok = join_delta();
-        if (ok && wait_warp(&bar->acc_full, 0, w)) {
+        if (ok && wait_warp(&bar->done, 0, w)) {
             tc_fence_after();
-            const int x = half * (D / 2);
-            store_row<D / 2>(tl + 384 + x, dq + (int64_t)i * a.g.dq.token + x, p.scale, p.d - x,
-                             i < p.Nq);
+            constexpr int W = D / 4;   // columns of dQ for each group of four warps
+            const int x = (warp >> 2) * W;
+            store_row<W>(lanes + 256 + x, dq + (int64_t)i * a.g.dq.token + x, p.scale, p.d - x,
+                         i < p.Nq);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssueWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -661,27 +666,26 @@ template <int D>
 cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
                    const void *v, const void *dout, const BwdArgs &a, cudaStream_t stream) {
     // the fixed tiles have 128 rows, the streamed blocks 64
-    CUtensorMap q128, k128, v128, d128, q64, k64, v64, d64;
-    if (!map_tokens(&q128, q, p.q, p.B, p.H, p.Nq, p.d, 128) ||
-        !map_tokens(&q64, q, p.q, p.B, p.H, p.Nq, p.d, 64) ||
-        !map_tokens(&d128, dout, g.dout, p.B, p.H, p.Nq, p.d, 128) ||
+    CUtensorMap k128, v128, q64, k64, v64, d64;
+    if (!map_tokens(&q64, q, p.q, p.B, p.H, p.Nq, p.d, 64) ||
         !map_tokens(&d64, dout, g.dout, p.B, p.H, p.Nq, p.d, 64) ||
         !map_tokens(&k128, k, p.k, p.B, p.Hkv, p.Nk, p.d, 128) ||
         !map_tokens(&k64, k, p.k, p.B, p.Hkv, p.Nk, p.d, 64) ||
         !map_tokens(&v128, v, p.v, p.B, p.Hkv, p.Nk, p.d, 128) ||
         !map_tokens(&v64, v, p.v, p.B, p.Hkv, p.Nk, p.d, 64))
         return cudaErrorInvalidValue;
-    constexpr uint32_t smem = BwdLayout<D>::kSmem;
-    cudaError_t e = tcs::set_smem(tc_window_dkv_kernel<D>, smem);
-    if (e == cudaSuccess) e = tcs::set_smem(tc_window_dq_kernel<D>, smem);
+    constexpr uint32_t smem_dkv = BwdLayout<D, 2, kDkvRing1, kDkvRing2>::kSmem;
+    constexpr uint32_t smem_dq = BwdLayout<D, 0, kDqRing1, kDqRing2>::kSmem;
+    cudaError_t e = tcs::set_smem(tc_window_dkv_kernel<D>, smem_dkv);
+    if (e == cudaSuccess) e = tcs::set_smem(tc_window_dq_kernel<D>, smem_dq);
     if (e != cudaSuccess) return e;
     const unsigned gk = (unsigned)p.B * p.Hkv * ((p.Nk + 127) / 128);
     const unsigned gq = (unsigned)p.B * p.H * ((p.Nq + 127) / 128);
     // dq first: it completes delta
-    tc_window_dq_kernel<D><<<gq, kThreads, smem, stream>>>(q128, k64, v64, d128, a);
+    tc_window_dq_kernel<D><<<gq, kThreads, smem_dq, stream>>>(k64, v64, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    tc_window_dkv_kernel<D><<<gk, kThreads, smem, stream>>>(q64, k128, v128, d64, a);
+    tc_window_dkv_kernel<D><<<gk, kThreads, smem_dkv, stream>>>(q64, k128, v128, d64, a);
     return cudaGetLastError();
 }
 
@@ -696,6 +700,8 @@ cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, c
     a.g = g;
     a.lse = lse;
     a.delta = delta;
+    a.q = (const __nv_bfloat16 *)q;
+    a.dout = (const __nv_bfloat16 *)dout;
     a.dq = (__nv_bfloat16 *)dq;
     a.dk = (__nv_bfloat16 *)dk;
     a.dv = (__nv_bfloat16 *)dv;

@@ -271,7 +271,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 // the first PV of a problem overwrites O: the epilogue must have read it
                 if (c.i == 0 && c.pc > 0 && !spin_phase(o_free + t, (c.pc - 1) & 1, w)) return false;
                 tc_fence_after();
-                mma_block64(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
+                mma_block64<16>(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
                              c.i > 0 ? 1u : 0u);
                 mma_commit(pv_done + t);
                 const bool last = c.i == c.pr.nh - 1;
