@@ -46,8 +46,8 @@ namespace win {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 608;
-constexpr int kLoadWarp = 16, kIssueWarp = 17, kStatsWarp = 18;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kIssueWarp = 17, kIssueWarp2 = 18, kStatsWarp = 19;
 constexpr int kExactBlocks = 6;
 constexpr int kDkvRing1 = 5, kDkvRing2 = 5, kDqRing1 = 8, kDqRing2 = 6;
 
@@ -132,7 +132,8 @@ template <int N> struct Slot {
 };
 
 // Barriers of one CTA.  N1, N2: blocks of the two rings.
-template <int N1, int N2> struct Bars {
+// READERS: issuers that read a block of the second ring.
+template <int N1, int N2, int READERS> struct Bars {
     uint64_t fix_full;                  // the fixed tiles
     uint64_t tmem_full;                 // Q and dO in tensor memory (dq), 8 warps
     uint64_t full1[N1], empty1[N1];     // Q (dkv) or K (dq)
@@ -142,7 +143,7 @@ template <int N1, int N2> struct Bars {
     uint64_t s_free[2];                 // S is read (dq), the half's 8 warps
     uint64_t p_full[2], ds_full[2];     // the half's 8 warps
     uint64_t delta_bar;                 // the parts of delta (dq), 16 warps, once
-    uint64_t done;                      // the last products
+    uint64_t done[2];                   // each issuer's last products
     uint64_t stall_bar;                 // never completed (fault injection)
     uint32_t tmem_slot;
     int abort_flag;
@@ -157,7 +158,7 @@ template <int N1, int N2> struct Bars {
         }
         for (int i = 0; i < N2; i++) {
             mbar_init(full2 + i, 1);
-            mbar_init(empty2 + i, 1);
+            mbar_init(empty2 + i, READERS);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(s_full + i, 1);
@@ -167,7 +168,8 @@ template <int N1, int N2> struct Bars {
             mbar_init(ds_full + i, 8);
         }
         mbar_init(&delta_bar, 16);
-        mbar_init(&done, 1);
+        mbar_init(done, 1);
+        mbar_init(done + 1, 1);
         mbar_init(&stall_bar, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -196,8 +198,8 @@ __device__ __forceinline__ void issuer(uint64_t *done, const Body &body) {
 
 // One CTA's loads of the blocks of both rings, in the order in which the products need
 // them.  coords(u, h, row): head and first row of block u.
-template <int D, typename L, int N1, int N2, typename Coords>
-__device__ __forceinline__ void load_blocks(uint8_t *sm, Bars<N1, N2> *bar,
+template <int D, typename L, int N1, int N2, int RD, typename Coords>
+__device__ __forceinline__ void load_blocks(uint8_t *sm, Bars<N1, N2, RD> *bar,
                                             const CUtensorMap *ring1, const CUtensorMap *ring2,
                                             int b, int n, const Coords &coords, const WaitCtx &w,
                                             int lane) {
@@ -249,7 +251,7 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmDo, BwdArgs a) {
     constexpr int PN = D / 64, N1 = kDkvRing1, N2 = kDkvRing2;
     using L = BwdLayout<D, 2, N1, N2>;
-    using B = Bars<N1, N2>;
+    using B = Bars<N1, N2, 2>;
     static_assert(sizeof(B) <= 512, "barriers");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = smem_raw;
@@ -333,42 +335,56 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             cur.next();
         }
     } else if (warp == kIssueWarp) {
-        issuer(&bar->done, [&]() {
+        issuer(bar->done, [&]() {
             if ((a.stall && !spin_phase(&bar->stall_bar, 0, w)) || !spin_phase(&bar->fix_full, 0, w))
                 return;
-            Slot<N1> next_s, cur_q;    // of the next S; of block u
-            Slot<N2> next_dp, cur_do;
+            Slot<N1> next;   // of the next S
+            Slot<N2> cur;    // dO of block u
             auto issue_s = [&](int h) -> bool {
-                if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
+                if (!spin_phase(bar->full1 + next.s, next.ph, w)) return false;
                 tc_fence_after();
-                mma_head<D, 64>(tmem + 64 * h, dK, dQ + next_s.s * kBlockDesc, idS);
+                mma_head<D, 64>(tmem + 64 * h, dK, dQ + next.s * kBlockDesc, idS);
                 mma_commit(bar->s_full + h);
-                next_s.next();
+                next.next();
                 return true;
             };
-            auto issue_dp = [&](int h) -> bool {
-                if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
-                tc_fence_after();
-                mma_head<D, 64>(tmem + 128 + 64 * h, dV, dO + next_dp.s * kBlockDesc, idS);
-                mma_commit(bar->dp_full + h);
-                next_dp.next();
-                return true;
-            };
-            for (int u = 0; u < 2 && u < n; u++)
-                if (!issue_s(u) || !issue_dp(u)) return;
+            if (!issue_s(0) || (n > 1 && !issue_s(1))) return;
             for (int u = 0; u < n; u++) {
-                const int h = u & 1, ph = (u >> 1) & 1;
-                if (!spin_phase(bar->p_full + h, ph, w)) return;
+                const int h = u & 1;
+                if (!spin_phase(bar->full2 + cur.s, cur.ph, w) ||
+                    !spin_phase(bar->p_full + h, (u >> 1) & 1, w))
+                    return;
                 tc_fence_after();
-                mma_block64<32>(tmem + 256, tmem + 64 * h, dOt + cur_do.s * kBlockDesc, idO, u > 0);
-                mma_commit(bar->empty2 + cur_do.s);   // (dP(u), issued before, read it too)
-                cur_do.next();
+                mma_block64<32>(tmem + 256, tmem + 64 * h, dOt + cur.s * kBlockDesc, idO, u > 0);
+                mma_commit(bar->empty2 + cur.s);
+                cur.next();
                 if (u + 2 < n && !issue_s(h)) return;
-                if (!spin_phase(bar->ds_full + h, ph, w)) return;
+            }
+        });
+    } else if (warp == kIssueWarp2) {
+        issuer(bar->done + 1, [&]() {
+            if (!spin_phase(&bar->fix_full, 0, w)) return;
+            Slot<N2> next;   // of the next dP
+            Slot<N1> cur;    // Q of block u
+            auto issue_dp = [&](int h) -> bool {
+                if (!spin_phase(bar->full2 + next.s, next.ph, w)) return false;
                 tc_fence_after();
-                mma_block64<32>(tmem + 384, tmem + 128 + 64 * h, dQt + cur_q.s * kBlockDesc, idO, u > 0);
-                mma_commit(bar->empty1 + cur_q.s);
-                cur_q.next();
+                mma_head<D, 64>(tmem + 128 + 64 * h, dV, dO + next.s * kBlockDesc, idS);
+                mma_commit(bar->dp_full + h);
+                mma_commit(bar->empty2 + next.s);
+                next.next();
+                return true;
+            };
+            if (!issue_dp(0) || (n > 1 && !issue_dp(1))) return;
+            for (int u = 0; u < n; u++) {
+                const int h = u & 1;
+                if (!spin_phase(bar->full1 + cur.s, cur.ph, w) ||
+                    !spin_phase(bar->ds_full + h, (u >> 1) & 1, w))
+                    return;
+                tc_fence_after();
+                mma_block64<32>(tmem + 384, tmem + 128 + 64 * h, dQt + cur.s * kBlockDesc, idO, u > 0);
+                mma_commit(bar->empty1 + cur.s);
+                cur.next();
                 if (u + 2 < n && !issue_dp(h)) return;
             }
         });
@@ -442,7 +458,7 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             tc_fence_before();
             mbar_arrive_warp(bar->ds_full + half);
         }
-        if (ok && wait_warp(&bar->done, 0, w)) {
+        if (ok && wait_warp(bar->done, 0, w) && wait_warp(bar->done + 1, 0, w)) {
             tc_fence_after();
             // a quarter of the head's columns, of dV and dK, for each group of four warps
             constexpr int W = D / 4;
@@ -474,7 +490,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
     // a key block stays from S(u) to dQ(u), a value block for dP(u) alone
     constexpr int PN = D / 64, N1 = kDqRing1, N2 = kDqRing2;
     using L = BwdLayout<D, 0, N1, N2>;
-    using B = Bars<N1, N2>;
+    using B = Bars<N1, N2, 1>;
     static_assert(sizeof(B) <= 512, "barriers");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = smem_raw;
@@ -520,44 +536,47 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
         };
         load_blocks<D, L>(sm, bar, &tmK, &tmV, b, n, coords, w, lane);
     } else if (warp == kIssueWarp) {
-        issuer(&bar->done, [&]() {
+        issuer(bar->done, [&]() {
             if ((a.stall && !spin_phase(&bar->stall_bar, 0, w)) || !spin_phase(&bar->tmem_full, 0, w))
                 return;
-            Slot<N1> next_s, cur_k;    // of the next S; of block u
-            Slot<N2> next_dp;
-            auto issue_s = [&](int h) -> bool {
-                if (!spin_phase(bar->full1 + next_s.s, next_s.ph, w)) return false;
-                tc_fence_after();
-                mma_head_ts<D, 64>(tmem + 64 * h, tmem + 384, dK + next_s.s * kBlockDesc, idS);
-                mma_commit(bar->s_full + h);
-                next_s.next();
-                return true;
-            };
-            auto issue_dp = [&](int h) -> bool {
-                if (!spin_phase(bar->full2 + next_dp.s, next_dp.ph, w)) return false;
-                tc_fence_after();
-                mma_head_ts<D, 64>(tmem + 128 + 64 * h, tmem + 448, dV + next_dp.s * kBlockDesc, idS);
-                mma_commit(bar->dp_full + h);
-                mma_commit(bar->empty2 + next_dp.s);
-                next_dp.next();
-                return true;
-            };
-            for (int u = 0; u < 2 && u < n; u++)
-                if (!issue_s(u) || !issue_dp(u)) return;
-            for (int v = 0; v <= n; v++) {
-                // S(v + 2) once S(v) is read, which comes before dS(v - 1) is written
-                if (v + 2 < n && (!spin_phase(bar->s_free + (v & 1), (v >> 1) & 1, w) ||
-                                  !issue_s(v & 1)))
+            Slot<N1> next;
+            for (int u = 0; u < n; u++) {
+                const int h = u & 1;
+                if (!spin_phase(bar->full1 + next.s, next.ph, w) ||
+                    (u >= 2 && !spin_phase(bar->s_free + h, ((u - 2) >> 1) & 1, w)))
                     return;
-                if (v == 0) continue;
-                const int u = v - 1, h = u & 1;
-                if (!spin_phase(bar->ds_full + h, (u >> 1) & 1, w)) return;
+                tc_fence_after();
+                mma_head_ts<D, 64>(tmem + 64 * h, tmem + 384, dK + next.s * kBlockDesc, idS);
+                mma_commit(bar->s_full + h);
+                next.next();
+            }
+        });
+    } else if (warp == kIssueWarp2) {
+        issuer(bar->done + 1, [&]() {
+            if (!spin_phase(&bar->tmem_full, 0, w)) return;
+            Slot<N2> next;   // of the next dP
+            Slot<N1> cur;    // K of block u
+            auto issue_dp = [&](int h) -> bool {
+                if (!spin_phase(bar->full2 + next.s, next.ph, w)) return false;
+                tc_fence_after();
+                mma_head_ts<D, 64>(tmem + 128 + 64 * h, tmem + 448, dV + next.s * kBlockDesc, idS);
+                mma_commit(bar->dp_full + h);
+                mma_commit(bar->empty2 + next.s);
+                next.next();
+                return true;
+            };
+            if (!issue_dp(0) || (n > 1 && !issue_dp(1))) return;
+            for (int u = 0; u < n; u++) {
+                const int h = u & 1;
+                if (!spin_phase(bar->full1 + cur.s, cur.ph, w) ||
+                    !spin_phase(bar->ds_full + h, (u >> 1) & 1, w))
+                    return;
                 tc_fence_after();
                 if (u >= n - nt)
-                    mma_block64<32>(tmem + 256, tmem + 128 + 64 * h, dKt + cur_k.s * kBlockDesc, idO,
+                    mma_block64<32>(tmem + 256, tmem + 128 + 64 * h, dKt + cur.s * kBlockDesc, idO,
                                     u > n - nt);
-                mma_commit(bar->empty1 + cur_k.s);
-                cur_k.next();
+                mma_commit(bar->empty1 + cur.s);
+                cur.next();
                 if (u + 2 < n && !issue_dp(h)) return;
             }
         });
@@ -646,7 +665,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
             mbar_arrive_warp(bar->ds_full + half);
         }
         if (ok && !summed) ok = join_delta();
-        if (ok && wait_warp(&bar->done, 0, w)) {
+        if (ok && wait_warp(bar->done + 1, 0, w)) {
             tc_fence_after();
             constexpr int W = D / 4;   // columns of dQ for each group of four warps
             const int x = (warp >> 2) * W;
