@@ -230,7 +230,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             const uint64_t dV = smem_desc_sw128(smem_u32(sm + L::kV), kPanel, 1024);
             constexpr uint32_t kTileDesc = kTile >> 4, kHalfDesc = 64 * 128 >> 4;
             const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
-            bool ok = !a.stall || spin_phase(stall_bar, 0, w);
+            bool ok = !a.stall || wait_phase(stall_bar, 0, w);
             struct Cursor {
                 int pi, pc, i, hc, jc0;
                 FwdProblem pr;
@@ -254,8 +254,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             };
             auto issue_s = [&](const Cursor &c) -> bool {
                 const int jc = c.jc0 + (c.i >> 1), sk = jc & 1, kh = c.i & 1, b = c.hc & 1;
-                if (c.i == 0 && !spin_phase(q_full + t, c.pc & 1, w)) return false;
-                if (kh == 0 && !spin_phase(k_full + sk, (jc >> 1) & 1, w)) return false;
+                if (c.i == 0 && !wait_phase(q_full + t, c.pc & 1, w)) return false;
+                if (kh == 0 && !wait_phase(k_full + sk, (jc >> 1) & 1, w)) return false;
                 tc_fence_after();
                 mma_head<D, 128>(tS + b * 64, dQ, dK + sk * kTileDesc + kh * kHalfDesc, idS);
                 mma_commit(s_full + 2 * t + b);
@@ -266,10 +266,10 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             };
             auto issue_pv = [&](const Cursor &c) -> bool {
                 const int jc = c.jc0 + (c.i >> 1), st = jc & 1, kh = c.i & 1, b = c.hc & 1;
-                if (kh == 0 && !spin_phase(v_full + st, (jc >> 1) & 1, w)) return false;
-                if (!spin_phase(p_full + 2 * t + b, (c.hc >> 1) & 1, w)) return false;
+                if (kh == 0 && !wait_phase(v_full + st, (jc >> 1) & 1, w)) return false;
+                if (!wait_phase(p_full + 2 * t + b, (c.hc >> 1) & 1, w)) return false;
                 // the first PV of a problem overwrites O: the epilogue must have read it
-                if (c.i == 0 && c.pc > 0 && !spin_phase(o_free + t, (c.pc - 1) & 1, w)) return false;
+                if (c.i == 0 && c.pc > 0 && !wait_phase(o_free + t, (c.pc - 1) & 1, w)) return false;
                 tc_fence_after();
                 mma_block64<16>(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
                              c.i > 0 ? 1u : 0u);
