@@ -90,15 +90,20 @@ monarch_status status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK :
 // A pointer field whose target (lengths, starts) must be 4-byte aligned.
 bool aligned4(const void *p) { return aligned(p, 4); }
 
+// A workspace for a call that needs `need` bytes (none: anything goes).
+monarch_status check_workspace(size_t need, const void *workspace, size_t ws_bytes) {
+    if (need == 0) return MONARCH_OK;
+    if (!workspace) return MONARCH_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return MONARCH_ERR_ALIGN;
+    return ws_bytes < at_least_256(need) ? MONARCH_ERR_NO_MEMORY : MONARCH_OK;
+}
+
 monarch_status run_token(const WinProblem &p, monarch_dtype dtype, const void *q, const void *k,
                          const void *v, void *out, float *lse, void *workspace, size_t ws_bytes,
                          cudaStream_t stream) {
     const win::TokenPlan plan = win::token_plan(p, dtype);
-    if (plan.bytes > 0) {
-        if (!workspace) return MONARCH_ERR_INVALID_ARG;
-        if (!aligned(workspace, 256)) return MONARCH_ERR_ALIGN;
-        if (ws_bytes < at_least_256(plan.bytes)) return MONARCH_ERR_NO_MEMORY;
-    }
+    const monarch_status ws = check_workspace(plan.bytes, workspace, ws_bytes);
+    if (ws != MONARCH_OK) return ws;
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
     return status_of(
@@ -128,9 +133,10 @@ extern "C" {
 size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc) {
     WinProblem p;
     if (validate_window(desc, &p) != MONARCH_OK) return 0;
-    return at_least_256(choose(p, desc->dtype) == kPathToken
-                            ? win::token_plan(p, desc->dtype).bytes
-                            : 0);
+    const int path = choose(p, desc->dtype);
+    return at_least_256(path == kPathToken    ? win::token_plan(p, desc->dtype).bytes
+                        : path == kPathTensor ? win::tc_forward_bytes(p)
+                                              : 0);
 }
 
 int monarch_window_attn_path(const monarch_window_desc *desc) {
@@ -157,9 +163,12 @@ monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc *desc, const
     if (path == kPathSimt)
         return status_of(win::simt_forward(p, (const float *)q, (const float *)k, (const float *)v,
                                            (float *)out, lse, s));
+    const monarch_status ws = check_workspace(win::tc_forward_bytes(p), workspace, ws_bytes);
+    if (ws != MONARCH_OK) return ws;
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
-    return status_of(win::tc_forward(p, q, k, v, out, lse, status, device_wait_limit(), s));
+    return status_of(
+        win::tc_forward(p, q, k, v, out, lse, workspace, status, device_wait_limit(), s));
 }
 
 size_t monarch_window_attn_bwd_workspace_bytes(const monarch_window_desc *desc) {

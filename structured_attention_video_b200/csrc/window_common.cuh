@@ -153,8 +153,10 @@ cudaError_t token_forward(const WinProblem &p, monarch_dtype dtype, const TokenP
                           void *workspace, int *status, long long limit, cudaStream_t stream);
 
 // Tensor-core kernels, bfloat16 (window_sm100.cu, window_bwd_sm100.cu).
+size_t tc_forward_bytes(const WinProblem &p);   // workspace, 0 where none is needed
 cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const void *v, void *out,
-                       float *lse, int *status, long long limit, cudaStream_t stream);
+                       float *lse, void *workspace, int *status, long long limit,
+                       cudaStream_t stream);
 
 cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
                         const void *v, const float *lse, float *delta, const void *dout,

@@ -3,8 +3,11 @@
 // operands of the second product).
 //
 // Persistent, 512 threads a CTA, one CTA an SM.  A problem is one head and a pair of
-// 128-row query tiles; its keys are the two runs of 128-key chunks that some row of
-// the pair sees.  Roles: warp 12 loads keys, warp 14 queries and values (TMA), warps 13
+// 128-row query tiles; its keys are the two runs of 64-key blocks that some row of the
+// pair sees, two blocks a chunk.  Either each CTA takes whole problems (the longest
+// first), or, where those would leave SMs idle, the chunks of all problems form one line
+// that the CTAs divide evenly: a problem cut by a boundary leaves its parts' unscaled sums,
+// maxima and row sums in the workspace, and a second kernel joins them in order.  Roles: warp 12 loads keys, warp 14 queries and values (TMA), warps 13
 // and 15 issue the products of tile 0 and 1, warps 0-3 and 4-7 are the softmax of tile
 // 0 and 1 (one query row a thread), warps 8-11 the epilogue.  Keys go in halves of 64:
 // each tile has two S buffers of 64 columns in tensor memory, so the logits of the
@@ -24,6 +27,20 @@ constexpr int kSoftmaxRegs = 136, kEpilogueRegs = 128, kProducerRegs = 112;
 static_assert(2 * kSoftmaxRegs + kEpilogueRegs + kProducerRegs == 4 * (65536 / kThreads),
               "the warpgroups' registers must add up to the launch's 128 per thread");
 
+// Entries of the line: (pair, batch), all heads of one alike; CTAs that divide it.
+constexpr int kMaxEntries = 512, kMaxCtas = 512;
+// Segments of one CTA.
+constexpr int kMaxSegments = 480;
+
+// What one CTA does of one problem, as shared memory holds it: key blocks
+// [first, first + nh) of the problem's.
+struct Record {
+    int unit;            // entry * H + head
+    int first, nh;
+    int sinks, window;   // blocks of the problem's sinks; first block of its window
+    int ends;            // the problem's last block is among them
+};
+
 // Shared memory for a head of D columns (tiles of 128 rows).
 template <int D> struct Layout {
     static constexpr uint32_t kTile = (D / 64) * kPanel;
@@ -32,7 +49,9 @@ template <int D> struct Layout {
     static constexpr uint32_t kV = kK + 2 * kTile;
     static constexpr uint32_t kL = kV + 2 * kTile;          // row sums [parity][tile][128]
     static constexpr uint32_t kStg = kL + 2048;             // epilogue: 4 warps x 32 rows x 128 B
-    static constexpr uint32_t kBar = kStg + 4 * 4096;
+    static constexpr uint32_t kLine = kStg + 4 * 4096;      // first chunk of each entry
+    static constexpr uint32_t kList = kLine + (kMaxEntries + 1) * 4 + 12;
+    static constexpr uint32_t kBar = kList + kMaxSegments * sizeof(Record);
     static constexpr uint32_t kSmem = kBar + 512 + 1024;    // + slack to align the base
     static_assert(kSmem <= (uint32_t)kMaxSmem, "window attention shared memory");
 };
@@ -41,6 +60,11 @@ struct FwdArgs {
     WinProblem p;
     int npairs;     // pairs of 128-row query tiles a head
     int nprob;      // npairs * B * H
+    int line;       // 1: the CTAs divide the line of all chunks
+    // line: per slot (2 a CTA: a part that starts inside its problem, one that starts with
+    // it) the problem and whether the part ends it, then maxima, row sums, sums
+    int2 *meta;
+    float *parts;
     __nv_bfloat16 *out;
     float *lse;     // or null
     int *status;
@@ -48,39 +72,130 @@ struct FwdArgs {
     int stall;
 };
 
-struct FwdProblem {
-    int b, h, i0;
+// Floats of one slot: 256 maxima, 256 row sums, 256 rows of d sums.
+__host__ __device__ constexpr int part_floats(int d) { return 512 + 256 * d; }
+
+// Entry e of the line: pair npairs - 1 - e / B of batch e % B.  Later rows see more keys
+// under a causal mask, so the longest problems come first and short ones fill the end.
+struct Entry {
+    int b, i0;
     Sequence seq;
-    KeyTiles kt;    // 128-key chunks
-    int nh;         // 64-key halves: two a chunk, but for a last one that nobody sees
+    KeyTiles kt;    // 64-key blocks
+};
+__device__ __forceinline__ Entry entry_of(const FwdArgs &a, int e) {
+    const WinProblem &p = a.p;
+    Entry x;
+    x.b = e % p.B;
+    x.i0 = (a.npairs - 1 - e / p.B) * 256;
+    x.seq = sequence(p, x.b);
+    x.kt = key_tiles<64>(p, x.seq, x.i0, x.i0 + 256);
+    return x;
+}
+
+// A segment, read from its record by each role.
+struct Segment {
+    int b, h, i0, first, nh, unit, turn, skip;
+    bool begins, ends;
+    __device__ __forceinline__ Segment(const FwdArgs &a, const Record &r) {
+        const int e = r.unit / a.p.H;
+        unit = r.unit;
+        h = unit - e * a.p.H;
+        b = e % a.p.B;
+        i0 = (a.npairs - 1 - e / a.p.B) * 256;
+        first = r.first;
+        nh = r.nh;
+        turn = r.sinks - first;   // blocks before it are the sinks', the others lie
+        skip = r.window - r.sinks;   // `skip` further
+        begins = first == 0;
+        ends = r.ends != 0;
+    }
+    __device__ __forceinline__ bool whole() const { return begins && ends; }
+    __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (begins ? 1 : 0); }
+    __device__ __forceinline__ int key(int i) const {
+        return (first + i + (i < turn ? 0 : skip)) * 64;
+    }
 };
 
-// Later rows see more keys under a causal mask: the pairs go from last to first, so
-// that the longest problems start first and the short ones fill the end.
-__device__ __forceinline__ FwdProblem fwd_problem(const FwdArgs &a, int unit) {
+// The CTA's segments into `list`; returns their number.  Whole problems: those of index
+// blockIdx, blockIdx + gridDim, ... (nh = 0: no row sees a key).  The line: chunks
+// [total * blockIdx / gridDim, total * (blockIdx + 1) / gridDim).
+__device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list) {
     const WinProblem &p = a.p;
-    FwdProblem q;
-    const int bh = unit % (p.B * p.H);
-    q.i0 = (a.npairs - 1 - unit / (p.B * p.H)) * 256;
-    q.b = bh / p.H;
-    q.h = bh % p.H;
-    q.seq = sequence(p, q.b);
-    q.kt = key_tiles<128>(p, q.seq, q.i0, q.i0 + 256);
-    q.nh = 2 * q.kt.count();
-    if (q.nh) {
-        int r0, r1;
-        real_rows(p, q.seq, q.i0, q.i0 + 256, r0, r1);
-        const int end = q.kt.nB ? row_keys(p, q.seq, r1 - 1).hi : row_keys(p, q.seq, r1 - 1).sink;
-        if (q.kt.tile(q.kt.count() - 1) * 128 + 64 >= end) q.nh--;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int count;
+    if (!a.line) {
+        const int n = a.nprob > (int)blockIdx.x
+                          ? (a.nprob - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const int unit = blockIdx.x + i * gridDim.x;
+            const KeyTiles kt = entry_of(a, unit / p.H).kt;
+            list[i] = Record{unit, 0, kt.count(), kt.nA, kt.first, 1};
+        }
+        return n;
     }
-    return q;
+    const int entries = a.npairs * p.B;
+    for (int e = threadIdx.x; e < entries; e += kThreads)
+        line[e + 1] = (entry_of(a, e).kt.count() + 1) / 2 * p.H;
+    if (threadIdx.x == 0) line[0] = 0;
+    if (threadIdx.x < 2) a.meta[2 * blockIdx.x + threadIdx.x] = make_int2(-1, 0);
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int e0 = 1; e0 <= entries; e0 += 32) {
+            int x = e0 + lane <= entries ? line[e0 + lane] : 0;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, m);
+                if (lane >= m) x += y;
+            }
+            if (e0 + lane <= entries) line[e0 + lane] = sum + x;
+            sum += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            int at = (int)((int64_t)sum * blockIdx.x / gridDim.x), n = 0, e = 0;
+            const int end = (int)((int64_t)sum * (blockIdx.x + 1) / gridDim.x);
+            while (at < end && n < kMaxSegments) {
+                while (line[e + 1] <= at) e++;
+                const KeyTiles kt = entry_of(a, e).kt;
+                const int blocks = kt.count(), chunks = (blocks + 1) / 2, rest = at - line[e];
+                const int h = rest / chunks, c0 = rest - h * chunks, c1 = min(chunks, c0 + end - at);
+                list[n++] = Record{e * p.H + h, 2 * c0, min(blocks, 2 * c1) - 2 * c0, kt.nA, kt.first,
+                                   c1 == chunks};
+                at += c1 - c0;
+            }
+            count = n;
+        }
+    }
+    __syncthreads();
+    return count;
+}
+
+// Blocks j and j + 1 of a segment's keys or values to a stage: one box of 128 rows, or two
+// of 64 where they are not neighbours (the sinks' last block) or the last is alone.
+template <int D>
+__device__ __forceinline__ void load_chunk(uint8_t *dst, const CUtensorMap *map64,
+                                           const CUtensorMap *map128, const Segment &sg, int j,
+                                           int G, uint64_t *bar) {
+    const int blocks = min(2, sg.nh - j), row = sg.key(j);
+    mbar_expect_tx(bar, blocks * Layout<D>::kTile / 2);
+    if (blocks == 2 && sg.key(j + 1) == row + 64) {
+        for (int pn = 0; pn < D / 64; pn++)
+            tma_load_4d(dst + pn * kPanel, map128, pn * 64, row, sg.h / G, sg.b, bar);
+        return;
+    }
+    for (int x = 0; x < blocks; x++)
+        for (int pn = 0; pn < D / 64; pn++)
+            tma_load_4d(dst + pn * kPanel + x * 64 * 128, map64, pn * 64, sg.key(j + x), sg.h / G,
+                        sg.b, bar);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, FwdArgs a) {
+                     const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmK128,
+                     const __grid_constant__ CUtensorMap tmV128, FwdArgs a) {
     using L = Layout<D>;
     constexpr int PN = D / 64;
     constexpr uint32_t kTile = L::kTile;
@@ -107,8 +222,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
 
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nmine = a.nprob > (int)blockIdx.x
-                          ? (a.nprob - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    int *line = reinterpret_cast<int *>(sm + L::kLine);
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; t++) {
@@ -133,13 +247,14 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         fence_mbar_init();
     }
     if (warp == 13) tmem_alloc(tmem_slot, 512);
+    Record *list = reinterpret_cast<Record *>(sm + L::kList);
+    const int nseg = list_segments(a, line, list);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{a.limit, a.status, abort_flag};
-    // Every role walks the same problems and skips those without keys (the softmax
-    // warps write their zeros); pc counts the others, and so does every barrier.
+    // Every role takes the same segments; pc counts those with keys, as the barriers do.
 
     if (warp >= 12) {
         regs_dec<kProducerRegs>();
@@ -148,20 +263,16 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             // back are done
             int issued[2] = {0, 0}, jc = 0;
             bool ok = true;
-            for (int pi = 0; ok && pi < nmine; pi++) {
-                const FwdProblem pr = fwd_problem(a, blockIdx.x + pi * gridDim.x);
-                for (int j = 0; j < (pr.nh + 1) / 2; j++, jc++) {
+            for (int si = 0; ok && si < nseg; si++) {
+                const Segment sg(a, list[si]);
+                if (sg.nh == 0) continue;
+                for (int j = 0; j < sg.nh; j += 2, jc++) {
                     const int sk = jc & 1;
                     if (jc >= 2 && !wait_warp(k_empty + sk, ((jc >> 1) - 1) & 1, w)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
-                        mbar_expect_tx(k_full + sk, kTile);
-                        for (int pn = 0; pn < PN; pn++)
-                            tma_load_4d(sm + L::kK + sk * kTile + pn * kPanel, &tmK, pn * 64,
-                                        pr.kt.tile(j) * 128, pr.h / p.G, pr.b, k_full + sk);
-                    }
+                    if (lane == 0) load_chunk<D>(sm + L::kK + sk * kTile, &tmK, &tmK128, sg, j, p.G, k_full + sk);
                     issued[sk]++;
                 }
             }
@@ -175,9 +286,9 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             // previous problem follows that problem's values in the issue order.
             int pc = 0, issued[2] = {0, 0}, jc = 0, qloads[2] = {0, 0};
             bool ok = true;
-            for (int pi = 0; ok && pi < nmine; pi++) {
-                const FwdProblem pr = fwd_problem(a, blockIdx.x + pi * gridDim.x);
-                if (!pr.nh) continue;
+            for (int si = 0; ok && si < nseg; si++) {
+                const Segment sg(a, list[si]);
+                if (sg.nh == 0) continue;
                 for (int t = 0; t < 2; t++) {
                     if (pc > 0 && !wait_warp(q_empty + t, (pc - 1) & 1, w)) {
                         ok = false;
@@ -187,24 +298,19 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                         mbar_expect_tx(q_full + t, kTile);
                         for (int pn = 0; pn < PN; pn++)
                             tma_load_4d(sm + L::kQ + t * kTile + pn * kPanel, &tmQ, pn * 64,
-                                        pr.i0 + t * 128, pr.h, pr.b, q_full + t);
+                                        sg.i0 + t * 128, sg.h, sg.b, q_full + t);
                     }
                     qloads[t]++;
                 }
                 if (!ok) break;
                 pc++;
-                for (int j = 0; j < (pr.nh + 1) / 2; j++, jc++) {
+                for (int j = 0; j < sg.nh; j += 2, jc++) {
                     const int st = jc & 1;
                     if (jc >= 2 && !wait_warp(v_empty + st, ((jc >> 1) - 1) & 1, w)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
-                        mbar_expect_tx(v_full + st, kTile);
-                        for (int pn = 0; pn < PN; pn++)
-                            tma_load_4d(sm + L::kV + st * kTile + pn * kPanel, &tmV, pn * 64,
-                                        pr.kt.tile(j) * 128, pr.h / p.G, pr.b, v_full + st);
-                    }
+                    if (lane == 0) load_chunk<D>(sm + L::kV + st * kTile, &tmV, &tmV128, sg, j, p.G, v_full + st);
                     issued[st]++;
                 }
             }
@@ -232,24 +338,19 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
             bool ok = !a.stall || wait_phase(stall_bar, 0, w);
             struct Cursor {
-                int pi, pc, i, hc, jc0;
-                FwdProblem pr;
+                int si, nh, pc, i, hc, jc0;   // segment, its blocks; block i, hc of all
             };
-            auto skip_empty = [&](Cursor &c) {
-                while (c.pi < nmine) {
-                    c.pr = fwd_problem(a, blockIdx.x + c.pi * gridDim.x);
-                    if (c.pr.nh) break;
-                    c.pi++;
-                }
+            auto find = [&](Cursor &c) {
+                while (c.si < nseg && (c.nh = list[c.si].nh) == 0) c.si++;
             };
             auto advance = [&](Cursor &c) {
                 c.hc++;
-                if (++c.i == c.pr.nh) {
+                if (++c.i == c.nh) {
                     c.i = 0;
-                    c.jc0 += (c.pr.nh + 1) / 2;
-                    c.pi++;
+                    c.jc0 += (c.nh + 1) / 2;
                     c.pc++;
-                    skip_empty(c);
+                    c.si++;
+                    find(c);
                 }
             };
             auto issue_s = [&](const Cursor &c) -> bool {
@@ -259,7 +360,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 tc_fence_after();
                 mma_head<D, 128>(tS + b * 64, dQ, dK + sk * kTileDesc + kh * kHalfDesc, idS);
                 mma_commit(s_full + 2 * t + b);
-                const bool last = c.i == c.pr.nh - 1;
+                const bool last = c.i == c.nh - 1;
                 if (kh == 1 || last) mma_commit(k_empty + sk);
                 if (last) mma_commit(q_empty + t);
                 return true;
@@ -274,20 +375,20 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 mma_block64<16>(tO, tS + b * 64, dV + st * kTileDesc + kh * kHalfDesc, idO,
                              c.i > 0 ? 1u : 0u);
                 mma_commit(pv_done + t);
-                const bool last = c.i == c.pr.nh - 1;
+                const bool last = c.i == c.nh - 1;
                 if (kh == 1 || last) mma_commit(v_empty + st);
                 if (last) mma_commit(o_full + t);
                 return true;
             };
-            Cursor cs{0, 0, 0, 0, 0, {}};   // next S to issue
-            skip_empty(cs);
+            Cursor cs{0, 0, 0, 0, 0, 0};    // next S to issue
+            find(cs);
             Cursor cp = cs;                 // next PV to issue
-            for (int k = 0; ok && k < 2 && cs.pi < nmine; k++) {
+            for (int k = 0; ok && k < 2 && cs.si < nseg; k++) {
                 ok = issue_s(cs);
                 advance(cs);
             }
-            while (ok && cp.pi < nmine) {
-                const bool more = cs.pi < nmine;
+            while (ok && cp.si < nseg) {
+                const bool more = cs.si < nseg;
                 ok = issue_pv(cp) && (!more || issue_s(cs));
                 if (more) advance(cs);
                 advance(cp);
@@ -304,15 +405,32 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         bool ok = true;
         int pc = 0;
-        for (int pi = 0; ok && pi < nmine; pi++) {
-            const FwdProblem pr = fwd_problem(a, blockIdx.x + pi * gridDim.x);
-            if (!pr.nh) continue;
+        for (int si = 0; ok && si < nseg; si++) {
+            const Segment sg(a, list[si]);
+            if (sg.nh == 0) continue;
             for (int t = 0; t < 2; t++) {
                 if (!wait_warp(o_full + t, pc & 1, w) || !wait_warp(l_full + t, pc & 1, w)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if (!sg.whole()) {   // the unscaled sums, for the join
+                    float *dst = a.parts + (int64_t)sg.slot() * part_floats(D) + 512 +
+                                 (t * 128 + wq * 32 + lane) * D;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32f(tmem + lane_off + 256 + t * 128 + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(dst + c + k) =
+                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive_warp(o_free + t);
+                    continue;
+                }
                 const float total = lsum[((pc & 1) * 2 + t) * 128 + wq * 32 + lane];
                 const float inv_l = 1.f / total;
                 uint32_t pk[D / 2];
@@ -332,8 +450,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 // the warp's 32 rows leave through shared memory, 128 bytes of a row at a
                 // time, so each store instruction covers four runs of 128 bytes
                 uint8_t *stg = sm + L::kStg + wq * 4096;
-                const int m0 = pr.i0 + t * 128 + wq * 32;
-                __nv_bfloat16 *const base = a.out + pr.b * p.o.batch + pr.h * p.o.head;
+                const int m0 = sg.i0 + t * 128 + wq * 32;
+                __nv_bfloat16 *const base = a.out + sg.b * p.o.batch + sg.h * p.o.head;
 #pragma unroll
                 for (int hf = 0; hf < PN; hf++) {
 #pragma unroll
@@ -368,21 +486,30 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint64_t c2 = f2_pack(c1, c1);
         bool ok = true;
         int pc = 0, hc = 0, jc0 = 0;
-        for (int pi = 0; ok && pi < nmine; pi++) {
-            const FwdProblem pr = fwd_problem(a, blockIdx.x + pi * gridDim.x);
-            const int m = pr.i0 + t * 128 + wq * 32 + lane;
-            if (!pr.nh) {   // no row of the pair sees a key
-                if (m < p.Nq) {
-                    uint4 *row = reinterpret_cast<uint4 *>(a.out + pr.b * p.o.batch +
-                                                           pr.h * p.o.head + (int64_t)m * p.o.token);
-                    for (int x = 0; x < p.d / 8; x++) row[x] = make_uint4(0, 0, 0, 0);
-                    if (a.lse) a.lse[((int64_t)pr.b * p.H + pr.h) * p.Nq + m] = -INFINITY;
-                }
+        // rows of a pair that sees no key: zeros
+        auto write_zeros = [&](int unit) {
+            const int e = unit / p.H, h = unit % p.H, bb = e % p.B;
+            const int m = (a.npairs - 1 - e / p.B) * 256 + t * 128 + wq * 32 + lane;
+            if (m >= p.Nq) return;
+            uint4 *row = reinterpret_cast<uint4 *>(a.out + bb * p.o.batch + h * p.o.head +
+                                                   (int64_t)m * p.o.token);
+            for (int c = 0; c < p.d / 8; c++) row[c] = make_uint4(0, 0, 0, 0);
+            if (a.lse) a.lse[((int64_t)bb * p.H + h) * p.Nq + m] = -INFINITY;
+        };
+        for (int e = 0; a.line && e < a.npairs * p.B; e++)   // (not in the line at all)
+            if (line[e + 1] == line[e])
+                for (int h = blockIdx.x; h < p.H; h += gridDim.x) write_zeros(e * p.H + h);
+        for (int si = 0; ok && si < nseg; si++) {
+            const Segment sg(a, list[si]);
+            if (sg.nh == 0) {
+                write_zeros(sg.unit);
                 continue;
             }
-            const RowKeys rk = row_keys(p, pr.seq, m);
+            const int m = sg.i0 + t * 128 + wq * 32 + lane;
+            const Sequence seq = sequence(p, sg.b);
+            const RowKeys rk = row_keys(p, seq, m);
             float m_run = -INFINITY, l_run = 0.f;
-            for (int i = 0; i < pr.nh; i++, hc++) {
+            for (int i = 0; i < sg.nh; i++, hc++) {
                 const int b = hc & 1;
                 if (!wait_warp(s_full + 2 * t + b, (hc >> 1) & 1, w)) {
                     ok = false;
@@ -390,7 +517,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 }
                 tc_fence_after();
                 const uint32_t tS = tS0 + b * 64;
-                const int j0 = pr.kt.tile(i >> 1) * 128 + (i & 1) * 64;
+                const int j0 = sg.key(i);
                 float x[64];
                 tmem_ld32f(tS, &x[0]);
                 tmem_ld32f(tS + 32, &x[32]);
@@ -440,7 +567,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 float s0, s1;
                 f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), s0, s1);
                 l_run = l_run * alpha + (s0 + s1);
-                if (j0 + 64 > pr.seq.len) {
+                if (j0 + 64 > seq.len) {
                     // values past the sequence may hold anything, and 0 * NaN is NaN: they
                     // become zeros before this half's PV (both tiles write the same zeros)
                     const int jc = jc0 + (i >> 1), st = jc & 1;
@@ -449,7 +576,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                         break;
                     }
                     zero_rows(sm + L::kV + st * kTile + (i & 1) * 64 * 128,
-                              max(0, pr.seq.len - j0), 64, PN, kPanel, wq * 32 + lane, 128);
+                              max(0, seq.len - j0), 64, PN, kPanel, wq * 32 + lane, 128);
                     fence_proxy_async_smem();
                 }
                 if (i > 0 && __any_sync(0xffffffffu, rescale)) {
@@ -474,9 +601,14 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 mbar_arrive_warp(p_full + 2 * t + b);
             }
             if (!ok) break;
-            jc0 += (pr.nh + 1) / 2;
-            if (a.lse && m < p.Nq)
-                a.lse[((int64_t)pr.b * p.H + pr.h) * p.Nq + m] =
+            jc0 += (sg.nh + 1) / 2;
+            if (!sg.whole()) {
+                float *dst = a.parts + (int64_t)sg.slot() * part_floats(D) + t * 128 + wq * 32 + lane;
+                dst[0] = m_run * c1;
+                dst[256] = l_run;
+                if (threadIdx.x == 0) a.meta[sg.slot()] = make_int2(sg.unit, sg.ends);
+            } else if (a.lse && m < p.Nq)
+                a.lse[((int64_t)sg.b * p.H + sg.h) * p.Nq + m] =
                     l_run == 0.f ? -INFINITY : (m_run * c1 + log2f(l_run)) * kLn2;
             // the row sums for the epilogue, once it has taken those of the last problem
             if (pc > 0 && !wait_warp(o_free + t, (pc - 1) & 1, w)) break;
@@ -493,35 +625,138 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
 }
 
+// The parts of problems that a boundary cut.  Block (c, y): the problem whose first part
+// CTA c made; 16 rows of it.  Parts in order, so the result does not vary.
+template <int D>
+__global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
+    const WinProblem &p = a.p;
+    __shared__ int slots[kMaxCtas], parts;
+    const int2 head = a.meta[2 * blockIdx.x + 1];
+    if (head.x < 0) return;
+    if (threadIdx.x < 32) {
+        // its first part, then those of the CTAs behind (some may have had no chunk)
+        int n = 1;
+        bool more = true;
+        if (threadIdx.x == 0) slots[0] = 2 * blockIdx.x + 1;
+        for (int c0 = blockIdx.x + 1; more && c0 < ctas; c0 += 32) {
+            const int c = c0 + threadIdx.x;
+            const int2 m = c < ctas ? a.meta[2 * c] : make_int2(-1, 0);
+            uint32_t mine = __ballot_sync(0xffffffffu, m.x == head.x);
+            const uint32_t last = __ballot_sync(0xffffffffu, m.x == head.x && m.y);
+            if (last) more = false, mine &= last | (last - 1);   // up to the one that ends it
+            if ((mine >> threadIdx.x) & 1)
+                slots[n + __popc(mine & ((1u << threadIdx.x) - 1))] = 2 * c;
+            n += __popc(mine);
+        }
+        if (threadIdx.x == 0) parts = n;
+    }
+    __syncthreads();
+    const int n = parts;
+    const Entry x = entry_of(a, head.x / p.H);
+    const int h = head.x % p.H;
+    for (int at = threadIdx.x; at < 16 * (D / 4); at += 256) {
+        const int row = blockIdx.y * 16 + at / (D / 4), col = at % (D / 4) * 4;
+        const int m = x.i0 + row;
+        if (m >= p.Nq || col >= p.d) continue;
+        float mx = -INFINITY;
+        for (int i = 0; i < n; i++) {
+            mx = fmaxf(mx, a.parts[(int64_t)slots[i] * part_floats(D) + row]);
+        }
+        const float safe = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < n; i++) {
+            const float *src = a.parts + (int64_t)slots[i] * part_floats(D);
+            const float f = exp2f(src[row] - safe);
+            const float4 v = *reinterpret_cast<const float4 *>(src + 512 + row * D + col);
+            sum = fmaf(f, src[256 + row], sum);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<uint2 *>(a.out + x.b * p.o.batch + h * p.o.head + (int64_t)m * p.o.token +
+                                   col) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (a.lse && col == 0)
+            a.lse[((int64_t)x.b * p.H + h) * p.Nq + m] =
+                sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    }
+}
+
+// Whether the CTAs divide the line of all chunks.  Whole problems on `sms` CTAs take as many
+// rounds of the longest problem as there are problems a CTA; the line takes the mean, and
+// about ten chunks' time (20 us) for the parts and the join.  Chunks are estimated from
+// the tensors' sizes and the window, as the lengths are on the device.
+bool use_line(const WinProblem &p, int nprob, int sms) {
+    const int64_t entries = (int64_t)((p.Nq + 255) / 256) * p.B;
+    if (entries > kMaxEntries || sms > kMaxCtas) return false;
+    int64_t most = p.Nk;
+    if (p.left >= 0 && p.right >= 0) {
+        const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + 256 + p.frame;
+        most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
+    }
+    const int64_t chunks = most / 128 + 1;
+    if (entries * p.H * chunks >= (1LL << 31)) return false;
+    // segments of a CTA: at most its chunks, and at most the problems
+    if (min((int64_t)nprob, nprob * chunks / sms + 2) > kMaxSegments) return false;
+    const int64_t rounds = (nprob + sms - 1) / sms;
+    return rounds * chunks - nprob * chunks / sms >= 10;
+}
+
 template <int D>
 cudaError_t launch(const WinProblem &p, const void *q, const void *k, const void *v, FwdArgs a,
-                   cudaStream_t stream) {
-    CUtensorMap mq, mk, mv;
+                   int sms, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv, mk128, mv128;
     if (!map_tokens(&mq, q, p.q, p.B, p.H, p.Nq, p.d, 128) ||
-        !map_tokens(&mk, k, p.k, p.B, p.Hkv, p.Nk, p.d, 128) ||
-        !map_tokens(&mv, v, p.v, p.B, p.Hkv, p.Nk, p.d, 128))
+        !map_tokens(&mk, k, p.k, p.B, p.Hkv, p.Nk, p.d, 64) ||
+        !map_tokens(&mv, v, p.v, p.B, p.Hkv, p.Nk, p.d, 64) ||
+        !map_tokens(&mk128, k, p.k, p.B, p.Hkv, p.Nk, p.d, 128) ||
+        !map_tokens(&mv128, v, p.v, p.B, p.Hkv, p.Nk, p.d, 128))
         return cudaErrorInvalidValue;
     cudaError_t e = tcs::set_smem(tc_window_fwd_kernel<D>, Layout<D>::kSmem);
     if (e != cudaSuccess) return e;
-    const int grid = min(a.nprob, tcs::sm_count());
-    tc_window_fwd_kernel<D><<<grid, kThreads, Layout<D>::kSmem, stream>>>(mq, mk, mv, a);
+    // (a CTA lists at most kMaxSegments problems: beyond, more CTAs than SMs)
+    const int grid =
+        a.line ? sms : max(min(a.nprob, sms), (a.nprob + kMaxSegments - 1) / kMaxSegments);
+    tc_window_fwd_kernel<D><<<grid, kThreads, Layout<D>::kSmem, stream>>>(mq, mk, mv, mk128,
+                                                                              mv128, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.line) return e;
+    window_join_kernel<D><<<dim3(grid, 16), 256, 0, stream>>>(a, grid);
     return cudaGetLastError();
 }
 
+size_t meta_bytes(int sms) { return ((size_t)sms * 2 * sizeof(int2) + 255) & ~(size_t)255; }
+
 }  // namespace
 
+size_t tc_forward_bytes(const WinProblem &p) {
+    const int sms = tcs::sm_count();
+    if (!use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms)) return 0;
+    return meta_bytes(sms) + (size_t)sms * 2 * part_floats(p.d == 128 ? 128 : 64) * sizeof(float);
+}
+
 cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const void *v, void *out,
-                       float *lse, int *status, long long limit, cudaStream_t stream) {
+                       float *lse, void *workspace, int *status, long long limit,
+                       cudaStream_t stream) {
+    const int sms = tcs::sm_count();
     FwdArgs a;
     a.p = p;
     a.npairs = (p.Nq + 255) / 256;
     a.nprob = a.npairs * p.B * p.H;
+    a.line = use_line(p, a.nprob, sms);
+    a.meta = (int2 *)workspace;
+    a.parts = (float *)((char *)workspace + meta_bytes(sms));
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
     a.status = status;
     a.limit = limit;
     a.stall = device_inject_stall();
-    return p.d == 128 ? launch<128>(p, q, k, v, a, stream) : launch<64>(p, q, k, v, a, stream);
+    return p.d == 128 ? launch<128>(p, q, k, v, a, sms, stream)
+                      : launch<64>(p, q, k, v, a, sms, stream);
 }
 
 }  // namespace win
