@@ -82,16 +82,19 @@ __device__ __forceinline__ uint32_t below(int n) {
     return n >= 32 ? ~0u : (1u << max(n, 0)) - 1;
 }
 
-// N columns of an accumulator row to bfloat16 in global memory (columns below d).
+// N columns of an accumulator row to bfloat16 in global memory (columns below d), if the
+// row is in the tensor; zeros if it is not real.
 template <int N>
 __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16 *dst, float scale, int d,
-                                          bool real) {
+                                          bool in, bool real) {
 #pragma unroll 1
     for (int c = 0; c < N; c += 16) {
         float o[16];
         tmem_ld16f(taddr + c, o);
         tmem_wait_ld();
-        if (!real || c >= d) continue;
+        if (!in || c >= d) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = real ? o[e] : 0.f;
 #pragma unroll
         for (int e = 0; e < 2; e++)
             *reinterpret_cast<uint4 *>(dst + c + 8 * e) =
@@ -395,7 +398,11 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lanes + 64 * half, td = ts + 128;
         int ilo, ihi, rfirst, rlast;
-        query_rows(p, seq, j, j + 1, ilo, ihi);   // the queries that see this key
+        // the queries that see this key; a row that is not a key takes them all, so that its
+        // warp needs no masks (its sums touch nothing else), and zeros are stored
+        query_rows(p, seq, j, j + 1, ilo, ihi);
+        const bool key = j < seq.len;
+        if (!key) ilo = 0, ihi = 0x7fffffff;
         real_rows(p, seq, 0, p.Nq, rfirst, rlast);
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
         bool ok = true;
@@ -466,10 +473,10 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             const bool real = j < p.Nk;
             store_row<W>(lanes + 256 + x,
                          a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
-                         p.d - (int)x, real);
+                         p.d - (int)x, real, key);
             store_row<W>(lanes + 384 + x,
                          a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x, p.scale,
-                         p.d - (int)x, real);
+                         p.d - (int)x, real, key);
         }
     }
     tc_fence_before();
@@ -594,9 +601,10 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
             tc_fence_before();
             mbar_arrive_warp(&bar->tmem_full);
         }
-        const RowKeys rk = row_keys(p, seq, i);
+        RowKeys rk = row_keys(p, seq, i);
         const int64_t at = ((int64_t)b * p.H + h) * p.Nq + i;
-        const bool real = rk.hi > 0;
+        const bool real = rk.hi > 0;   // (others take every key, and zeros are stored)
+        if (!real) rk = RowKeys{0, 0x7fffffff, 0};
         const float nl = real ? -a.lse[at] * kLog2e : 0.f;
         float nd = real && n == nt ? -a.delta[at] : 0.f;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
@@ -670,7 +678,7 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
             constexpr int W = D / 4;   // columns of dQ for each group of four warps
             const int x = (warp >> 2) * W;
             store_row<W>(lanes + 256 + x, dq + (int64_t)i * a.g.dq.token + x, p.scale, p.d - x,
-                         i < p.Nq);
+                         i < p.Nq, real);
         }
     }
     tc_fence_before();

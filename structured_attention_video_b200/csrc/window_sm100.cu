@@ -58,7 +58,8 @@ template <int D> struct Layout {
 
 struct FwdArgs {
     WinProblem p;
-    int npairs;     // pairs of 128-row query tiles a head
+    int tiles;      // 128-row query tiles of a problem: 2, or 1 where pairs are fewer than SMs
+    int npairs;     // problems a head
     int nprob;      // npairs * B * H
     int line;       // 1: the CTAs divide the line of all chunks
     // line: per slot (2 a CTA: a part that starts inside its problem, one that starts with
@@ -86,9 +87,9 @@ __device__ __forceinline__ Entry entry_of(const FwdArgs &a, int e) {
     const WinProblem &p = a.p;
     Entry x;
     x.b = e % p.B;
-    x.i0 = (a.npairs - 1 - e / p.B) * 256;
+    x.i0 = (a.npairs - 1 - e / p.B) * 128 * a.tiles;
     x.seq = sequence(p, x.b);
-    x.kt = key_tiles<64>(p, x.seq, x.i0, x.i0 + 256);
+    x.kt = key_tiles<64>(p, x.seq, x.i0, x.i0 + 128 * a.tiles);
     return x;
 }
 
@@ -101,7 +102,7 @@ struct Segment {
         unit = r.unit;
         h = unit - e * a.p.H;
         b = e % a.p.B;
-        i0 = (a.npairs - 1 - e / a.p.B) * 256;
+        i0 = (a.npairs - 1 - e / a.p.B) * 128 * a.tiles;
         first = r.first;
         nh = r.nh;
         turn = r.sinks - first;   // blocks before it are the sinks', the others lie
@@ -229,9 +230,9 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             mbar_init(q_full + t, 1);
             mbar_init(q_empty + t, 1);
             mbar_init(k_full + t, 1);
-            mbar_init(k_empty + t, 2);
+            mbar_init(k_empty + t, a.tiles);
             mbar_init(v_full + t, 1);
-            mbar_init(v_empty + t, 2);
+            mbar_init(v_empty + t, a.tiles);
             for (int b = 0; b < 2; b++) {
                 mbar_init(s_full + 2 * t + b, 1);
                 mbar_init(p_full + 2 * t + b, 4);
@@ -241,7 +242,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             mbar_init(o_free + t, 4);
             mbar_init(l_full + t, 4);
         }
-        mbar_init(mma_done, 2);
+        mbar_init(mma_done, a.tiles);
         mbar_init(stall_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -289,7 +290,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             for (int si = 0; ok && si < nseg; si++) {
                 const Segment sg(a, list[si]);
                 if (sg.nh == 0) continue;
-                for (int t = 0; t < 2; t++) {
+                for (int t = 0; t < a.tiles; t++) {
                     if (pc > 0 && !wait_warp(q_empty + t, (pc - 1) & 1, w)) {
                         ok = false;
                         break;
@@ -327,7 +328,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             // tile t uses S buffer hc & 1.  Order: S of the first two halves, then per
             // half PV(hc), S(hc + 2).  S(hc + 2) overwrites the columns that PV(hc)
             // reads as P: one thread's products execute in issue order.
-            if (elect_one()) {
+            if (warp - 13 < 2 * a.tiles - 1 && elect_one()) {
             const int t = warp == 13 ? 0 : 1;
             constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0);
             constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
@@ -408,7 +409,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int si = 0; ok && si < nseg; si++) {
             const Segment sg(a, list[si]);
             if (sg.nh == 0) continue;
-            for (int t = 0; t < 2; t++) {
+            for (int t = 0; t < a.tiles; t++) {
                 if (!wait_warp(o_full + t, pc & 1, w) || !wait_warp(l_full + t, pc & 1, w)) {
                     ok = false;
                     break;
@@ -475,9 +476,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             pc++;
         }
-    } else {
+    } else if (regs_inc<kSoftmaxRegs>(); (warp >> 2) < a.tiles) {
         // ---------------- softmax of tile t: one query row a thread
-        regs_inc<kSoftmaxRegs>();
         const int t = warp >> 2, wq = warp & 3;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const uint32_t tS0 = tmem + lane_off + t * 128;
@@ -489,7 +489,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         // rows of a pair that sees no key: zeros
         auto write_zeros = [&](int unit) {
             const int e = unit / p.H, h = unit % p.H, bb = e % p.B;
-            const int m = (a.npairs - 1 - e / p.B) * 256 + t * 128 + wq * 32 + lane;
+            const int m = (a.npairs - 1 - e / p.B) * 128 * a.tiles + t * 128 + wq * 32 + lane;
             if (m >= p.Nq) return;
             uint4 *row = reinterpret_cast<uint4 *>(a.out + bb * p.o.batch + h * p.o.head +
                                                    (int64_t)m * p.o.token);
@@ -507,7 +507,11 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             const int m = sg.i0 + t * 128 + wq * 32 + lane;
             const Sequence seq = sequence(p, sg.b);
-            const RowKeys rk = row_keys(p, seq, m);
+            // a row that is not real takes every key, so that its warp needs no masks (its
+            // sums touch nothing else), and its row sum goes out as 0
+            RowKeys rk = row_keys(p, seq, m);
+            const bool real = rk.hi > 0;
+            if (!real) rk = RowKeys{0, 0x7fffffff, 0};
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = 0; i < sg.nh; i++, hc++) {
                 const int b = hc & 1;
@@ -602,6 +606,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
             if (!ok) break;
             jc0 += (sg.nh + 1) / 2;
+            if (!real) m_run = -INFINITY, l_run = 0.f;
             if (!sg.whole()) {
                 float *dst = a.parts + (int64_t)sg.slot() * part_floats(D) + t * 128 + wq * 32 + lane;
                 dst[0] = m_run * c1;
@@ -745,9 +750,14 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
     const int sms = tcs::sm_count();
     FwdArgs a;
     a.p = p;
-    a.npairs = (p.Nq + 255) / 256;
+    a.line = use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms);
+    // A tile alone on its SM takes little more than half of a pair's time a key block
+    // (the two tiles share the exponentials' units), so where the pairs are fewer than
+    // the SMs single tiles finish sooner: two padded causal batches of 1023 tokens with 8
+    // heads 27 -> 18 us.
+    a.tiles = a.line || (p.Nq + 255) / 256 * p.B * p.H >= sms ? 2 : 1;
+    a.npairs = (p.Nq + 128 * a.tiles - 1) / (128 * a.tiles);
     a.nprob = a.npairs * p.B * p.H;
-    a.line = use_line(p, a.nprob, sms);
     a.meta = (int2 *)workspace;
     a.parts = (float *)((char *)workspace + meta_bytes(sms));
     a.out = (__nv_bfloat16 *)out;
