@@ -90,6 +90,11 @@ monarch_status status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK :
 // A pointer field whose target (lengths, starts) must be 4-byte aligned.
 bool aligned4(const void *p) { return aligned(p, 4); }
 
+// delta_i of every query row, at the front of the backward's workspace.
+size_t delta_bytes(const WinProblem &p) {
+    return ((size_t)p.B * p.H * p.Nq * sizeof(float) + 255) & ~(size_t)255;
+}
+
 // A workspace for a call that needs `need` bytes (none: anything goes).
 monarch_status check_workspace(size_t need, const void *workspace, size_t ws_bytes) {
     if (need == 0) return MONARCH_OK;
@@ -174,7 +179,8 @@ monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc *desc, const
 size_t monarch_window_attn_bwd_workspace_bytes(const monarch_window_desc *desc) {
     WinProblem p;
     if (validate_window(desc, &p) != MONARCH_OK) return 0;
-    return at_least_256((size_t)p.B * p.H * p.Nq * sizeof(float));   // delta
+    return at_least_256(delta_bytes(p) +
+                        (desc->dtype == MONARCH_BF16 ? win::tc_backward_bytes(p) : 0));
 }
 
 monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
@@ -211,7 +217,8 @@ monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
                                             (float *)dq, (float *)dk, (float *)dv, s));
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
-    return status_of(win::tc_backward(p, g, q, k, v, lse, delta, dout, dq, dk, dv, status,
+    return status_of(win::tc_backward(p, g, q, k, v, lse, delta, dout, dq, dk, dv,
+                                      (char *)workspace + delta_bytes(p), status,
                                       device_wait_limit(), s));
 }
 

@@ -72,6 +72,8 @@ struct BwdArgs {
     float *delta;   // of the rounded out; rows of few keys are written again (dq kernel)
     const __nv_bfloat16 *q, *dout;
     __nv_bfloat16 *dq, *dk, *dv;
+    int splits;     // parts of a key tile's query blocks, a CTA each (dkv)
+    float *parts;   // splits > 1: [key tile, batch, head][split][128][dV | dK of D]
     int *status;
     long long limit;
     int stall;
@@ -102,6 +104,18 @@ __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16 *dst, fl
                            pack_bf16(o[8 * e + 2] * scale, o[8 * e + 3] * scale),
                            pack_bf16(o[8 * e + 4] * scale, o[8 * e + 5] * scale),
                            pack_bf16(o[8 * e + 6] * scale, o[8 * e + 7] * scale));
+    }
+}
+// N columns of an accumulator row as they are.
+template <int N> __device__ __forceinline__ void store_part(uint32_t taddr, float *dst) {
+#pragma unroll 1
+    for (int c = 0; c < N; c += 16) {
+        float o[16];
+        tmem_ld16f(taddr + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4 *>(dst + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
     }
 }
 __device__ __forceinline__ void zero_row(__nv_bfloat16 *dst, int n) {
@@ -264,17 +278,25 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (the first key tiles first: they are seen by the most queries under a causal mask)
-    const int unit = blockIdx.x % (p.B * p.Hkv), hk = unit % p.Hkv, b = unit / p.Hkv;
-    const int j0 = blockIdx.x / (p.B * p.Hkv) * 128;
+    const int tile_unit = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int unit = tile_unit % (p.B * p.Hkv), hk = unit % p.Hkv, b = unit / p.Hkv;
+    const int j0 = tile_unit / (p.B * p.Hkv) * 128;
     const Sequence seq = sequence(p, b);
     int first, last;
     query_rows(p, seq, j0, j0 + 128, first, last);
     const int t0 = first / 64, nt = last > first ? (last + 63) / 64 - t0 : 0;
-    const int n = nt * p.G;   // query blocks over the group's heads
+    // query blocks over the group's heads; this CTA's
+    const int u0 = (int)((int64_t)nt * p.G * split / a.splits);
+    const int n = (int)((int64_t)nt * p.G * (split + 1) / a.splits) - u0;
+    // (row of this CTA's part: dV, then dK, in 32 bits)
+    float *const part_base = a.parts + (int64_t)blockIdx.x * 128 * 2 * D;
 
     if (n == 0) {             // no query sees these keys (the same for the whole CTA)
         const int j = j0 + threadIdx.x;
-        if (threadIdx.x < 128 && j < p.Nk) {
+        if (a.splits > 1) {
+            for (int x = threadIdx.x; x < 128 * 2 * D / 4; x += kThreads)
+                reinterpret_cast<float4 *>(part_base)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (threadIdx.x < 128 && j < p.Nk) {
             zero_row(a.dk + b * a.g.dk.batch + hk * a.g.dk.head + (int64_t)j * a.g.dk.token, p.d);
             zero_row(a.dv + b * a.g.dv.batch + hk * a.g.dv.head + (int64_t)j * a.g.dv.token, p.d);
         }
@@ -288,8 +310,8 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
     const uint32_t tmem = bar->tmem_slot;
     const WaitCtx w{a.limit, a.status, &bar->abort_flag};
     auto coords = [&](int u, int &h, int &row) {
-        h = hk * p.G + u / nt;
-        row = (t0 + u % nt) * 64;
+        h = hk * p.G + (u0 + u) / nt;
+        row = (t0 + (u0 + u) % nt) * 64;
     };
 
     constexpr uint32_t idS = idesc_bf16(128, 64, 0, 0), idO = idesc_bf16(128, D, 0, 1);
@@ -406,7 +428,7 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         real_rows(p, seq, 0, p.Nq, rfirst, rlast);
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
         bool ok = true;
-        int x0 = half % nt;   // block of its head
+        int x0 = (u0 + half) % nt;   // block of its head
         for (int u = half; u < n; u += 2) {
             const int ph = (u >> 1) & 1, s1 = u % N1, c0 = (t0 + x0) * 64 + 32 * part;
             x0 += 2;
@@ -471,12 +493,18 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
             constexpr int W = D / 4;
             const int64_t x = (half * 2 + part) * W;
             const bool real = j < p.Nk;
+            if (a.splits > 1) {
+                float *dst = part_base + row * 2 * D + x;
+                store_part<W>(lanes + 256 + x, dst);
+                store_part<W>(lanes + 384 + x, dst + D);
+            } else {
             store_row<W>(lanes + 256 + x,
                          a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
                          p.d - (int)x, real, key);
             store_row<W>(lanes + 384 + x,
                          a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x, p.scale,
                          p.d - (int)x, real, key);
+            }
         }
     }
     tc_fence_before();
@@ -485,6 +513,33 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// dk and dv from the parts of each key tile's query blocks, added in order.
+template <int D>
+__global__ void __launch_bounds__(256) window_dkv_join_kernel(BwdArgs a) {
+    const WinProblem &p = a.p;
+    const int tile_unit = blockIdx.x, unit = tile_unit % (p.B * p.Hkv);
+    const int hk = unit % p.Hkv, b = unit / p.Hkv, j0 = tile_unit / (p.B * p.Hkv) * 128;
+    const Sequence seq = sequence(p, b);
+    const float *base = a.parts + (int64_t)tile_unit * a.splits * 128 * 2 * D;
+    const int at = blockIdx.y * 256 + threadIdx.x;   // 4 columns of a row
+    const int row = at / (2 * D / 4), x = at % (2 * D / 4) * 4, j = j0 + row;
+    const bool is_k = x >= D;
+    const int col = is_k ? x - D : x;
+    if (j >= p.Nk || col >= p.d) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < seq.len)
+        for (int s = 0; s < a.splits; s++) {
+            const float4 y = *reinterpret_cast<const float4 *>(base + ((int64_t)s * 128 + row) * 2 * D + x);
+            sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+        }
+    const float f = is_k ? p.scale : 1.f;
+    __nv_bfloat16 *dst =
+        is_k ? a.dk + b * a.g.dk.batch + hk * a.g.dk.head + (int64_t)j * a.g.dk.token
+             : a.dv + b * a.g.dv.batch + hk * a.g.dv.head + (int64_t)j * a.g.dv.token;
+    *reinterpret_cast<uint2 *>(dst + col) =
+        make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
 }
 
 // ---------------------------------------------------------------- dq
@@ -706,23 +761,47 @@ cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const 
     cudaError_t e = tcs::set_smem(tc_window_dkv_kernel<D>, smem_dkv);
     if (e == cudaSuccess) e = tcs::set_smem(tc_window_dq_kernel<D>, smem_dq);
     if (e != cudaSuccess) return e;
-    const unsigned gk = (unsigned)p.B * p.Hkv * ((p.Nk + 127) / 128);
+    const unsigned key_tiles = (unsigned)p.B * p.Hkv * ((p.Nk + 127) / 128);
+    const unsigned gk = key_tiles * a.splits;
     const unsigned gq = (unsigned)p.B * p.H * ((p.Nq + 127) / 128);
     // dq first: it completes delta
     tc_window_dq_kernel<D><<<gq, kThreads, smem_dq, stream>>>(k64, v64, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     tc_window_dkv_kernel<D><<<gk, kThreads, smem_dkv, stream>>>(q64, k128, v128, d64, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.splits == 1) return e;
+    window_dkv_join_kernel<D><<<dim3(key_tiles, 128 * 2 * D / 4 / 256), 256, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+// Parts of a key tile's query blocks in the dk/dv kernel: where the key tiles are fewer
+// than the SMs, as many as fill them, of eight blocks at least (a part's prologue, its
+// store and the join cost about four).  Two causal sequences of 1023 tokens, 8 heads on 2
+// key heads, d = 64: 32 tiles of up to 64 blocks, 49 us whole.
+int dkv_splits(const WinProblem &p) {
+    const int64_t tiles = (int64_t)p.B * p.Hkv * ((p.Nk + 127) / 128);
+    const int64_t blocks = (int64_t)((p.Nq + 63) / 64) * p.G;
+    const int64_t fill = tcs::sm_count() / tiles;
+    return (int)max((int64_t)1, min(fill, blocks / 8));
 }
 
 }  // namespace
 
+size_t tc_backward_bytes(const WinProblem &p) {
+    const int splits = dkv_splits(p);
+    if (splits == 1) return 0;
+    const size_t tiles = (size_t)p.B * p.Hkv * ((p.Nk + 127) / 128);
+    return tiles * splits * 128 * 2 * (p.d == 128 ? 128 : 64) * sizeof(float);
+}
+
 cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
                         const void *v, const float *lse, float *delta, const void *dout,
-                        void *dq, void *dk, void *dv, int *status, long long limit,
+                        void *dq, void *dk, void *dv, void *parts, int *status, long long limit,
                         cudaStream_t stream) {
     BwdArgs a;
+    a.splits = dkv_splits(p);
+    a.parts = (float *)parts;
     a.p = p;
     a.g = g;
     a.lse = lse;

@@ -158,9 +158,10 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
                        float *lse, void *workspace, int *status, long long limit,
                        cudaStream_t stream);
 
+size_t tc_backward_bytes(const WinProblem &p);   // of `parts`, 0 where none are needed
 cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
                         const void *v, const float *lse, float *delta, const void *dout,
-                        void *dq, void *dk, void *dv, int *status, long long limit,
+                        void *dq, void *dk, void *dv, void *parts, int *status, long long limit,
                         cudaStream_t stream);
 
 }  // namespace win

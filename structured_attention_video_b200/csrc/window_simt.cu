@@ -2,9 +2,9 @@
 // and backward (float32 inputs; the tensor cores round operands to fewer bits), and
 // the row sums delta = dO.O of both types' backward.
 //
-// One CTA of 256 threads takes 64 rows of one side (queries; keys for dk and dv)
+// One CTA of 256 threads takes 16 RT rows of one side (queries; keys for dk and dv)
 // and walks tiles of the other side.  Thread (ty, tx) of a 16 x 16 grid owns rows
-// 4 ty .. 4 ty + 3: in the logit products columns tx, tx + 16, ..., in the
+// RT ty .. RT ty + RT - 1: in the logit products columns tx, tx + 16, ..., in the
 // accumulating products d/16 columns of the head dimension.  The products run on
 // packed pairs of float32 (fma.rn.f32x2).  The 16 threads of a row are half a warp,
 // so softmax rows reduce with shuffles and the probabilities pass from the first
@@ -24,7 +24,6 @@ using tc::f2_pack;
 using tc::f2_unpack;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRows = 64;
 
 // Shared-memory row of D floats, padded so that 16-byte reads of 8 consecutive rows
 // cover all banks.
@@ -45,27 +44,27 @@ __device__ __forceinline__ void load_rows(float *sm, const float *base, int64_t 
     }
 }
 
-// s[i][j] = row (4 ty + i) of a . row (tx + 16 j) of b.
-template <int D, int NC>
+// s[i][j] = row (RT ty + i) of a . row (tx + 16 j) of b.
+template <int D, int RT, int NC>
 __device__ __forceinline__ void dot_tile(const float *a, const float *b, int ty, int tx,
-                                         float (&s)[4][NC]) {
-    uint64_t acc[4][NC];
+                                         float (&s)[RT][NC]) {
+    uint64_t acc[RT][NC];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < RT; i++)
 #pragma unroll
         for (int j = 0; j < NC; j++) acc[i][j] = 0;
-    const float *ap = a + 4 * ty * kPitch<D>, *bp = b + tx * kPitch<D>;
+    const float *ap = a + RT * ty * kPitch<D>, *bp = b + tx * kPitch<D>;
 #pragma unroll 4
     for (int x = 0; x < D; x += 4) {
-        ulonglong2 av[4], bv[NC];
+        ulonglong2 av[RT], bv[NC];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < RT; i++)
             av[i] = *reinterpret_cast<const ulonglong2 *>(ap + i * kPitch<D> + x);
 #pragma unroll
         for (int j = 0; j < NC; j++)
             bv[j] = *reinterpret_cast<const ulonglong2 *>(bp + j * 16 * kPitch<D> + x);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int j = 0; j < NC; j++) {
                 acc[i][j] = f2_fma(av[i].x, bv[j].x, acc[i][j]);
@@ -73,7 +72,7 @@ __device__ __forceinline__ void dot_tile(const float *a, const float *b, int ty,
             }
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < RT; i++)
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             float lo, hi;
@@ -84,16 +83,16 @@ __device__ __forceinline__ void dot_tile(const float *a, const float *b, int ty,
 
 // Columns of the head dimension that thread tx owns: pair q of D/32 covers
 // columns 2 tx + 32 q and the next.
-// o[i][q] += sum over the C columns of w of w[4 ty + i][c] * b[c][columns].
-template <int D, int C, int PW>
+// o[i][q] += sum over the C columns of w of w[RT ty + i][c] * b[c][columns].
+template <int D, int RT, int C, int PW>
 __device__ __forceinline__ void add_product(const float *w, const float *b, int ty, int tx,
-                                            uint64_t (&o)[4][D / 32]) {
-    const float *wp = w + 4 * ty * PW, *bp = b + 2 * tx;
+                                            uint64_t (&o)[RT][D / 32]) {
+    const float *wp = w + RT * ty * PW, *bp = b + 2 * tx;
 #pragma unroll 2
     for (int c = 0; c < C; c += 4) {
-        float4 wv[4];
+        float4 wv[RT];
 #pragma unroll
-        for (int i = 0; i < 4; i++) wv[i] = *reinterpret_cast<const float4 *>(wp + i * PW + c);
+        for (int i = 0; i < RT; i++) wv[i] = *reinterpret_cast<const float4 *>(wp + i * PW + c);
 #pragma unroll
         for (int cc = 0; cc < 4; cc++) {
             uint64_t bv[D / 32];
@@ -101,7 +100,7 @@ __device__ __forceinline__ void add_product(const float *w, const float *b, int 
             for (int q = 0; q < D / 32; q++)
                 bv[q] = *reinterpret_cast<const uint64_t *>(bp + (c + cc) * kPitch<D> + 32 * q);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < RT; i++) {
                 const float x = cc == 0 ? wv[i].x : cc == 1 ? wv[i].y : cc == 2 ? wv[i].z : wv[i].w;
                 const uint64_t xx = f2_pack(x, x);
 #pragma unroll
@@ -111,13 +110,13 @@ __device__ __forceinline__ void add_product(const float *w, const float *b, int 
     }
 }
 
-template <int D>
+template <int D, int RT>
 __device__ __forceinline__ void store_rows(float *base, int64_t stride, int r0, int valid, int ty,
-                                           int tx, const uint64_t (&o)[4][D / 32],
-                                           const float (&scale)[4]) {
+                                           int tx, const uint64_t (&o)[RT][D / 32],
+                                           const float (&scale)[RT]) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = r0 + 4 * ty + i;
+    for (int i = 0; i < RT; i++) {
+        const int r = r0 + RT * ty + i;
         if (r >= valid) continue;
 #pragma unroll
         for (int q = 0; q < D / 32; q++) {
@@ -141,34 +140,34 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 }
 
 // ---------------------------------------------------------------- forward
-// 64 queries of one head against tiles of 64 keys.  K and V take turns in one
+// 16 RT queries of one head against tiles of 64 keys.  K and V take turns in one
 // buffer, so that two CTAs fit on an SM at d = 128 and one computes while the
 // other loads.
-template <int D>
+template <int D, int RT>
 constexpr int fwd_smem() {
-    return (2 * kRows * kPitch<D> + kRows * 68) * 4;
+    return ((16 * RT + 64) * kPitch<D> + 16 * RT * 68) * 4;
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, float *out,
                 float *lse) {
     extern __shared__ __align__(16) float smf[];
-    float *sq = smf, *skv = smf + kRows * kPitch<D>, *sp = skv + kRows * kPitch<D>;
+    float *sq = smf, *skv = smf + 16 * RT * kPitch<D>, *sp = skv + 64 * kPitch<D>;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
-    const int i0 = blockIdx.x * kRows;
+    const int i0 = blockIdx.x * (16 * RT);
     const Sequence seq = sequence(p, b);
-    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + kRows);
+    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + (16 * RT));
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, kRows>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
-    RowKeys rk[4];
-    float m[4], l[4];
-    uint64_t o[4][D / 32];
+    load_rows<D, (16 * RT)>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    RowKeys rk[RT];
+    float m[RT], l[RT];
+    uint64_t o[RT][D / 32];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        rk[i] = row_keys(p, seq, i0 + 4 * ty + i);
+    for (int i = 0; i < RT; i++) {
+        rk[i] = row_keys(p, seq, i0 + RT * ty + i);
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -179,10 +178,10 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
         __syncthreads();   // the buffer's last readers are done
         load_rows<D, 64>(skv, kb, p.k.token, j0, seq.len);
         __syncthreads();
-        float s[4][4];
-        dot_tile<D, 4>(sq, skv, ty, tx, s);
+        float s[RT][4];
+        dot_tile<D, RT, 4>(sq, skv, ty, tx, s);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < RT; i++) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -198,7 +197,7 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
             for (int j = 0; j < 4; j++) {
                 const float e = exp2f(s[i][j] - safe);
                 sum += e;
-                sp[(4 * ty + i) * 68 + tx + 16 * j] = e;
+                sp[(RT * ty + i) * 68 + tx + 16 * j] = e;
             }
             l[i] = l[i] * alpha + sum;   // this thread's columns; joined at the end
             m[i] = mx;
@@ -209,52 +208,52 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
         __syncthreads();   // K is read
         load_rows<D, 64>(skv, vb, p.v.token, j0, seq.len);
         __syncthreads();
-        add_product<D, 64, 68>(sp, skv, ty, tx, o);
+        add_product<D, RT, 64, 68>(sp, skv, ty, tx, o);
     }
-    float inv[4];
+    float inv[RT];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < RT; i++) {
         const float total = half_warp_sum(l[i]);
         inv[i] = total > 0.f ? 1.f / total : 0.f;
         if (total != total) inv[i] = total;   // NaN inputs stay visible
-        const int r = i0 + 4 * ty + i;
+        const int r = i0 + RT * ty + i;
         if (lse && tx == 0 && r < p.Nq)
             lse[((int64_t)b * p.H + h) * p.Nq + r] =
                 total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
     }
-    store_rows<D>(out + b * p.o.batch + h * p.o.head, p.o.token, i0, p.Nq, ty, tx, o, inv);
+    store_rows<D, RT>(out + b * p.o.batch + h * p.o.head, p.o.token, i0, p.Nq, ty, tx, o, inv);
 }
 
 // ---------------------------------------------------------------- backward
-// dq: 64 queries against tiles of 32 keys.  dS = P (dO.V - delta) with
+// dq: 16 RT queries against tiles of 32 keys.  dS = P (dO.V - delta) with
 // P = exp(S - lse); dq = scale * dS K.
-template <int D>
+template <int D, int RT>
 constexpr int dq_smem() {
-    return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
+    return ((2 * (16 * RT) + 2 * 32) * kPitch<D> + (16 * RT) * 36) * 4;
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
                const float *lse, const float *delta, const float *dout, float *dq) {
     extern __shared__ __align__(16) float smf[];
-    float *sq = smf, *sdo = sq + kRows * kPitch<D>, *sk = sdo + kRows * kPitch<D>;
+    float *sq = smf, *sdo = sq + (16 * RT) * kPitch<D>, *sk = sdo + (16 * RT) * kPitch<D>;
     float *sv = sk + 32 * kPitch<D>, *sds = sv + 32 * kPitch<D>;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
-    const int i0 = blockIdx.x * kRows;
+    const int i0 = blockIdx.x * (16 * RT);
     const Sequence seq = sequence(p, b);
-    const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + kRows);
+    const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + (16 * RT));
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, kRows>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
-    load_rows<D, kRows>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
-    RowKeys rk[4];
-    float lm[4], dl[4];
-    uint64_t o[4][D / 32];
+    load_rows<D, (16 * RT)>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    load_rows<D, (16 * RT)>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
+    RowKeys rk[RT];
+    float lm[RT], dl[RT];
+    uint64_t o[RT][D / 32];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = i0 + 4 * ty + i;
+    for (int i = 0; i < RT; i++) {
+        const int r = i0 + RT * ty + i;
         rk[i] = row_keys(p, seq, r);
         const int64_t at = ((int64_t)b * p.H + h) * p.Nq + r;
         lm[i] = r < p.Nq ? lse[at] * (1.f / kLn2) : 0.f;
@@ -268,49 +267,51 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
         load_rows<D, 32>(sk, kb, p.k.token, j0, seq.len);
         load_rows<D, 32>(sv, vb, p.v.token, j0, seq.len);
         __syncthreads();
-        float s[4][2], dp[4][2];
-        dot_tile<D, 2>(sq, sk, ty, tx, s);
-        dot_tile<D, 2>(sdo, sv, ty, tx, dp);
+        float s[RT][2], dp[RT][2];
+        dot_tile<D, RT, 2>(sq, sk, ty, tx, s);
+        dot_tile<D, RT, 2>(sdo, sv, ty, tx, dp);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const float e = exp2f(fmaf(s[i][j], p.scale_log2, -lm[i]));
-                sds[(4 * ty + i) * 36 + tx + 16 * j] =
+                sds[(RT * ty + i) * 36 + tx + 16 * j] =
                     rk[i].sees(j0 + tx + 16 * j) ? e * (dp[i][j] - dl[i]) : 0.f;
             }
         __syncwarp();
-        add_product<D, 32, 36>(sds, sk, ty, tx, o);
+        add_product<D, RT, 32, 36>(sds, sk, ty, tx, o);
     }
-    const float sc[4] = {p.scale, p.scale, p.scale, p.scale};
-    store_rows<D>(dq + b * g.dq.batch + h * g.dq.head, g.dq.token, i0, p.Nq, ty, tx, o, sc);
+    float sc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; i++) sc[i] = p.scale;
+    store_rows<D, RT>(dq + b * g.dq.batch + h * g.dq.head, g.dq.token, i0, p.Nq, ty, tx, o, sc);
 }
 
-// dk, dv: 64 keys of one key head against tiles of 32 queries of every head of its
+// dk, dv: 16 RT keys of one key head against tiles of 32 queries of every head of its
 // group.  dv += P^T dO, dk += dS^T q (times scale at the end).
-template <int D>
+template <int D, int RT>
 constexpr int dkv_smem() {
-    return ((2 * kRows + 2 * 32) * kPitch<D> + kRows * 36) * 4;
+    return ((2 * (16 * RT) + 2 * 32) * kPitch<D> + (16 * RT) * 36) * 4;
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
                 const float *lse, const float *delta, const float *dout, float *dk, float *dv) {
     extern __shared__ __align__(16) float smf[];
-    float *sk = smf, *sv = sk + kRows * kPitch<D>, *sq = sv + kRows * kPitch<D>;
+    float *sk = smf, *sv = sk + (16 * RT) * kPitch<D>, *sq = sv + (16 * RT) * kPitch<D>;
     float *sdo = sq + 32 * kPitch<D>, *sw = sdo + 32 * kPitch<D>;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int hk = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv;
-    const int j0 = blockIdx.x * kRows;
+    const int j0 = blockIdx.x * (16 * RT);
     const Sequence seq = sequence(p, b);
     int first, last;
-    query_rows(p, seq, j0, j0 + kRows, first, last);
-    load_rows<D, kRows>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);
-    load_rows<D, kRows>(sv, v + b * p.v.batch + hk * p.v.head, p.v.token, j0, seq.len);
-    uint64_t ok[4][D / 32], ov[4][D / 32];
+    query_rows(p, seq, j0, j0 + (16 * RT), first, last);
+    load_rows<D, (16 * RT)>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);
+    load_rows<D, (16 * RT)>(sv, v + b * p.v.batch + hk * p.v.head, p.v.token, j0, seq.len);
+    uint64_t ok[RT][D / 32], ov[RT][D / 32];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < RT; i++)
 #pragma unroll
         for (int x = 0; x < D / 32; x++) ok[i][x] = ov[i][x] = 0;
     int rfirst, rlast;
@@ -326,9 +327,9 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
             load_rows<D, 32>(sq, qb, p.q.token, i0, rlast);
             load_rows<D, 32>(sdo, db, g.dout.token, i0, rlast);
             __syncthreads();
-            float s[4][2], dp[4][2];
-            dot_tile<D, 2>(sk, sq, ty, tx, s);
-            dot_tile<D, 2>(sv, sdo, ty, tx, dp);
+            float s[RT][2], dp[RT][2];
+            dot_tile<D, RT, 2>(sk, sq, ty, tx, s);
+            dot_tile<D, RT, 2>(sv, sdo, ty, tx, dp);
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 const int i = i0 + tx + 16 * c;
@@ -337,28 +338,30 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
                 const float lm = real ? lse[row + i] * (1.f / kLn2) : 0.f;
                 const float dl = real ? delta[row + i] : 0.f;
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const bool see = rk.sees(j0 + 4 * ty + r);
+                for (int r = 0; r < RT; r++) {
+                    const bool see = rk.sees(j0 + RT * ty + r);
                     const float e = see ? exp2f(fmaf(s[r][c], p.scale_log2, -lm)) : 0.f;
                     s[r][c] = e;
                     dp[r][c] = see ? e * (dp[r][c] - dl) : 0.f;
-                    sw[(4 * ty + r) * 36 + tx + 16 * c] = e;
+                    sw[(RT * ty + r) * 36 + tx + 16 * c] = e;
                 }
             }
             __syncwarp();
-            add_product<D, 32, 36>(sw, sdo, ty, tx, ov);
+            add_product<D, RT, 32, 36>(sw, sdo, ty, tx, ov);
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < 2; c++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) sw[(4 * ty + r) * 36 + tx + 16 * c] = dp[r][c];
+                for (int r = 0; r < RT; r++) sw[(RT * ty + r) * 36 + tx + 16 * c] = dp[r][c];
             __syncwarp();
-            add_product<D, 32, 36>(sw, sq, ty, tx, ok);
+            add_product<D, RT, 32, 36>(sw, sq, ty, tx, ok);
         }
     }
-    const float sc[4] = {p.scale, p.scale, p.scale, p.scale}, one[4] = {1.f, 1.f, 1.f, 1.f};
-    store_rows<D>(dk + b * g.dk.batch + hk * g.dk.head, g.dk.token, j0, p.Nk, ty, tx, ok, sc);
-    store_rows<D>(dv + b * g.dv.batch + hk * g.dv.head, g.dv.token, j0, p.Nk, ty, tx, ov, one);
+    float sc[RT], one[RT];
+#pragma unroll
+    for (int i = 0; i < RT; i++) sc[i] = p.scale, one[i] = 1.f;
+    store_rows<D, RT>(dk + b * g.dk.batch + hk * g.dk.head, g.dk.token, j0, p.Nk, ty, tx, ok, sc);
+    store_rows<D, RT>(dv + b * g.dv.batch + hk * g.dv.head, g.dv.token, j0, p.Nk, ty, tx, ov, one);
 }
 
 // ---------------------------------------------------------------- delta
@@ -421,30 +424,70 @@ cudaError_t allow_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Rows a thread: 4 (tiles of 64 rows) for the arithmetic per shared-memory read, fewer
+// while the tiles leave SMs without a CTA, since each then walks its keys in less time:
+// 4 heads of 780 tokens, 255 keys a row, d = 64, forward and backward 157 us at 4.
+int rows_a_thread(int64_t heads, int rows) {
+    for (int rt = 4; rt > 1; rt /= 2)
+        if (heads * ((rows + 16 * rt - 1) / (16 * rt)) >= 148) return rt;
+    return 1;
+}
+
+template <int D, int RT>
+cudaError_t forward_rt(const WinProblem &p, const float *q, const float *k, const float *v,
+                       float *out, float *lse, cudaStream_t stream) {
+    constexpr int smem = fwd_smem<D, RT>();
+    cudaError_t e = allow_smem(simt_fwd_kernel<D, RT>, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H);
+    simt_fwd_kernel<D, RT><<<grid, 256, smem, stream>>>(p, q, k, v, out, lse);
+    return cudaGetLastError();
+}
+template <int D, int RT>
+cudaError_t dq_rt(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
+                  const float *v, const float *lse, const float *delta, const float *dout,
+                  float *dq, cudaStream_t stream) {
+    constexpr int smem = dq_smem<D, RT>();
+    cudaError_t e = allow_smem(simt_dq_kernel<D, RT>, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H);
+    simt_dq_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dq);
+    return cudaGetLastError();
+}
+template <int D, int RT>
+cudaError_t dkv_rt(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
+                   const float *v, const float *lse, const float *delta, const float *dout,
+                   float *dk, float *dv, cudaStream_t stream) {
+    constexpr int smem = dkv_smem<D, RT>();
+    cudaError_t e = allow_smem(simt_dkv_kernel<D, RT>, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.Nk + 16 * RT - 1) / (16 * RT), p.B * p.Hkv);
+    simt_dkv_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
+    return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const float *v,
                       float *out, float *lse, cudaStream_t stream) {
-    cudaError_t e = allow_smem(simt_fwd_kernel<D>, fwd_smem<D>());
-    if (e != cudaSuccess) return e;
-    const dim3 grid((p.Nq + kRows - 1) / kRows, p.B * p.H);
-    simt_fwd_kernel<D><<<grid, 256, fwd_smem<D>(), stream>>>(p, q, k, v, out, lse);
-    return cudaGetLastError();
+    const int rt = rows_a_thread((int64_t)p.B * p.H, p.Nq);
+    if (rt == 4) return forward_rt<D, 4>(p, q, k, v, out, lse, stream);
+    if (rt == 2) return forward_rt<D, 2>(p, q, k, v, out, lse, stream);
+    return forward_rt<D, 1>(p, q, k, v, out, lse, stream);
 }
 
 template <int D>
 cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                        const float *v, const float *lse, const float *delta, const float *dout,
                        float *dq, float *dk, float *dv, cudaStream_t stream) {
-    cudaError_t e = allow_smem(simt_dq_kernel<D>, dq_smem<D>());
-    if (e == cudaSuccess) e = allow_smem(simt_dkv_kernel<D>, dkv_smem<D>());
+    const int rq = rows_a_thread((int64_t)p.B * p.H, p.Nq);
+    const cudaError_t e = rq == 4   ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, stream)
+                          : rq == 2 ? dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, stream)
+                                    : dq_rt<D, 1>(p, g, q, k, v, lse, delta, dout, dq, stream);
     if (e != cudaSuccess) return e;
-    const dim3 gq((p.Nq + kRows - 1) / kRows, p.B * p.H);
-    simt_dq_kernel<D><<<gq, 256, dq_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dq);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const dim3 gk((p.Nk + kRows - 1) / kRows, p.B * p.Hkv);
-    simt_dkv_kernel<D><<<gk, 256, dkv_smem<D>(), stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
-    return cudaGetLastError();
+    const int rk = rows_a_thread((int64_t)p.B * p.Hkv, p.Nk);
+    if (rk == 4) return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
+    if (rk == 2) return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
+    return dkv_rt<D, 1>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
 }
 
 }  // namespace
