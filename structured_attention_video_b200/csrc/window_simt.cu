@@ -29,20 +29,31 @@ constexpr float kLn2 = 0.6931471805599453f;
 // cover all banks.
 template <int D> constexpr int kPitch = D + 4;
 
-// Rows [r0, r0 + R) of a [tokens][D] matrix into shared memory; rows outside
-// [0, valid) become zero.
+// Rows [r0, r0 + R) of a [tokens][D] matrix into shared memory, asynchronously (16-byte
+// copies of one group per thread); rows outside [0, valid) become zero.
 template <int D, int R>
 __device__ __forceinline__ void load_rows(float *sm, const float *base, int64_t stride, int r0,
                                           int valid) {
     constexpr int kChunks = D / 4;
     for (int i = threadIdx.x; i < R * kChunks; i += 256) {
         const int r = i / kChunks, c = i % kChunks;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < valid)
-            x = *reinterpret_cast<const float4 *>(base + (int64_t)(r0 + r) * stride + c * 4);
-        *reinterpret_cast<float4 *>(sm + r * kPitch<D> + c * 4) = x;
+        const bool in = r0 + r < valid;
+        const float *src = base + (in ? (int64_t)(r0 + r) * stride + c * 4 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         tc::smem_u32(sm + r * kPitch<D> + c * 4)),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
     }
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's copies have landed.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two stages of the streamed tiles, the next one's copies behind this one's arithmetic,
+// where two CTAs with them fit on an SM; at d = 128 two CTAs of one stage do instead.
+template <int D> constexpr int kStages = D == 128 ? 1 : 2;
 
 // s[i][j] = row (RT ty + i) of a . row (tx + 16 j) of b.
 template <int D, int RT, int NC>
@@ -140,12 +151,11 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 }
 
 // ---------------------------------------------------------------- forward
-// 16 RT queries of one head against tiles of 64 keys.  K and V take turns in one
-// buffer, so that two CTAs fit on an SM at d = 128 and one computes while the
-// other loads.
+// 16 RT queries of one head against tiles of 64 keys.  With one stage K and V take turns
+// in one buffer.
 template <int D, int RT>
 constexpr int fwd_smem() {
-    return ((16 * RT + 64) * kPitch<D> + 16 * RT * 68) * 4;
+    return ((16 * RT + 64 * (kStages<D> == 2 ? 4 : 1)) * kPitch<D> + 16 * RT * 68) * 4;
 }
 
 template <int D, int RT>
@@ -153,15 +163,25 @@ __global__ void __launch_bounds__(256, 2)
 simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, float *out,
                 float *lse) {
     extern __shared__ __align__(16) float smf[];
-    float *sq = smf, *skv = smf + 16 * RT * kPitch<D>, *sp = skv + 64 * kPitch<D>;
+    constexpr int kTileFloats = 64 * kPitch<D>;
+    float *sq = smf, *sp = sq + 16 * RT * kPitch<D>, *skv = sp + 16 * RT * 68;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
-    const int i0 = blockIdx.x * (16 * RT);
+    const int i0 = blockIdx.x * 16 * RT;
     const Sequence seq = sequence(p, b);
-    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + (16 * RT));
+    const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + 16 * RT);
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, (16 * RT)>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    auto load = [&](float *dst, const float *src, int64_t stride, int it) {
+        load_rows<D, 64>(dst, src, stride, kt.tile(it) * 64, seq.len);
+    };
+    const int n = kt.count();
+    if (kStages<D> == 2 && n > 0) {
+        load(skv, kb, p.k.token, 0);
+        load(skv + kTileFloats, vb, p.v.token, 0);
+    }
+    copies_commit();
     RowKeys rk[RT];
     float m[RT], l[RT];
     uint64_t o[RT][D / 32];
@@ -173,13 +193,28 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
 #pragma unroll
         for (int x = 0; x < D / 32; x++) o[i][x] = 0;
     }
-    for (int it = 0; it < kt.count(); it++) {
+    for (int it = 0; it < n; it++) {
         const int j0 = kt.tile(it) * 64;
+        const float *sk = skv, *sv = skv;
         __syncthreads();   // the buffer's last readers are done
-        load_rows<D, 64>(skv, kb, p.k.token, j0, seq.len);
+        if (kStages<D> == 2) {
+            float *next = skv + ((it + 1) & 1) * 2 * kTileFloats;
+            if (it + 1 < n) {
+                load(next, kb, p.k.token, it + 1);
+                load(next + kTileFloats, vb, p.v.token, it + 1);
+            }
+            copies_commit();
+            copies_wait<1>();
+            sk = skv + (it & 1) * 2 * kTileFloats;
+            sv = sk + kTileFloats;
+        } else {
+            load(skv, kb, p.k.token, it);
+            copies_commit();
+            copies_wait<0>();
+        }
         __syncthreads();
         float s[RT][4];
-        dot_tile<D, RT, 4>(sq, skv, ty, tx, s);
+        dot_tile<D, RT, 4>(sq, sk, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < RT; i++) {
             float mx = -INFINITY;
@@ -205,10 +240,16 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
 #pragma unroll
             for (int x = 0; x < D / 32; x++) o[i][x] = f2_mul(o[i][x], aa);
         }
-        __syncthreads();   // K is read
-        load_rows<D, 64>(skv, vb, p.v.token, j0, seq.len);
-        __syncthreads();
-        add_product<D, RT, 64, 68>(sp, skv, ty, tx, o);
+        if (kStages<D> == 2) {
+            __syncwarp();      // the row's probabilities come from its own half warp
+        } else {
+            __syncthreads();   // K is read
+            load(skv, vb, p.v.token, it);
+            copies_commit();
+            copies_wait<0>();
+            __syncthreads();
+        }
+        add_product<D, RT, 64, 68>(sp, sv, ty, tx, o);
     }
     float inv[RT];
 #pragma unroll
@@ -229,7 +270,7 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
 // P = exp(S - lse); dq = scale * dS K.
 template <int D, int RT>
 constexpr int dq_smem() {
-    return ((2 * (16 * RT) + 2 * 32) * kPitch<D> + (16 * RT) * 36) * 4;
+    return ((2 * 16 * RT + 2 * 32 * kStages<D>) * kPitch<D> + 16 * RT * 36) * 4;
 }
 
 template <int D, int RT>
@@ -237,8 +278,9 @@ __global__ void __launch_bounds__(256, 2)
 simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
                const float *lse, const float *delta, const float *dout, float *dq) {
     extern __shared__ __align__(16) float smf[];
-    float *sq = smf, *sdo = sq + (16 * RT) * kPitch<D>, *sk = sdo + (16 * RT) * kPitch<D>;
-    float *sv = sk + 32 * kPitch<D>, *sds = sv + 32 * kPitch<D>;
+    constexpr int kTileFloats = 32 * kPitch<D>;
+    float *sq = smf, *sdo = sq + 16 * RT * kPitch<D>, *sds = sdo + 16 * RT * kPitch<D>;
+    float *skv = sds + 16 * RT * 36;   // [stage][K, V]
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
     const int i0 = blockIdx.x * (16 * RT);
@@ -246,8 +288,16 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
     const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + (16 * RT));
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, (16 * RT)>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
-    load_rows<D, (16 * RT)>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
+    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    load_rows<D, 16 * RT>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
+    const int n = kt.count();
+    auto load = [&](int it) {
+        float *dst = skv + it % kStages<D> * 2 * kTileFloats;
+        load_rows<D, 32>(dst, kb, p.k.token, kt.tile(it) * 32, seq.len);
+        load_rows<D, 32>(dst + kTileFloats, vb, p.v.token, kt.tile(it) * 32, seq.len);
+    };
+    if (kStages<D> == 2 && n > 0) load(0);
+    copies_commit();
     RowKeys rk[RT];
     float lm[RT], dl[RT];
     uint64_t o[RT][D / 32];
@@ -261,11 +311,13 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
 #pragma unroll
         for (int x = 0; x < D / 32; x++) o[i][x] = 0;
     }
-    for (int it = 0; it < kt.count(); it++) {
+    for (int it = 0; it < n; it++) {
         const int j0 = kt.tile(it) * 32;
+        const float *sk = skv + it % kStages<D> * 2 * kTileFloats, *sv = sk + kTileFloats;
         __syncthreads();
-        load_rows<D, 32>(sk, kb, p.k.token, j0, seq.len);
-        load_rows<D, 32>(sv, vb, p.v.token, j0, seq.len);
+        if (it + kStages<D> - 1 < n) load(it + kStages<D> - 1);
+        copies_commit();
+        copies_wait<kStages<D> - 1>();
         __syncthreads();
         float s[RT][2], dp[RT][2];
         dot_tile<D, RT, 2>(sq, sk, ty, tx, s);
@@ -291,7 +343,7 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
 // group.  dv += P^T dO, dk += dS^T q (times scale at the end).
 template <int D, int RT>
 constexpr int dkv_smem() {
-    return ((2 * (16 * RT) + 2 * 32) * kPitch<D> + (16 * RT) * 36) * 4;
+    return ((2 * 16 * RT + 2 * 32 * kStages<D>) * kPitch<D> + 16 * RT * 36) * 4;
 }
 
 template <int D, int RT>
@@ -299,16 +351,17 @@ __global__ void __launch_bounds__(256, 2)
 simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
                 const float *lse, const float *delta, const float *dout, float *dk, float *dv) {
     extern __shared__ __align__(16) float smf[];
-    float *sk = smf, *sv = sk + (16 * RT) * kPitch<D>, *sq = sv + (16 * RT) * kPitch<D>;
-    float *sdo = sq + 32 * kPitch<D>, *sw = sdo + 32 * kPitch<D>;
+    constexpr int kTileFloats = 32 * kPitch<D>;
+    float *sk = smf, *sv = sk + 16 * RT * kPitch<D>, *sw = sv + 16 * RT * kPitch<D>;
+    float *sqd = sw + 16 * RT * 36;   // [stage][Q, dO]
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int hk = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv;
     const int j0 = blockIdx.x * (16 * RT);
     const Sequence seq = sequence(p, b);
     int first, last;
     query_rows(p, seq, j0, j0 + (16 * RT), first, last);
-    load_rows<D, (16 * RT)>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);
-    load_rows<D, (16 * RT)>(sv, v + b * p.v.batch + hk * p.v.head, p.v.token, j0, seq.len);
+    load_rows<D, 16 * RT>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);
+    load_rows<D, 16 * RT>(sv, v + b * p.v.batch + hk * p.v.head, p.v.token, j0, seq.len);
     uint64_t ok[RT][D / 32], ov[RT][D / 32];
 #pragma unroll
     for (int i = 0; i < RT; i++)
@@ -316,17 +369,28 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
         for (int x = 0; x < D / 32; x++) ok[i][x] = ov[i][x] = 0;
     int rfirst, rlast;
     real_rows(p, seq, 0, p.Nq, rfirst, rlast);
-    for (int gh = 0; gh < p.G; gh++) {
-        const int h = hk * p.G + gh;
-        const float *qb = q + b * p.q.batch + h * p.q.head;
-        const float *db = dout + b * g.dout.batch + h * g.dout.head;
-        const int64_t row = ((int64_t)b * p.H + h) * p.Nq;
-        for (int i0 = first / 32 * 32; i0 < last; i0 += 32) {
-            __syncthreads();
-            // rows behind the sequence's end enter as zeros, whatever they hold
-            load_rows<D, 32>(sq, qb, p.q.token, i0, rlast);
-            load_rows<D, 32>(sdo, db, g.dout.token, i0, rlast);
-            __syncthreads();
+    // tiles of 32 queries of every head of the group
+    const int t0 = first / 32, nt = last > first ? (last + 31) / 32 - t0 : 0, n = nt * p.G;
+    auto load = [&](int u) {
+        float *dst = sqd + u % kStages<D> * 2 * kTileFloats;
+        const int h = hk * p.G + u / nt, i0 = (t0 + u % nt) * 32;
+        // rows behind the sequence's end enter as zeros, whatever they hold
+        load_rows<D, 32>(dst, q + b * p.q.batch + h * p.q.head, p.q.token, i0, rlast);
+        load_rows<D, 32>(dst + kTileFloats, dout + b * g.dout.batch + h * g.dout.head, g.dout.token,
+                         i0, rlast);
+    };
+    if (kStages<D> == 2 && n > 0) load(0);
+    copies_commit();
+    for (int u = 0; u < n; u++) {
+        const int64_t row = ((int64_t)b * p.H + hk * p.G + u / nt) * p.Nq;
+        const int i0 = (t0 + u % nt) * 32;
+        const float *sq = sqd + u % kStages<D> * 2 * kTileFloats, *sdo = sq + kTileFloats;
+        __syncthreads();
+        if (u + kStages<D> - 1 < n) load(u + kStages<D> - 1);
+        copies_commit();
+        copies_wait<kStages<D> - 1>();
+        __syncthreads();
+        {
             float s[RT][2], dp[RT][2];
             dot_tile<D, RT, 2>(sk, sq, ty, tx, s);
             dot_tile<D, RT, 2>(sv, sdo, ty, tx, dp);
@@ -424,14 +488,12 @@ cudaError_t allow_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows a thread: 4 (tiles of 64 rows) for the arithmetic per shared-memory read, fewer
-// while the tiles leave SMs without a CTA, since each then walks its keys in less time:
-// 4 heads of 780 tokens, 255 keys a row, d = 64, forward and backward 157 us at 4.
-int rows_a_thread(int64_t heads, int rows) {
-    for (int rt = 4; rt > 1; rt /= 2)
-        if (heads * ((rows + 16 * rt - 1) / (16 * rt)) >= 148) return rt;
-    return 1;
-}
+// Rows a thread: 4 (tiles of 64 rows), or 2 where those tiles would leave SMs without a
+// CTA.  A tile's time is its shared-memory reads, most of them of the streamed side and
+// the same for any number of rows, next to the FMAs, which halve; with 1 row a thread two
+// CTAs share an SM's shared memory and take longer (4 heads of 780 tokens, 255 keys a row,
+// d = 64: forward 43 us at 4 rows, 33 at 1).
+int rows_a_thread(int64_t heads, int rows) { return heads * ((rows + 63) / 64) >= 148 ? 4 : 2; }
 
 template <int D, int RT>
 cudaError_t forward_rt(const WinProblem &p, const float *q, const float *k, const float *v,
@@ -471,8 +533,7 @@ cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const
                       float *out, float *lse, cudaStream_t stream) {
     const int rt = rows_a_thread((int64_t)p.B * p.H, p.Nq);
     if (rt == 4) return forward_rt<D, 4>(p, q, k, v, out, lse, stream);
-    if (rt == 2) return forward_rt<D, 2>(p, q, k, v, out, lse, stream);
-    return forward_rt<D, 1>(p, q, k, v, out, lse, stream);
+    return forward_rt<D, 2>(p, q, k, v, out, lse, stream);
 }
 
 template <int D>
@@ -480,14 +541,12 @@ cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, c
                        const float *v, const float *lse, const float *delta, const float *dout,
                        float *dq, float *dk, float *dv, cudaStream_t stream) {
     const int rq = rows_a_thread((int64_t)p.B * p.H, p.Nq);
-    const cudaError_t e = rq == 4   ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, stream)
-                          : rq == 2 ? dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, stream)
-                                    : dq_rt<D, 1>(p, g, q, k, v, lse, delta, dout, dq, stream);
+    const cudaError_t e = rq == 4 ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, stream)
+                                  : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, stream);
     if (e != cudaSuccess) return e;
     const int rk = rows_a_thread((int64_t)p.B * p.Hkv, p.Nk);
     if (rk == 4) return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
-    if (rk == 2) return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
-    return dkv_rt<D, 1>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
+    return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
 }
 
 }  // namespace
