@@ -22,21 +22,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T> struct Chunk;   // 16 bytes
+// 16 bytes of a row: as they are, and as floats.
+template <typename T> struct Chunk;
 template <> struct Chunk<float> {
     static constexpr int n = 4;
-    __device__ static __forceinline__ void load(const float *p, float (&x)[4]) {
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    __device__ static __forceinline__ void floats(const uint4 &v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
-    __device__ static __forceinline__ void store(float *p, const float (&x)[4]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    __device__ static __forceinline__ uint4 bits(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
     }
 };
 template <> struct Chunk<__nv_bfloat16> {
     static constexpr int n = 8;
-    __device__ static __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    __device__ static __forceinline__ void floats(const uint4 &v, float (&x)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -44,14 +45,14 @@ template <> struct Chunk<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
-    __device__ static __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+    __device__ static __forceinline__ uint4 bits(const float (&x)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -98,72 +99,87 @@ __device__ __forceinline__ void token_position(const RotaryProblem &p, int b, in
 
 // HALF: pairs (i, i + pairs), chunks of both halves in one thread; else pairs
 // (2 i, 2 i + 1) inside a chunk.  Items of a token: the rotated chunks, then the
-// chunks behind the rotated part, which are copied (or, in place, left alone).
+// chunks behind the rotated part, which are copied (or, in place, left alone).  A block has
+// `tokens` whole tokens.  The heads go in batches whose loads are issued together, the
+// first batch's before the sines and cosines are computed.
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads)
-rotary_kernel(RotaryProblem p, const T *q, const T *k, T *qo, T *ko) {
-    constexpr int V = Chunk<T>::n;
-    const int rotated = HALF ? p.pairs / V : (2 * p.pairs + V - 1) / V;
-    const int items = HALF ? rotated + (p.d - 2 * p.pairs) / V : p.d / V;
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= (int64_t)p.B * p.N * items) return;
-    const int item = (int)(id % items);
-    const int64_t tok = id / items;
-    const int n = (int)(tok % p.N), b = (int)(tok / p.N);
+rotary_kernel(RotaryProblem p, int items, int rotated, int tokens, const T *q, const T *k, T *qo,
+              T *ko) {
+    constexpr int V = Chunk<T>::n, U = HALF ? 3 : 4, P = HALF ? V : V / 2;
+    const int t = (int)threadIdx.x / items, item = (int)threadIdx.x - t * items;
+    const unsigned tok = blockIdx.x * tokens + t;
+    if (t >= tokens || tok >= (unsigned)p.B * p.N) return;
+    const int b = tok / (unsigned)p.N, n = tok - b * p.N;
     const bool copy = item >= rotated;
     const int x0 = copy && HALF ? 2 * p.pairs + (item - rotated) * V : item * V;
 
-    float cs[HALF ? V : V / 2], sn[HALF ? V : V / 2];
+    // heads [h0, h1) of q's and then k's
+    const int heads = p.H + p.Hkv;
+    const int h0 = blockIdx.y * p.heads_per_block, h1 = min(heads, h0 + p.heads_per_block);
+    const int64_t iq = b * p.q.batch + n * p.q.token + x0, ik = b * p.k.batch + n * p.k.token + x0;
+    const int64_t oq = b * p.qo.batch + n * p.qo.token + x0,
+                  ok = b * p.ko.batch + n * p.ko.token + x0;
+    auto source = [&](int h) {
+        return h < p.H ? q + iq + h * p.q.head : k + ik + (h - p.H) * p.k.head;
+    };
+    auto target = [&](int h) {
+        return h < p.H ? qo + oq + h * p.qo.head : ko + ok + (h - p.H) * p.ko.head;
+    };
+    uint4 a[U], c[HALF ? U : 1];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (h + u >= h1) break;
+            const T *src = source(h + u);
+            a[u] = __ldcs(reinterpret_cast<const uint4 *>(src));
+            if (HALF && !copy) c[u] = __ldcs(reinterpret_cast<const uint4 *>(src + p.pairs));
+        }
+    };
+    load(h0);
+
+    float cs[P], sn[P];
+#pragma unroll
+    for (int i = 0; i < P; i++) cs[i] = 1.f, sn[i] = 0.f;
     if (!copy) {
         int64_t pos[3];
         token_position(p, b, n, pos);
 #pragma unroll
-        for (int i = 0; i < (HALF ? V : V / 2); i++) {
+        for (int i = 0; i < P; i++) {
             const int pair = HALF ? x0 + i : x0 / 2 + i;
-            cs[i] = 1.f;
-            sn[i] = 0.f;
             if (pair < p.pairs) turn(p, pos, pair, cs[i], sn[i]);
         }
     }
-    // heads [h0, h1) of q's and then k's
-    const int heads = p.H + p.Hkv;
-    const int h0 = blockIdx.y * p.heads_per_block, h1 = min(heads, h0 + p.heads_per_block);
-#pragma unroll 4
-    for (int hh = h0; hh < h1; hh++) {
-        const bool isq = hh < p.H;
-        const int h = isq ? hh : hh - p.H;
-        const Strides &si = isq ? p.q : p.k, &so = isq ? p.qo : p.ko;
-        const T *src = (isq ? q : k) + b * si.batch + h * si.head + n * si.token + x0;
-        T *dst = (isq ? qo : ko) + b * so.batch + h * so.head + n * so.token + x0;
-        float a[V];
-        if (copy) {
-            if (src != dst) {
-                Chunk<T>::load(src, a);
-                Chunk<T>::store(dst, a);
-            }
-            continue;
-        }
-        Chunk<T>::load(src, a);
-        if (HALF) {
-            float c[V], ra[V], rc[V];
-            Chunk<T>::load(src + p.pairs, c);
+    for (int h = h0; h < h1; h += U) {
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                ra[i] = a[i] * cs[i] - c[i] * sn[i];
-                rc[i] = a[i] * sn[i] + c[i] * cs[i];
+        for (int u = 0; u < U; u++) {
+            if (h + u >= h1) break;
+            T *dst = target(h + u);
+            if (copy) {
+                if (dst != source(h + u)) __stcs(reinterpret_cast<uint4 *>(dst), a[u]);
+                continue;
             }
-            Chunk<T>::store(dst, ra);
-            Chunk<T>::store(dst + p.pairs, rc);
-        } else {
-            float r[V];
+            float x[V], r[V];
+            Chunk<T>::floats(a[u], x);
+            if (HALF) {
+                float y[V], s[V];
+                Chunk<T>::floats(c[u], y);
 #pragma unroll
-            for (int i = 0; i < V / 2; i++) {
-                const float c = a[2 * i + 1];
-                r[2 * i] = a[2 * i] * cs[HALF ? 0 : i] - c * sn[HALF ? 0 : i];
-                r[2 * i + 1] = a[2 * i] * sn[HALF ? 0 : i] + c * cs[HALF ? 0 : i];
+                for (int i = 0; i < V; i++) {
+                    r[i] = x[i] * cs[HALF ? i : 0] - y[i] * sn[HALF ? i : 0];
+                    s[i] = x[i] * sn[HALF ? i : 0] + y[i] * cs[HALF ? i : 0];
+                }
+                __stcs(reinterpret_cast<uint4 *>(dst + p.pairs), Chunk<T>::bits(s));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; i++) {
+                    r[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
+                    r[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
+                }
             }
-            Chunk<T>::store(dst, r);
+            __stcs(reinterpret_cast<uint4 *>(dst), Chunk<T>::bits(r));
         }
+        if (h + U < h1) load(h + U);
     }
 }
 
@@ -210,10 +226,15 @@ cudaError_t run(RotaryProblem p, const void *q, const void *k, void *qo, void *k
                 cudaStream_t stream) {
     constexpr int V = Chunk<T>::n;
     const bool half = p.half, pairwise = half && p.pairs % V != 0;
+    const int rotated = half ? p.pairs / V : (2 * p.pairs + V - 1) / V;
     const int items = pairwise ? p.d - p.pairs
-                      : half   ? p.pairs / V + (p.d - 2 * p.pairs) / V
+                      : half   ? rotated + (p.d - 2 * p.pairs) / V
                                : p.d / V;
-    const int64_t blocks = ((int64_t)p.B * p.N * items + kThreads - 1) / kThreads;
+    // (an item is 16 bytes: at most 256 of them at d = 1024)
+    const int tokens = pairwise ? 0 : kThreads / items;
+    const int64_t all = (int64_t)p.B * p.N;
+    const int64_t blocks =
+        pairwise ? (all * items + kThreads - 1) / kThreads : (all + tokens - 1) / tokens;
     // few tokens: the heads spread over blocks as well, so that the loads of a short
     // call run side by side instead of one after another
     const int heads = p.H + p.Hkv;
@@ -226,9 +247,9 @@ cudaError_t run(RotaryProblem p, const void *q, const void *k, void *qo, void *k
     if (pairwise)
         rotary_half_pairs_kernel<T><<<grid, kThreads, 0, stream>>>(p, qq, kk, oq, ok);
     else if (half)
-        rotary_kernel<T, true><<<grid, kThreads, 0, stream>>>(p, qq, kk, oq, ok);
+        rotary_kernel<T, true><<<grid, kThreads, 0, stream>>>(p, items, rotated, tokens, qq, kk, oq, ok);
     else
-        rotary_kernel<T, false><<<grid, kThreads, 0, stream>>>(p, qq, kk, oq, ok);
+        rotary_kernel<T, false><<<grid, kThreads, 0, stream>>>(p, items, rotated, tokens, qq, kk, oq, ok);
     return cudaGetLastError();
 }
 

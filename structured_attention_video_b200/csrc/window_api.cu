@@ -268,8 +268,9 @@ monarch_status monarch_rotary(const monarch_rotary_desc *c, const void *q, const
     const int64_t size = c->dtype == MONARCH_BF16 ? 2 : 4, chunk = 16 / size;
     if (c->d > 1024 || c->d % chunk) return MONARCH_ERR_UNSUPPORTED;
     if (2 * (int64_t)c->pairs > c->d || c->N > (1 << 30)) return MONARCH_ERR_SHAPE;
-    // blocks of the launch: one thread an element of a token at most
-    if ((int64_t)c->B * c->N * c->d >= (1LL << 38) || c->H > 32767 || c->Hkv > 32767)
+    // token indexes in 32 bits; blocks of the launch: one thread an element of a token at most
+    if ((int64_t)c->B * c->N >= (1LL << 31) || (int64_t)c->B * c->N * c->d >= (1LL << 38) ||
+        c->H > 32767 || c->Hkv > 32767)
         return MONARCH_ERR_SHAPE;
     int64_t sum = 0;
     for (int i = 0; i < c->axes; i++) {
