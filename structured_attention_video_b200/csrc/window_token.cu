@@ -214,6 +214,10 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Ring of kStages tiles of 64 keys and values: 96 KB at d = 128, so two CTAs fit on an
 // SM and keep up to 192 KB in flight.
 template <int D> struct Ring {
@@ -242,18 +246,13 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
     volatile uint32_t *good = reinterpret_cast<volatile uint32_t *>(empty + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + NS) + NS;
     const WinProblem &p = a.p;
+    if (threadIdx.x == 0) {
+        prefetch_map(&tmK);
+        prefetch_map(&tmV);
+    }
     const TokenUnit u = token_unit<64>(a);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
     const int rows = p.Nq * p.G;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; s++) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, kTokWarps);
-        }
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    __syncthreads();
     const WaitCtx w{a.limit, a.status, abort_flag};
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -264,11 +263,19 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
         for (int c = 0; c < 4; c++) o[x][c] = 0.f;
 
     if (warp == kTokWarps) {
-        // ---------------- loads
+        // ---------------- loads; the first ones go out before the block meets
+        if (lane == 0) {
+            for (int s = 0; s < NS; s++) {
+                mbar_init(full + s, 1);
+                mbar_init(empty + s, kTokWarps);
+            }
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
         int issued = 0;
-        for (int g = u.g0; g < u.g1; g++) {
-            const int it = g - u.g0, st = it % NS, j0 = u.kt.tile(g) * 64;
-            if (it >= NS && !wait_warp(empty + st, (it / NS - 1) & 1, w)) break;
+        auto load = [&](int g) {
+            const int st = issued % NS, j0 = u.kt.tile(g) * 64;
             uint8_t *dst = sm + st * R::kStage;
             if (p.table) {
                 // one box of min(page, 64) keys a lane; pages that hold no visible key, or
@@ -311,6 +318,13 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                 }
             }
             issued++;
+        };
+        int g = u.g0;
+        for (; g < u.g1 && issued < NS; g++) load(g);
+        __syncthreads();
+        for (; g < u.g1; g++) {
+            if (!wait_warp(empty + issued % NS, (issued / NS - 1) & 1, w)) break;
+            load(g);
         }
         // every issued copy lands before the ring is used for the parts
         if (lane == 0)
@@ -336,6 +350,7 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                         in ? *reinterpret_cast<const uint32_t *>(src + x * 16 + c * 8) : 0u;
                 }
         }
+        __syncthreads();   // the barriers are initialised
         // this lane's row of an 8 x 8 matrix: key r8 (+ 8) of the 16, 16-byte column c
         const int r8 = lane & 7, mi = lane >> 3;
         const uint32_t base = smem_u32(sm) + warp * 16 * 128;
@@ -634,7 +649,10 @@ cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
 }  // namespace
 
 // Parts: about three CTAs an SM (two at a time of the bfloat16 kernel's, whose ring holds
-// what the memory's latency needs), none below two tiles of keys.  Up to 8 parts are
+// what the memory's latency needs), none below two tiles of keys.  More parts balance
+// ragged lengths better and cost more prologues and joins: 8 x 8 heads of up to 4097 keys
+// 26-30 us at 1.7 to 3 CTAs an SM, 47 at 6; sixteen sequences up to 8192 keys 75 us at
+// 1.7, 66 at 3, 85 at 6; four of 131072 keys 409 us at 1, 260-265 at 2 to 4.  Up to 8 parts are
 // one cluster; more make clusters of one size each.
 TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
     TokenPlan t;
