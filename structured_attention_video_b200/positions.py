@@ -2,12 +2,16 @@
 onto the C ABI (monarch_rotary, monarch_rotary_frequencies)."""
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import _lib
-from .window import _DTYPES, _LAYOUTS, _check, _fill, _index_tensor, _launch, _strides
+from .window import _device_and_dtype, _index_pointer, _is_bnhd, _launch, _strides
 
 _STYLES = ("interleaved", "half")
+_pack_desc = struct.Struct("@16ifPPqq12q").pack   # monarch_rotary_desc
+_desc_from = _lib.RotaryDesc.from_buffer_copy
 _SCALINGS = {None: _lib.ROTARY_PLAIN, "linear": _lib.ROTARY_LINEAR, "ntk": _lib.ROTARY_NTK,
              "yarn": _lib.ROTARY_YARN}
 
@@ -37,10 +41,9 @@ def rotary_frequencies(dims, *, base=10000.0, scaling=None, factor=1.0, original
 
 
 def _run(q, k, freqs, dims, style, grid, positions, start, magnitude, layout, out, inverse):
-    if layout not in _LAYOUTS or style not in _STYLES:
-        raise ValueError("layout must be one of %s and style one of %s"
-                         % (list(_LAYOUTS), list(_STYLES)))
-    head, token = (1, 2) if layout == "bhnd" else (2, 1)
+    bnhd = _is_bnhd(layout)
+    if style not in _STYLES:
+        raise ValueError("style must be one of %s" % (list(_STYLES),))
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("expected 4-D tensors")
     if out is None:
@@ -50,61 +53,69 @@ def _run(q, k, freqs, dims, style, grid, positions, start, magnitude, layout, ou
         q_out, k_out = out
         if (k is None) != (k_out is None):
             raise ValueError("out must be (q_out, k_out), k_out None exactly when k is")
-    _check(q, q_out, *(() if k is None else (k, k_out)))
-    B, N, d = q.shape[0], q.shape[token], q.shape[3]
+    B, H, N, d = q.shape
+    if bnhd:
+        H, N = N, H
     if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
         raise ValueError("outputs must have the inputs' shapes")
-    if k is not None and (k.shape[0] != B or k.shape[token] != N or k.shape[3] != d):
-        raise ValueError("q and k must share batch, tokens and head dimension")
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.device != q.device or \
+    sq, so = _strides(q, bnhd), _strides(q_out, bnhd)
+    if k is None:
+        dev, dtype = _device_and_dtype(q, q_out)
+        Hkv, sk, sko, kp, kop = 0, (0, 0, 0), (0, 0, 0), None, None
+    else:
+        dev, dtype = _device_and_dtype(q, q_out, k, k_out)
+        kB, Hkv, kN, kd = k.shape
+        if bnhd:
+            Hkv, kN = kN, Hkv
+        if kB != B or kN != N or kd != d:
+            raise ValueError("q and k must share batch, tokens and head dimension")
+        sk, sko = _strides(k, bnhd), _strides(k_out, bnhd)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or freqs.get_device() != dev or \
             not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 vector on the inputs' device")
-    desc = _lib.RotaryDesc()
-    desc.B, desc.N, desc.H, desc.d = B, N, q.shape[head], d
-    desc.Hkv = 0 if k is None else k.shape[head]
-    pairs = desc.pairs = freqs.shape[0]
+    pairs = freqs.shape[0]
     if dims is None:
         dims = (2 * pairs,)
-    if not 1 <= len(dims) <= 3 or any(w < 0 or w % 2 for w in dims) or sum(dims) != 2 * pairs:
+    axes = len(dims)
+    if not 1 <= axes <= 3 or any(w < 0 or w % 2 for w in dims) or sum(dims) != 2 * pairs:
         raise ValueError("dims must be 1 to 3 even widths that sum to twice the frequencies")
-    desc.axes = len(dims)
-    for i, w in enumerate(dims):
-        desc.pairs_of_axis[i] = w // 2
-    desc.half, desc.inverse = int(style == "half"), int(inverse)
-    desc.dtype, desc.magnitude = _DTYPES[q.dtype], magnitude
+    grid_h = grid_w = 0
     if grid is not None:
-        f, h, w = grid
-        if f * h * w != N:
-            raise ValueError("N = %d but f*h*w = %d" % (N, f * h * w))
+        f, grid_h, grid_w = grid
+        if f * grid_h * grid_w != N:
+            raise ValueError("N = %d but f*h*w = %d" % (N, f * grid_h * grid_w))
         if positions is not None:
             raise ValueError("give grid or positions, not both")
-        desc.grid_h, desc.grid_w = h, w
+    pos, pos_batch, pos_token = 0, 0, 0
     if positions is not None:
-        want = (N,) if len(dims) == 1 else (N, len(dims))
+        want = (N,) if axes == 1 else (N, axes)
         if positions.dim() == len(want):
             positions = positions[None]
-        if positions.dtype != torch.int32 or positions.device != q.device or \
+        if positions.dtype is not torch.int32 or positions.get_device() != dev or \
                 tuple(positions.shape[1:]) != want or positions.shape[0] not in (1, B) or \
-                (len(want) == 2 and len(dims) > 1 and positions.stride(2) != 1):
+                (axes > 1 and positions.stride(2) != 1):
             raise ValueError("positions must be int32 [N] or [B, N], with several axes a last "
                              "dimension of them, on the inputs' device")
-        desc.positions = positions.data_ptr()
-        desc.pos_batch = positions.stride(0) if positions.shape[0] > 1 else 0
-        desc.pos_token = positions.stride(1) if N > 1 else 0
+        pos = positions.data_ptr()
+        pos_batch = positions.stride(0) if positions.shape[0] > 1 else 0
+        pos_token = positions.stride(1) if N > 1 else 0
+    first, starts = 0, 0
     if isinstance(start, int):
         if not -2 ** 31 <= start < 2 ** 31:
             raise ValueError("start out of range")
-        desc.start = start
+        first = start
     else:
-        desc.starts = _index_tensor(start, "start", B, q.device)
-    _fill(desc.q, _strides(q, head, token, d))
-    _fill(desc.q_out, _strides(q_out, head, token, d))
-    if k is not None:
-        _fill(desc.k, _strides(k, head, token, d))
-        _fill(desc.k_out, _strides(k_out, head, token, d))
-    _launch(q.device, _lib.monarch_rotary, "monarch_rotary", desc, q.data_ptr(),
-            None if k is None else k.data_ptr(), freqs.data_ptr(), q_out.data_ptr(),
-            None if k is None else k_out.data_ptr())
+        starts = _index_pointer(start, "start", B, dev)
+    try:
+        desc = _desc_from(_pack_desc(
+            B, N, H, Hkv, d, pairs, axes, dims[0] // 2, dims[1] // 2 if axes > 1 else 0,
+            dims[2] // 2 if axes > 2 else 0, style == "half", inverse, grid_h, grid_w, first, dtype,
+            magnitude, starts, pos, pos_batch, pos_token, *sq, *sk, *so, *sko))
+    except struct.error as e:
+        raise ValueError("an argument is not a number in the library's range: %s" % e) from None
+    _launch(dev, _lib.monarch_rotary, "monarch_rotary", desc, q.data_ptr(), kp, freqs.data_ptr(),
+            q_out.data_ptr(), kop)
     return q_out, k_out
 
 
