@@ -10,11 +10,13 @@ attention entry points fails loudly when that library is missing.
 
 Next to it: exact attention over a window of frames with the first frames kept
 (window_attention, its backward, and paged_attention for one new token over a paged
-cache), and the rotary positions of queries and keys (rotary, rotary_backward).
+cache), and the rotary positions of queries and keys (rotary, rotary_backward), which
+the Monarch attention takes as an option (rotary=Rotary(...)).
 """
 
 _MODULES = {
     "monarch_attention": "attention", "workspace_bytes": "attention", "kernel_path": "attention",
+    "Rotary": "attention",
     "window_attention": "window", "window_attention_backward": "window",
     "window_attention_path": "window", "paged_attention": "window",
     "rotary": "positions", "rotary_backward": "positions", "rotary_frequencies": "positions",

@@ -6,11 +6,34 @@ the library's CUDA kernels.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
-from . import _lib
+from . import _lib, positions
 
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
+
+
+class Rotary(NamedTuple):
+    """Rotary positions that an attention call gives its queries and keys (positions.rotary):
+    freqs float64 [pairs] on the device; dims of three axes (frame, row, column) take the
+    clip's grid, one axis counts tokens; start is the first frame (or token)."""
+    freqs: torch.Tensor
+    dims: tuple | None = None
+    style: str = "interleaved"
+    start: int = 0
+    magnitude: float = 1.0
+
+    def turn(self, q, k, f, h, w, first=0, backward=False, out=None):
+        """(q, k) of f frames turned by their positions, `first` frames behind start;
+        backward: gradients turned back.  [B, H, f*h*w, d] tensors."""
+        three = self.dims is not None and len(self.dims) == 3
+        call = positions.rotary_backward if backward else positions.rotary
+        return call(q, k, self.freqs, dims=self.dims, style=self.style,
+                    grid=(f, h, w) if three else None,
+                    start=self.start + (first if three else first * h * w),
+                    magnitude=self.magnitude, out=out)
 
 
 def _shape_args(q, f, h, w, b1, b2, tiles, iters):
@@ -46,8 +69,14 @@ def kernel_path(q, *, f, h, w, b1, b2, tiles=1, iters=1) -> int:
     return _lib.monarch_attn_path(*args, _DTYPES[q.dtype])
 
 
-def monarch_attention(q, k, v, *, f, h, w, b1, b2, tiles=1, iters=1, out=None, workspace=None):
-    """Y = M V with M the tiled Monarch approximation of softmax(Q K^T / sqrt(d))."""
+def monarch_attention(q, k, v, *, f, h, w, b1, b2, tiles=1, iters=1, out=None, workspace=None,
+                      rotary=None):
+    """Y = M V with M the tiled Monarch approximation of softmax(Q K^T / sqrt(d)).
+    rotary (a Rotary): q and k get rotary positions first."""
+    if rotary is not None:
+        _check_tensors(q, k, v)
+        _shape_args(q, f, h, w, b1, b2, tiles, iters)
+        q, k = rotary.turn(q, k, f, h, w)
     if out is None:
         out = torch.empty_like(q)
     _check_tensors(q, k, v, out)
@@ -69,14 +98,20 @@ def monarch_attention(q, k, v, *, f, h, w, b1, b2, tiles=1, iters=1, out=None, w
     return out
 
 
-def monarch_attention_kv(q, k, v, *, fq, fk, h, w, b1, b1k, b2, tiles=1, iters=1, out=None):
+def monarch_attention_kv(q, k, v, *, fq, fk, h, w, b1, b1k, b2, tiles=1, iters=1, out=None,
+                         rotary=None):
     """Queries of a chunk of fq frames [B, H, fq*h*w, d] against keys and values of
-    fk frames [B, H, fk*h*w, d] (a cache of earlier frames and the chunk's own)."""
+    fk frames [B, H, fk*h*w, d] (a cache of earlier frames and the chunk's own).
+    rotary (a Rotary): q and k get rotary positions first, the chunk being the newest fq
+    of the fk frames (a cache that holds turned keys needs none)."""
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
         raise ValueError("expected [B, H, N, d] tensors, k and v alike")
     B, H, nq, d = q.shape
     if nq != fq * h * w or k.shape != (B, H, fk * h * w, d):
         raise ValueError("query or key/value lengths do not match the frame counts")
+    if rotary is not None:
+        q, _ = rotary.turn(q, None, fq, h, w, first=fk - fq)
+        k, _ = rotary.turn(k, None, fk, h, w)
     if out is None:
         out = torch.empty_like(q)
     for t in (q, k, v, out):
@@ -112,11 +147,15 @@ def monarch_attention_units(q, k, v, out, *, f, h, w, b1, b2, tiles=1, iters=1, 
     return out
 
 
-def monarch_attention_backward(q, k, v, dy, *, f, h, w, b1, b2, tiles=1, iters=1, workspace=None):
+def monarch_attention_backward(q, k, v, dy, *, f, h, w, b1, b2, tiles=1, iters=1, workspace=None,
+                               rotary=None):
     """Gradients (dq, dk, dv) of a loss whose gradient with respect to
-    monarch_attention(q, k, v, ...) is dy (one iteration)."""
+    monarch_attention(q, k, v, ...) is dy (one iteration).  rotary: as in that call; dq and
+    dk are those of its unturned q and k."""
     _check_tensors(q, k, v, dy)
     args = _shape_args(q, f, h, w, b1, b2, tiles, iters)
+    if rotary is not None:
+        q, k = rotary.turn(q, k, f, h, w)
     dt = _DTYPES[q.dtype]
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     need = _lib.monarch_attn_bwd_workspace_bytes(*args, dt)
@@ -134,6 +173,8 @@ def monarch_attention_backward(q, k, v, dy, *, f, h, w, b1, b2, tiles=1, iters=1
                                         workspace.data_ptr(),
                                         workspace.numel() * workspace.element_size(), stream),
                "monarch_attn_bwd_ws")
+    if rotary is not None:
+        rotary.turn(dq, dk, f, h, w, backward=True, out=(dq, dk))
     return dq, dk, dv
 
 

@@ -155,6 +155,8 @@ def window_attention(q, k, v, *, window=(-1, 0), sinks=0, frame=1, lengths=None,
     float32 [B, H, Nq] (natural logarithm, -inf in rows that see nothing)."""
     if out is None:
         out = torch.empty_like(q)
+    elif out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+        raise ValueError("out must not be an input")
     desc, shape, dev = _describe(q, k, v, out, window, sinks, frame, lengths, starts, scale, layout)
     lse = torch.empty(shape, dtype=torch.float32, device=q.device) if return_lse else None
     ws, size, _owner = _workspace(_lib.monarch_window_attn_workspace_bytes(desc), workspace, q)
@@ -214,6 +216,8 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, *, window=(-1, 0),
         raise ValueError("expected q [B, H, d] and 4-D pools of pages, k and v alike")
     if out is None:
         out = torch.empty_like(q)
+    elif out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be an input")
     dev, dtype = _device_and_dtype(q, k_pages, v_pages, out)
     B, H, d = q.shape
     pages, Hkv, page, kd = k_pages.shape

@@ -180,6 +180,80 @@ def test_captured_and_replayed():
         assert torch.equal(x, y)
 
 
+# ---------------------------------------------------------------- how the work is divided
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64)])
+@pytest.mark.parametrize("mask", [((-1, -1), 0, 1), ((-1, 0), 0, 1), ((1500, 0), 40, 1),
+                                  ((2, 0), 1, 400)])
+def test_few_queries_against_long_caches(dtype, d, mask):
+    """Fewer query tiles than SMs against thousands of keys: the CTAs divide the line of all
+    key chunks and cut problems; ragged lengths, one sequence empty, one shorter than its
+    queries."""
+    window, sinks, frame = mask
+    lens = (6000, 0, 4097, 350)
+    q, k, v, _ = make(20, dtype, 4, 3, 1, d, 600, 6000)
+    for b, n in enumerate(lens):
+        k[b, :, n:], v[b, :, n:] = NAN, NAN
+    out, lse = check(q, k, v, window=window, sinks=sinks, frame=frame, lengths=ints(*lens))
+    assert (out[1] == 0).all() and (out[3, :, :250] == 0).all()
+    assert (lse[3, :, :250] == -float("inf")).all()
+    check(q, k, v, window=window, sinks=sinks, frame=frame, lengths=ints(0, 0, 0, 0))
+    check(q[:1, :1], k[:1], v[:1], window=window, sinks=sinks, frame=frame)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_problems_than_sms(d):
+    q, k, v, dout = make(21, "bf16", 3, 64, 64, d, 300, 300)
+    check(q, k, v, dout, window=(90, 0), sinks=2, lengths=ints(300, 141, 0), starts=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (16, 1)])
+def test_few_key_tiles_with_many_query_blocks(dtype, H, Hkv):
+    """The query blocks of a key tile are split over CTAs (bfloat16) and joined."""
+    q, k, v, dout = make(22, dtype, 1, H, Hkv, 64, 1000, 1000)
+    check(q, k, v, dout, window=(-1, 0), starts=0)
+    check(q, k, v, dout, window=(100, 30), sinks=3, starts=0, lengths=ints(777))
+
+
+@pytest.mark.parametrize("N", [64, 128, 192, 256, 320, 384, 448, 512])
+def test_rows_of_few_keys_get_exact_deltas(N):
+    """Around the number of key blocks up to which delta comes from the products."""
+    q, k, v, dout = make(N, "bf16", 1, 2, 2, 128, N, N)
+    check(q, k, v, dout, window=(-1, 0))
+    check(q, k, v, dout, window=(-1, -1))
+
+
+def test_heads_past_32_bit_offsets():
+    """A cache whose last head starts past 2^31 elements."""
+    cap, Hkv, d = 1 << 21, 9, 128
+    cache = torch.empty((2, 1, Hkv, cap, d), dtype=torch.bfloat16, device="cuda")
+    q, k, v, _ = make(23, "bf16", 1, Hkv, Hkv, d, 130, 200)
+    cache[0, :, :, :200], cache[1, :, :, :200] = k, v
+    ref = attention(q, k, v)
+    for n in (130, 3):
+        out = window_attention(q[:, :, 130 - n:], cache[0], cache[1], lengths=ints(200))
+        assert_within(out, ref["out"][:, :, 130 - n:], ref["out_bound"][:, :, 130 - n:], "out")
+
+
+def test_waits_give_up_and_the_next_call_is_right():
+    """Fault injection on the host: the issuing threads wait on a barrier that nothing
+    completes, give up after a short limit, and the status says so."""
+    q, k, v, dout = make(24, "bf16", 1, 2, 2, 128, 300, 300)
+    out, lse = window_attention(q, k, v, return_lse=True)
+    torch.cuda.synchronize()
+    old = _lib.monarch_set_wait_limit(2000)
+    _lib.monarch_debug_inject_stall(True)
+    try:
+        window_attention(q, k, v)
+        assert _lib.monarch_last_device_status(None) == 7   # MONARCH_ERR_TIMEOUT
+        window_attention_backward(q, k, v, out, lse, dout)
+        assert _lib.monarch_last_device_status(None) == 7
+    finally:
+        _lib.monarch_debug_inject_stall(False)
+        _lib.monarch_set_wait_limit(old)
+    check(q, k, v, dout)
+
+
 # ---------------------------------------------------------------- paged
 def pages_of(k, v, page, lengths, layout, seed=0, extra=3):
     """Scattered pages that hold each sequence's keys, and NaN everywhere else."""
