@@ -150,6 +150,8 @@ rotary_kernel(RotaryProblem p, int items, int rotated, int tokens, const T *q, c
             if (pair < p.pairs) turn(p, pos, pair, cs[i], sn[i]);
         }
     }
+    // pairs of an interleaved chunk that turn; the words behind them stay as they are
+    const int turning = HALF || copy ? P : min(P, p.pairs - x0 / 2);
     for (int h = h0; h < h1; h += U) {
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -177,7 +179,14 @@ rotary_kernel(RotaryProblem p, int items, int rotated, int tokens, const T *q, c
                     r[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
                 }
             }
-            __stcs(reinterpret_cast<uint4 *>(dst), Chunk<T>::bits(r));
+            uint4 bits = Chunk<T>::bits(r);
+            if (turning < P) {   // (word w holds part of pair w P / 4)
+                if (turning <= 0) bits.x = a[u].x;
+                if (turning <= P / 4) bits.y = a[u].y;
+                if (turning <= P / 2) bits.z = a[u].z;
+                if (turning <= 3 * P / 4) bits.w = a[u].w;
+            }
+            __stcs(reinterpret_cast<uint4 *>(dst), bits);
         }
         if (h + U < h1) load(h + U);
     }

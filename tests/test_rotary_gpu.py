@@ -114,6 +114,24 @@ def test_in_place_strided_and_magnitude(dtype):
     assert (cache[:, :, :70] == 0).all() and (cache[:, :, 120:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("style", ["interleaved", "half"])
+@pytest.mark.parametrize("width", [2, 6, 20])
+def test_elements_that_do_not_turn_are_copied(dtype, style, width):
+    """Bit for bit, whatever they hold and wherever the turned part ends."""
+    freqs, _ = rotary_frequencies(width)
+    q = make(10, dtype, 2, 3, 9, 32, "bhnd")
+    rest = q[..., width:]
+    rest[..., 0::4], rest[..., 1::4], rest[..., 2::4] = float("inf"), float("nan"), -0.0
+    a, _ = rotary(q, None, freqs, style=style, start=3)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(a[..., width:].contiguous().view(bits), rest.contiguous().view(bits))
+    pos = (3 + torch.arange(9, device="cuda"))[None, :, None].expand(1, 9, width // 2)
+    q[..., width:] = 0
+    a, _ = rotary(q, None, freqs, style=style, start=3)
+    check(a, reference(q, pos, freqs, style, "bhnd"), q, dtype)
+
+
 def test_backward_is_the_gradient():
     """Against central differences of the forward's 64-bit form along a direction."""
     freqs, _ = rotary_frequencies((8, 12, 12))
