@@ -30,14 +30,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D> constexpr int kPitch = D + 4;
 
 // Rows [r0, r0 + R) of a [tokens][D] matrix into shared memory, asynchronously (16-byte
-// copies of one group per thread); rows outside [0, valid) become zero.
+// copies of one group per thread); rows outside [low, valid) become zero.
 template <int D, int R>
 __device__ __forceinline__ void load_rows(float *sm, const float *base, int64_t stride, int r0,
-                                          int valid) {
+                                          int valid, int low = 0) {
     constexpr int kChunks = D / 4;
     for (int i = threadIdx.x; i < R * kChunks; i += 256) {
         const int r = i / kChunks, c = i % kChunks;
-        const bool in = r0 + r < valid;
+        const bool in = r0 + r >= low && r0 + r < valid;
         const float *src = base + (in ? (int64_t)(r0 + r) * stride + c * 4 : 0);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                          tc::smem_u32(sm + r * kPitch<D> + c * 4)),
@@ -374,10 +374,10 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
     auto load = [&](int u) {
         float *dst = sqd + u % kStages<D> * 2 * kTileFloats;
         const int h = hk * p.G + u / nt, i0 = (t0 + u % nt) * 32;
-        // rows behind the sequence's end enter as zeros, whatever they hold
-        load_rows<D, 32>(dst, q + b * p.q.batch + h * p.q.head, p.q.token, i0, rlast);
+        // rows that are not real enter as zeros, whatever they hold
+        load_rows<D, 32>(dst, q + b * p.q.batch + h * p.q.head, p.q.token, i0, rlast, rfirst);
         load_rows<D, 32>(dst + kTileFloats, dout + b * g.dout.batch + h * g.dout.head, g.dout.token,
-                         i0, rlast);
+                         i0, rlast, rfirst);
     };
     if (kStages<D> == 2 && n > 0) load(0);
     copies_commit();

@@ -103,6 +103,20 @@ def test_positions_before_and_behind_the_sequence(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padding_in_front_with_garbage(dtype):
+    """Sequences aligned to the right: rows before position 0 hold anything."""
+    B, N = 3, 150
+    q, k, v, dout = make(14, dtype, B, 4, 2, 64, N, N)
+    front = (0, 45, 149)
+    for b, n in enumerate(front):
+        q[b, :, :n], dout[b, :, :n] = NAN, NAN
+        k[b, :, N - n:], v[b, :, N - n:] = NAN, NAN
+    lengths = ints(*(N - n for n in front))
+    for window, sinks in (((-1, 0), 0), ((20, 0), 3), ((9, 9), 0)):
+        check(q, k, v, dout, window=window, sinks=sinks, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strided_inputs_and_outputs(dtype):
     """Slices of a fused projection and of a longer cache, read and written in place."""
     g = torch.Generator(device="cuda")
