@@ -704,9 +704,12 @@ bool use_line(const WinProblem &p, int nprob, int sms) {
         most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
     }
     const int64_t chunks = most / 128 + 1;
-    if (entries * p.H * chunks >= (1LL << 31)) return false;
+    // at most one more: a run of n keys meets at most n / 64 + 2 blocks, the sinks' and the
+    // window's n / 64 + 3 together
+    const int64_t bound = entries * p.H * (chunks + 1);
+    if (bound >= (1LL << 31)) return false;
     // segments of a CTA: at most its chunks, and at most the problems
-    if (min((int64_t)nprob, nprob * chunks / sms + 2) > kMaxSegments) return false;
+    if (min((int64_t)nprob, bound / sms + 1) > kMaxSegments) return false;
     const int64_t rounds = (nprob + sms - 1) / sms;
     return rounds * chunks - nprob * chunks / sms >= 10;
 }

@@ -115,8 +115,8 @@ def _workspace(need, workspace, q):
         return None, 0, None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != q.get_device():
-        raise ValueError("workspace must be on the inputs' device")
+    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the inputs' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -152,7 +152,9 @@ def window_attention(q, k, v, *, window=(-1, 0), sinks=0, frame=1, lengths=None,
     gives each sequence's keys, Nk by default; starts (an int or int32 [B] on the
     device) the position of its first query, by default such that the queries are its
     newest tokens.  scale defaults to 1/sqrt(d).  Returns out, or (out, lse) with lse
-    float32 [B, H, Nq] (natural logarithm, -inf in rows that see nothing)."""
+    float32 [B, H, Nq] (natural logarithm, -inf in rows that see nothing).  out may be a
+    strided view that overlaps no input; a workspace (uint8, any size) spares the
+    allocation where it is large enough, and calls that overlap must not share one."""
     if out is None:
         out = torch.empty_like(q)
     elif out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
