@@ -445,6 +445,13 @@ MONARCH_API int monarch_attn_path(int B, int H, int f, int h, int w, int d, int 
  * neither are queries and dout of rows that are not real.  Keys and values below
  * lengths[b] should be finite: a NaN or an infinity there can reach every query that
  * shares a tile with one that sees it.
+ *
+ * Every call may be captured into a CUDA graph once a call of its kind has run in the
+ * context (the first one loads its kernels); each captured call wants a workspace of its
+ * own where two replays can overlap.  The kernels wait with the limit of
+ * monarch_set_wait_limit and report through monarch_last_device_status;
+ * monarch_debug_inject_stall reaches those of path 1 and the bfloat16 backward.  The
+ * monarch_profile_* hooks do not cover these kernels.
  * ------------------------------------------------------------------------ */
 typedef struct {
     int64_t batch, head, token;   /* elements between batches, heads and tokens */
@@ -466,8 +473,10 @@ typedef struct {
 } monarch_window_desc;
 
 /*
- * Workspace bytes of monarch_window_attn_fwd_ws, or 0 if the arguments fail
- * validation; 256 where none is needed (workspace may then be NULL).  Pure host function.
+ * Workspace bytes of monarch_window_attn_fwd_ws on the current device, or 0 if the
+ * arguments fail validation; 256 where none is needed (workspace may then be NULL).  Paths
+ * 1 and 2 need one where the keys of a row are split over more CTAs than join by
+ * themselves.  Host function.
  * Source: no counterpart in the pages (a property of this implementation).
  */
 MONARCH_API size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc);
@@ -504,6 +513,9 @@ MONARCH_API monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc 
  * dk and dv summed over the query heads that share a key head.  `grads` holds the
  * strides of dout and of the three gradients (same rules as desc's).  dq, dk and dv are
  * fully overwritten: zeros in rows that are not real and keys past lengths[b].
+ * The workspace (256-byte aligned, never NULL) holds delta and, where few key tiles meet
+ * many queries, parts of dk and dv; in the bfloat16 kernels rows of few keys get delta
+ * from the products themselves, as out's rounding would be most of their dq's error.
  * Deterministic: no atomics.
  * Source: no counterpart in the pages (the derivative of the forward map).
  */

@@ -10,26 +10,29 @@
 //   tc_window_dkv_kernel  128 keys of one key head against the 128-query tiles of
 //                         every head of its group that see them;
 //   tc_window_dq_kernel   128 queries of one head against their 128-key tiles.
-// 608 threads a CTA, one CTA an SM: warps 0-15 the elementwise work, warp 16 loads, one
-// thread of warp 17 issues every product, warp 18 stages lse and delta (dkv).
+// 640 threads a CTA, one CTA an SM: warps 0-15 the elementwise work, warp 16 loads, one
+// thread of warp 17 issues S and dV, one of warp 18 dP and dK (or dQ), warp 19 stages lse
+// and delta (dkv).
 //
 // The streamed side goes in blocks of 64 rows (queries in dkv, keys in dq).  Blocks u
 // with u % 2 = h belong to warps 8 h .. 8 h + 7 (a thread has 32 columns of one row, its
 // tensor-memory lane, of the fixed tile), so the two groups work on different blocks at
 // different times and the tensor pipe has the products of one while the other computes.
-// Order of the products (fixed, so the sums are too):
-//   dkv:  dV(u) S(u+2) after P(u);  dK(u) dP(u+2) after dS(u)
-//   dq:   S(u+2) once S(u) is read;  dQ(u) dP(u+2) after dS(u)
+// Order of each issuer's products (fixed, and each accumulator has one issuer, so the
+// sums are fixed too):
+//   dkv:  dV(u) S(u+2) after P(u)         |  dK(u) dP(u+2) after dS(u)
+//   dq:   S(u+2) once S(u) is read        |  dQ(u) dP(u+2) after dS(u)
 // P lies over S and dS over dP in tensor memory; a later product into the same columns
-// follows in issue order.  What shaped this (d = 128, nine 480p frames):
+// follows in issue order.  What shaped this (d = 128, 12 heads, nine 480p frames of which each sees four):
 //  - Two stages of 128 rows with 128-column products, all warps in step: dkv 1107 us, dq
 //    787; the pipe waited for loads and for the elementwise work in turn.
-//  - Two or three issuing threads, to fill the gaps at one's barrier polls: dkv 915-932,
-//    dq 600-620.  Where a product has to follow another thread's, the commit, the wait and
-//    the pipe's latency cost about 700 clocks, and interleaved streams run slower.
+//  - 64-row blocks, one thread elected for the whole role (an election or a branch per
+//    product costs 30 to 80 clocks each): dkv 735, dq 659.
 //  - M = 128, N = 64 reads 4 KB of A and 2 KB of B a K-step, 48 clocks of shared memory's
 //    128 bytes a clock against 32 of the tensor pipe: Q and dO live in tensor memory in dq
-//    (648 -> 624); in dkv the accumulators leave no room.
+//    (659 -> 648); in dkv the accumulators leave no room.
+//  - Sixteen elementwise warps of 32 columns instead of eight of 64: dkv 710, dq 581.  A
+//    second issuer, as one thread's barrier polls left the pipe idle: dkv 672, dq 536.
 //
 // delta comes from out as the forward rounded it, an error of 2^-8 |dO.O| at most.  A
 // row of n keys of like weight has |O| of about n^(-1/2) |v|, so against dP it matters
@@ -37,8 +40,10 @@
 // their keys once for delta = sum P dP from the same products that form dS, and the dq
 // kernel runs first to hand it to the dk/dv kernel.  (Two padded causal
 // sequences of 1023 and 681 tokens, d = 64: dq is 2.6e-3 from 64 bits without it.)
-// Bound by the tensor pipe: 4 (3) products of 128 x 128 x d a tile against 16384
-// exponentials at 16 a clock.
+// Bound by the tensor pipe and, nearly as long, the elementwise warps' issue slots: 4 (3)
+// products of 128 x 128 x d a tile against 16384 exponentials at 16 a clock.  The same
+// frames, forward included: 1638 us against 967 of the fewest products at the rate of a
+// large matrix product.
 #include "window_tc.cuh"
 
 namespace monarch {
@@ -498,12 +503,12 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
                 store_part<W>(lanes + 256 + x, dst);
                 store_part<W>(lanes + 384 + x, dst + D);
             } else {
-            store_row<W>(lanes + 256 + x,
-                         a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
-                         p.d - (int)x, real, key);
-            store_row<W>(lanes + 384 + x,
-                         a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x, p.scale,
-                         p.d - (int)x, real, key);
+                store_row<W>(lanes + 256 + x,
+                             a.dv + b * a.g.dv.batch + hk * a.g.dv.head + j * a.g.dv.token + x, 1.f,
+                             p.d - (int)x, real, key);
+                store_row<W>(lanes + 384 + x,
+                             a.dk + b * a.g.dk.batch + hk * a.g.dk.head + j * a.g.dk.token + x,
+                             p.scale, p.d - (int)x, real, key);
             }
         }
     }
@@ -778,7 +783,7 @@ cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const 
 // Parts of a key tile's query blocks in the dk/dv kernel: where the key tiles are fewer
 // than the SMs, as many as fill them, of eight blocks at least (a part's prologue, its
 // store and the join cost about four).  Two causal sequences of 1023 tokens, 8 heads on 2
-// key heads, d = 64: 32 tiles of up to 64 blocks, 49 us whole.
+// key heads, d = 64: 32 tiles of up to 64 blocks, 49 us whole, 20 and 4.5 for the join split.
 int dkv_splits(const WinProblem &p) {
     const int64_t tiles = (int64_t)p.B * p.Hkv * ((p.Nk + 127) / 128);
     const int64_t blocks = (int64_t)((p.Nq + 63) / 64) * p.G;

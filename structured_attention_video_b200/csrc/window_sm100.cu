@@ -7,14 +7,20 @@
 // pair sees, two blocks a chunk.  Either each CTA takes whole problems (the longest
 // first), or, where those would leave SMs idle, the chunks of all problems form one line
 // that the CTAs divide evenly: a problem cut by a boundary leaves its parts' unscaled sums,
-// maxima and row sums in the workspace, and a second kernel joins them in order.  Roles: warp 12 loads keys, warp 14 queries and values (TMA), warps 13
-// and 15 issue the products of tile 0 and 1, warps 0-3 and 4-7 are the softmax of tile
-// 0 and 1 (one query row a thread), warps 8-11 the epilogue.  Keys go in halves of 64:
-// each tile has two S buffers of 64 columns in tensor memory, so the logits of the
-// next half are ready while the softmax works on this one; P overwrites S in place.
-// The running maximum moves only when it grows by more than 2^8, so O is rarely
-// rescaled.  Bound by the exponentials (16 a clock and SM, 2 tiles x 128 x 64 a half)
-// together with the issue slots of the softmax warps, then by the products.
+// maxima and row sums in the workspace, and a second kernel joins them in order.  Roles:
+// warp 12 loads keys, warp 14 queries and values (TMA), warps 13 and 15 issue the products
+// of tile 0 and 1, warps 0-3 and 4-7 are the softmax of tile 0 and 1 (one query row a
+// thread), warps 8-11 the epilogue.  Keys go in halves of 64: each tile has two S buffers
+// of 64 columns in tensor memory, so the logits of the next half are ready while the
+// softmax works on this one; P overwrites S in place.  The running maximum moves only
+// when it grows by more than 2^8, so O is rarely rescaled.
+//
+// Bound by the exponentials (16 a clock and SM, 2 tiles x 128 x 64 a half) together with
+// the issue slots of the softmax warps, then by the products.  A 480p chunk of 4680
+// queries that see 18720 keys, 12 heads, d = 128: 541 us (996 TFLOP/s; 641 us where the
+// power limit lowers the clocks of a long run), against 331 for the products alone.  Rejected: one
+// maximum a block guessed from the last one's (fewer instructions on the common path, but
+// 27% more time for the test and the repeat behind it).
 #include "window_tc.cuh"
 
 namespace monarch {
@@ -693,7 +699,9 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
 
 // Whether the CTAs divide the line of all chunks.  Whole problems on `sms` CTAs take as many
 // rounds of the longest problem as there are problems a CTA; the line takes the mean, and
-// about ten chunks' time (20 us) for the parts and the join.  Chunks are estimated from
+// about ten chunks' time (20 us) for the parts and the join.  4680 queries
+// that see 18720 keys, 12 heads (228 pairs of 147 chunks on 148 SMs): 620 us whole, 541 by
+// the line.  Chunks are estimated from
 // the tensors' sizes and the window, as the lengths are on the device.
 bool use_line(const WinProblem &p, int nprob, int sms) {
     const int64_t entries = (int64_t)((p.Nq + 255) / 256) * p.B;
@@ -757,7 +765,7 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
     // A tile alone on its SM takes little more than half of a pair's time a key block
     // (the two tiles share the exponentials' units), so where the pairs are fewer than
     // the SMs single tiles finish sooner: two padded causal batches of 1023 tokens with 8
-    // heads 27 -> 18 us.
+    // heads 27 -> 22 us.
     a.tiles = a.line || (p.Nq + 255) / 256 * p.B * p.H >= sms ? 2 : 1;
     a.npairs = (p.Nq + 128 * a.tiles - 1) / (128 * a.tiles);
     a.nprob = a.npairs * p.B * p.H;
