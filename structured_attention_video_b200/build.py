@@ -1,10 +1,12 @@
-"""Builds libmonarch.so in-tree with nvcc for sm_100a.
+"""Builds libmonarch.so in-tree with nvcc for sm_100a, and the torch binding next to it.
 
     python -m structured_attention_video_b200.build [--force]
 
 Each .cu file under csrc/ compiles to an object in parallel; the objects link
 into structured_attention_video_b200/_build/libmonarch.so (CUDA runtime linked
 statically, so the library needs only the NVIDIA driver at run time).
+csrc/torch_binding.cpp becomes the CPython module monarch_torch.so, which marshals torch
+tensors onto the library's C ABI.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmonarch.so")
+BINDING = os.path.join(OUT_DIR, "monarch_torch.so")
 HEADERS = [os.path.join(os.path.dirname(PKG), "include", "monarch_attn.h")]
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -45,6 +48,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = sources()
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + HEADERS
     if not force and not _stale(LIB, deps):
+        _build_binding(force)
         return LIB
     nvcc = _nvcc()
 
@@ -70,7 +74,32 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB)
+    _build_binding(force)
     return LIB
+
+
+def _build_binding(force: bool) -> None:
+    src = os.path.join(CSRC, "torch_binding.cpp")
+    if not force and not _stale(BINDING, [src] + HEADERS):
+        return
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    includes = [os.path.join(root, "include"), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    # (libmonarch.so is found next to the module; torch's libraries are loaded before it)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[x for i in includes for x in ("-isystem", i)], src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-L" + OUT_DIR, "-l:libmonarch.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (src, res.stdout, res.stderr))
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from structured_attention_video_b200 import rotary, rotary_backward, rotary_frequencies
+from structured_attention_video_b200 import _lib, rotary, rotary_backward, rotary_frequencies
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -130,6 +130,32 @@ def test_elements_that_do_not_turn_are_copied(dtype, style, width):
     q[..., width:] = 0
     a, _ = rotary(q, None, freqs, style=style, start=3)
     check(a, reference(q, pos, freqs, style, "bhnd"), q, dtype)
+
+
+def test_wrong_arguments_are_refused():
+    freqs, _ = rotary_frequencies(32)
+    q, k = make(11, "f32", 2, 4, 24, 64, "bhnd"), make(12, "f32", 2, 2, 24, 64, "bhnd")
+    pos = torch.arange(24, dtype=torch.int32, device="cuda")
+    rotary(q, k, freqs, positions=pos[None].expand(2, 24))
+    for bad in (dict(style="whole"), dict(layout="nbhd"), dict(dims=(32, 2)), dict(dims=(31, 1)),
+                dict(dims=()), dict(dims=(8, 8, 8, 8)), dict(dims=(-2, 34)),
+                dict(dims=(8, 12, 12), grid=(2, 3, 5)), dict(dims=(8, 12, 12), grid=(2, 12)),
+                dict(positions=pos.long()), dict(positions=pos[:23]), dict(positions=pos.cpu()),
+                dict(positions=pos.expand(3, 24)), dict(positions=pos, dims=(8, 12, 12)),
+                dict(positions=pos[:, None].expand(24, 3), dims=(8, 12, 12)), dict(start=2 ** 31),
+                dict(start=pos), dict(start=1.5), dict(magnitude="x"), dict(out=(q,)),
+                dict(out=(q, None)), dict(out=(q[:1], k)), dict(out=(q, k.bfloat16()))):
+        with pytest.raises(ValueError):
+            rotary(q, k, freqs, **bad)
+    for a, b, f in ((q[0], k, freqs), (q, k[:, :, :23], freqs), (q, k.bfloat16(), freqs),
+                    (q, k, freqs.float()), (q, k, freqs.cpu()), (q, k, freqs[::2]),
+                    (q.cpu(), None, freqs), (q, k.cpu(), freqs), (q.transpose(2, 3), None, freqs)):
+        with pytest.raises(ValueError):
+            rotary(a, b, f)
+    with pytest.raises(_lib.MonarchError):      # more pairs than the head has
+        rotary(q[..., :16], None, freqs)
+    with pytest.raises(_lib.MonarchError):      # three axes without a grid or positions
+        rotary(q, k, freqs, dims=(8, 12, 12))
 
 
 def test_backward_is_the_gradient():

@@ -6,7 +6,6 @@ import pytest
 import torch
 
 from structured_attention_video_b200 import _lib, rotary, rotary_frequencies, window_attention
-from structured_attention_video_b200.window import _workspace
 
 P = 1 << 20   # never dereferenced: validation fails first
 OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, NO_MEMORY = range(6)
@@ -186,14 +185,3 @@ def test_cpu_tensors_are_refused():
         window_attention(q, q, q)
     with pytest.raises(ValueError):
         rotary(q, q, torch.ones(32, dtype=torch.float64))
-
-
-def test_workspace_of_repeated_bytes_is_refused():
-    """An expanded tensor counts more bytes than it has."""
-    q = torch.zeros(1)
-    with pytest.raises(ValueError):
-        _workspace(1000, torch.zeros(1, dtype=torch.uint8).expand(4096), q)
-    pointer, size, owner = _workspace(1000, None, q)
-    assert size == 1000 and owner.data_ptr() == pointer
-    mine = torch.zeros(4096, dtype=torch.uint8)
-    assert _workspace(1000, mine, q) == (mine.data_ptr(), 4096, mine)

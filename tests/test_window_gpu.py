@@ -249,6 +249,74 @@ def test_heads_past_32_bit_offsets():
         assert_within(out, ref["out"][:, :, 130 - n:], ref["out_bound"][:, :, 130 - n:], "out")
 
 
+def test_workspaces():
+    """The caller's where it is large enough; never one that counts bytes it has not."""
+    q, k, v, dout = make(15, "bf16", 1, 2, 2, 64, 90, 90)
+    out, lse = window_attention(q, k, v, return_lse=True)
+    mine = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    want = window_attention_backward(q, k, v, out, lse, dout)
+    for ws in (mine, mine[:16], mine.view(torch.float32)):
+        got = window_attention_backward(q, k, v, out, lse, dout, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for ws in (mine[:1].expand(1 << 20), mine[::2], mine.cpu()):
+        with pytest.raises(ValueError):
+            window_attention_backward(q, k, v, out, lse, dout, workspace=ws)
+
+
+def test_wrong_arguments_are_refused():
+    q, k, v, dout = make(16, "bf16", 2, 4, 2, 64, 40, 40)
+    out, lse = window_attention(q, k, v, return_lse=True)
+    lens = ints(40, 40)
+    for bad in (dict(window=(1,)), dict(window=(1, 2, 3)), dict(window=(2 ** 40, 0)),
+                dict(window=(1.5, 0)), dict(sinks=2 ** 31), dict(frame="x"), dict(scale="x"),
+                dict(layout="nbhd"), dict(lengths=lens.long()), dict(lengths=lens[:1]),
+                dict(lengths=lens.cpu()), dict(starts=-2 ** 31), dict(starts=2 ** 31),
+                dict(starts=ints(1, 2, 3)), dict(out=q), dict(out=v), dict(out=out[:, :2]),
+                dict(out=out.float()), dict(out=out.cpu())):
+        with pytest.raises(ValueError):
+            window_attention(q, k, v, **bad)
+    for a, b, c in ((q[0], k, v), (q, k, v[:, :1]), (q, k[:1], v[:1]), (q, k.float(), v),
+                    (q, k[..., :32], v[..., :32]), (q.transpose(2, 3), k, v), (q.cpu(), k, v),
+                    (q, k.cpu(), v.cpu()), (q.half(), k.half(), v.half())):
+        with pytest.raises(ValueError):
+            window_attention(a, b, c)
+    with pytest.raises(TypeError):
+        window_attention(q, k, None)
+    for bad in (dict(window=(-2, 0)), dict(frame=0), dict(sinks=-1), dict(scale=0.0),
+                dict(scale=float("inf"))):
+        with pytest.raises(_lib.MonarchError):
+            window_attention(q, k, v, **bad)
+    with pytest.raises(_lib.MonarchError):     # broadcast keys have no strides of their own
+        window_attention(q, k[:, :1].expand(2, 2, 40, 64), v)
+    for x in (lse.double(), lse[:, :, :39], lse.transpose(1, 2)):
+        with pytest.raises(ValueError):
+            window_attention_backward(q, k, v, out, x, dout)
+    with pytest.raises(ValueError):
+        window_attention_backward(q, k, v, out, lse, dout.float())
+    with pytest.raises(ValueError):            # the gradient of a plain sum
+        window_attention_backward(q, k, v, out, lse, torch.ones_like(q[:1, :1, :1, :1]).expand_as(q))
+
+
+def test_paged_wrong_arguments_are_refused():
+    q = torch.randn(2, 4, 64, device="cuda")
+    pool = torch.randn(6, 2, 16, 64, device="cuda")
+    table, lens = ints(0, 1, 2, 3, 4, 5).view(2, 3), ints(20, 48)
+    paged_attention(q, pool, pool, table, lens)
+    for args in ((q[0], pool, pool, table, lens), (q, pool, pool[:3], table, lens),
+                 (q, pool[..., :32], pool[..., :32], table, lens), (q, pool, pool, table[0], lens),
+                 (q, pool, pool, table.long(), lens), (q, pool, pool, table[:, :0], lens),
+                 (q, pool, pool, table[:1], lens), (q, pool, pool, table, lens.long()),
+                 (q, pool, pool, table.cpu(), lens), (q, pool.bfloat16(), pool.bfloat16(), table, lens)):
+        with pytest.raises(ValueError):
+            paged_attention(*args)
+    with pytest.raises(ValueError):
+        paged_attention(q, pool, pool, table, lens, out=q)
+    with pytest.raises(TypeError):
+        paged_attention(q, pool, pool, table, None)
+    with pytest.raises(_lib.MonarchError):     # pages of 12
+        paged_attention(q, pool[:, :, :12], pool[:, :, :12], table, lens)
+
+
 def test_waits_give_up_and_the_next_call_is_right():
     """Fault injection on the host: the issuing threads wait on a barrier that nothing
     completes, give up after a short limit, and the status says so."""
