@@ -62,13 +62,15 @@ template <int D> struct Layout {
     static_assert(kSmem <= (uint32_t)kMaxSmem, "window attention shared memory");
 };
 
+enum { kEvery, kWhole, kLine };
+
 struct FwdArgs {
     WinProblem p;
     int tiles;      // 128-row query tiles of a problem: 2, or 1 where pairs are fewer than SMs
     int npairs;     // problems a head
     int nprob;      // npairs * B * H
-    int line;       // 1: the CTAs divide the line of all chunks
-    // line: per slot (2 a CTA: a part that starts inside its problem, one that starts with
+    int how;        // how the CTAs divide the problems
+    // kLine: per slot (2 a CTA: a part that starts inside its problem, one that starts with
     // it) the problem and whether the part ends it, then maxima, row sums, sums
     int2 *meta;
     float *parts;
@@ -123,14 +125,18 @@ struct Segment {
     }
 };
 
-// The CTA's segments into `list`; returns their number.  Whole problems: those of index
-// blockIdx, blockIdx + gridDim, ... (nh = 0: no row sees a key).  The line: chunks
-// [total * blockIdx / gridDim, total * (blockIdx + 1) / gridDim).
+// The CTA's segments into `list`; returns their number.  Whole problems (how == kWhole): the
+// ones that have keys are dealt out forwards and backwards in turn, so that each CTA gets as
+// many and long ones meet short ones.  (Counting those of empty pairs too left some CTAs
+// four and others two: a ragged batch of 2 x 4001 tokens 99 -> 85 us.)  More entries than
+// `line` holds (kEvery): those of index blockIdx, blockIdx + gridDim, ..., without keys (nh =
+// 0) or not.  The line (kLine): chunks [total * blockIdx / gridDim, total * (blockIdx + 1) /
+// gridDim).
 __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list) {
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ int count;
-    if (!a.line) {
+    if (a.how == kEvery) {
         const int n = a.nprob > (int)blockIdx.x
                           ? (a.nprob - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
         for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -141,10 +147,13 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
         return n;
     }
     const int entries = a.npairs * p.B;
-    for (int e = threadIdx.x; e < entries; e += kThreads)
-        line[e + 1] = (entry_of(a, e).kt.count() + 1) / 2 * p.H;
+    for (int e = threadIdx.x; e < entries; e += kThreads) {
+        const int chunks = (entry_of(a, e).kt.count() + 1) / 2;
+        line[e + 1] = (a.how == kLine ? chunks : min(chunks, 1)) * p.H;
+    }
     if (threadIdx.x == 0) line[0] = 0;
-    if (threadIdx.x < 2) a.meta[2 * blockIdx.x + threadIdx.x] = make_int2(-1, 0);
+    if (a.how == kLine && threadIdx.x < 2)
+        a.meta[2 * blockIdx.x + threadIdx.x] = make_int2(-1, 0);
     __syncthreads();
     if (warp == 0) {
         int sum = 0;
@@ -158,7 +167,7 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
             if (e0 + lane <= entries) line[e0 + lane] = sum + x;
             sum += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) {
+        if (lane == 0 && a.how == kLine) {
             int at = (int)((int64_t)sum * blockIdx.x / gridDim.x), n = 0, e = 0;
             const int end = (int)((int64_t)sum * (blockIdx.x + 1) / gridDim.x);
             while (at < end && n < kMaxSegments) {
@@ -174,7 +183,25 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
         }
     }
     __syncthreads();
-    return count;
+    if (a.how == kLine) return count;
+    const int total = line[entries], rounds = (total + gridDim.x - 1) / gridDim.x;
+    auto problem = [&](int i) {
+        return i * (int)gridDim.x + (int)(i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    };
+    for (int i = threadIdx.x; i < rounds; i += kThreads) {
+        const int x = problem(i);
+        if (x >= total) continue;
+        int lo = 0, hi = entries;   // the entry with line[e] <= x < line[e + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            (line[mid] <= x ? lo : hi) = mid;
+        }
+        const KeyTiles kt = entry_of(a, lo).kt;
+        list[i] = Record{lo * p.H + (x - line[lo]), 0, kt.count(), kt.nA, kt.first, 1};
+    }
+    __syncthreads();
+    // (only the last round may be short of one)
+    return rounds == 0 || problem(rounds - 1) < total ? rounds : rounds - 1;
 }
 
 // Blocks j and j + 1 of a segment's keys or values to a stage: one box of 128 rows, or two
@@ -502,9 +529,10 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
             for (int c = 0; c < p.d / 8; c++) row[c] = make_uint4(0, 0, 0, 0);
             if (a.lse) a.lse[((int64_t)bb * p.H + h) * p.Nq + m] = -INFINITY;
         };
-        for (int e = 0; a.line && e < a.npairs * p.B; e++)   // (not in the line at all)
+        for (int e = 0; a.how != kEvery && e < a.npairs * p.B; e++)   // (in no segment)
             if (line[e + 1] == line[e])
-                for (int h = blockIdx.x; h < p.H; h += gridDim.x) write_zeros(e * p.H + h);
+                for (int h = (blockIdx.x + e) % gridDim.x; h < p.H; h += gridDim.x)
+                    write_zeros(e * p.H + h);
         for (int si = 0; ok && si < nseg; si++) {
             const Segment sg(a, list[si]);
             if (sg.nh == 0) {
@@ -736,11 +764,11 @@ cudaError_t launch(const WinProblem &p, const void *q, const void *k, const void
     if (e != cudaSuccess) return e;
     // (a CTA lists at most kMaxSegments problems: beyond, more CTAs than SMs)
     const int grid =
-        a.line ? sms : max(min(a.nprob, sms), (a.nprob + kMaxSegments - 1) / kMaxSegments);
+        a.how == kLine ? sms : max(min(a.nprob, sms), (a.nprob + kMaxSegments - 1) / kMaxSegments);
     tc_window_fwd_kernel<D><<<grid, kThreads, Layout<D>::kSmem, stream>>>(mq, mk, mv, mk128,
                                                                               mv128, a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !a.line) return e;
+    if (e != cudaSuccess || a.how != kLine) return e;
     window_join_kernel<D><<<dim3(grid, 16), 256, 0, stream>>>(a, grid);
     return cudaGetLastError();
 }
@@ -761,14 +789,15 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
     const int sms = tcs::sm_count();
     FwdArgs a;
     a.p = p;
-    a.line = use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms);
+    a.how = use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms) ? kLine : kWhole;
     // A tile alone on its SM takes little more than half of a pair's time a key block
     // (the two tiles share the exponentials' units), so where the pairs are fewer than
     // the SMs single tiles finish sooner: two padded causal batches of 1023 tokens with 8
     // heads 27 -> 22 us.
-    a.tiles = a.line || (p.Nq + 255) / 256 * p.B * p.H >= sms ? 2 : 1;
+    a.tiles = a.how == kLine || (p.Nq + 255) / 256 * p.B * p.H >= sms ? 2 : 1;
     a.npairs = (p.Nq + 128 * a.tiles - 1) / (128 * a.tiles);
     a.nprob = a.npairs * p.B * p.H;
+    if (a.how == kWhole && (int64_t)a.npairs * p.B > kMaxEntries) a.how = kEvery;
     a.meta = (int2 *)workspace;
     a.parts = (float *)((char *)workspace + meta_bytes(sms));
     a.out = (__nv_bfloat16 *)out;

@@ -220,6 +220,20 @@ def test_more_problems_than_sms(d):
     check(q, k, v, dout, window=(90, 0), sinks=2, lengths=ints(300, 141, 0), starts=0)
 
 
+@pytest.mark.parametrize("B,H,N,lens", [(3, 64, 900, (0, 900, 300)), (2, 40, 1300, (1300, 1)),
+                                        (300, 1, 300, None), (5, 3, 200, (0, 7, 200, 0, 129)),
+                                        (2, 96, 300, (0, 0))])
+def test_ragged_batches_over_the_ctas(B, H, N, lens):
+    """Problems without keys lie among the others, over one to several rounds of CTAs."""
+    q, k, v, _ = make(23, "bf16", B, H, 1, 32, N, N)
+    lens = ints(*(lens or [(97 * b) % (N + 1) for b in range(B)]))
+    for b, n in enumerate(lens.tolist()):
+        q[b, :, n:], k[b, :, n:], v[b, :, n:] = NAN, NAN, NAN
+    out, lse = check(q, k, v, window=(200, 0), sinks=1, lengths=lens, starts=0)
+    for b, n in enumerate(lens.tolist()):
+        assert (out[b, :, n:] == 0).all() and (lse[b, :, n:] == -float("inf")).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (16, 1)])
 def test_few_key_tiles_with_many_query_blocks(dtype, H, Hkv):
