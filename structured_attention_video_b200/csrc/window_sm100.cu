@@ -62,7 +62,7 @@ template <int D> struct Layout {
     static_assert(kSmem <= (uint32_t)kMaxSmem, "window attention shared memory");
 };
 
-enum { kEvery, kWhole, kLine };
+enum { kEvery, kReal, kLine };
 
 struct FwdArgs {
     WinProblem p;
@@ -125,22 +125,26 @@ struct Segment {
     }
 };
 
-// The CTA's segments into `list`; returns their number.  Whole problems (how == kWhole): the
-// ones that have keys are dealt out forwards and backwards in turn, so that each CTA gets as
-// many and long ones meet short ones.  (Counting those of empty pairs too left some CTAs
-// four and others two: a ragged batch of 2 x 4001 tokens 99 -> 85 us.)  More entries than
-// `line` holds (kEvery): those of index blockIdx, blockIdx + gridDim, ..., without keys (nh =
-// 0) or not.  The line (kLine): chunks [total * blockIdx / gridDim, total * (blockIdx + 1) /
-// gridDim).
+// The CTA's segments into `list`; returns their number.  Whole problems are dealt out
+// forwards and backwards in turn, so that each CTA gets as many and long ones meet short
+// ones: all of them (kEvery; nh = 0: no row sees a key), or those that have keys (kReal).
+// The line (kLine): chunks [total * blockIdx / gridDim, total * (blockIdx + 1) / gridDim).
 __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list) {
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ int count;
+    auto problem = [&](int i) {
+        return i * (int)gridDim.x + (int)(i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    };
+    // (only the last round may be short of one)
+    auto rounds_of = [&](int total) {
+        const int rounds = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+        return rounds == 0 || problem(rounds - 1) < total ? rounds : rounds - 1;
+    };
     if (a.how == kEvery) {
-        const int n = a.nprob > (int)blockIdx.x
-                          ? (a.nprob - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+        const int n = rounds_of(a.nprob);
         for (int i = threadIdx.x; i < n; i += kThreads) {
-            const int unit = blockIdx.x + i * gridDim.x;
+            const int unit = problem(i);
             const KeyTiles kt = entry_of(a, unit / p.H).kt;
             list[i] = Record{unit, 0, kt.count(), kt.nA, kt.first, 1};
         }
@@ -184,13 +188,9 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
     }
     __syncthreads();
     if (a.how == kLine) return count;
-    const int total = line[entries], rounds = (total + gridDim.x - 1) / gridDim.x;
-    auto problem = [&](int i) {
-        return i * (int)gridDim.x + (int)(i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    };
-    for (int i = threadIdx.x; i < rounds; i += kThreads) {
+    const int n = rounds_of(line[entries]);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
         const int x = problem(i);
-        if (x >= total) continue;
         int lo = 0, hi = entries;   // the entry with line[e] <= x < line[e + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
@@ -199,9 +199,7 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
         const KeyTiles kt = entry_of(a, lo).kt;
         list[i] = Record{lo * p.H + (x - line[lo]), 0, kt.count(), kt.nA, kt.first, 1};
     }
-    __syncthreads();
-    // (only the last round may be short of one)
-    return rounds == 0 || problem(rounds - 1) < total ? rounds : rounds - 1;
+    return n;
 }
 
 // Blocks j and j + 1 of a segment's keys or values to a stage: one box of 128 rows, or two
@@ -257,6 +255,7 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *line = reinterpret_cast<int *>(sm + L::kLine);
+    if (a.how == kLine) let_next_start();
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; t++) {
@@ -670,6 +669,7 @@ template <int D>
 __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
     const WinProblem &p = a.p;
     __shared__ int slots[kMaxCtas], parts;
+    wait_for_last();
     const int2 head = a.meta[2 * blockIdx.x + 1];
     if (head.x < 0) return;
     if (threadIdx.x < 32) {
@@ -769,8 +769,7 @@ cudaError_t launch(const WinProblem &p, const void *q, const void *k, const void
                                                                               mv128, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.how != kLine) return e;
-    window_join_kernel<D><<<dim3(grid, 16), 256, 0, stream>>>(a, grid);
-    return cudaGetLastError();
+    return launch_next(window_join_kernel<D>, dim3(grid, 16), 256, 0, stream, a, grid);
 }
 
 size_t meta_bytes(int sms) { return ((size_t)sms * 2 * sizeof(int2) + 255) & ~(size_t)255; }
@@ -789,7 +788,7 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
     const int sms = tcs::sm_count();
     FwdArgs a;
     a.p = p;
-    a.how = use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms) ? kLine : kWhole;
+    a.how = use_line(p, (p.Nq + 255) / 256 * p.B * p.H, sms) ? kLine : kEvery;
     // A tile alone on its SM takes little more than half of a pair's time a key block
     // (the two tiles share the exponentials' units), so where the pairs are fewer than
     // the SMs single tiles finish sooner: two padded causal batches of 1023 tokens with 8
@@ -797,7 +796,12 @@ cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const 
     a.tiles = a.how == kLine || (p.Nq + 255) / 256 * p.B * p.H >= sms ? 2 : 1;
     a.npairs = (p.Nq + 128 * a.tiles - 1) / (128 * a.tiles);
     a.nprob = a.npairs * p.B * p.H;
-    if (a.how == kWhole && (int64_t)a.npairs * p.B > kMaxEntries) a.how = kEvery;
+    // Several rounds of a ragged batch: problems without keys would leave some CTAs one
+    // round more than others (2 x 4001 tokens, the second sequence of 2667: 78.7 -> 75.2
+    // us).  With one round the list of the others only delays the start (two short batches
+    // 68 -> 72 us, forward and backward).
+    if (a.how == kEvery && p.lengths && a.nprob > sms && (int64_t)a.npairs * p.B <= kMaxEntries)
+        a.how = kReal;
     a.meta = (int2 *)workspace;
     a.parts = (float *)((char *)workspace + meta_bytes(sms));
     a.out = (__nv_bfloat16 *)out;
