@@ -625,6 +625,7 @@ __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, fl
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float safe = mx == -INFINITY ? 0.f : mx;
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
     for (int s = 0; s < a.clusters; s++) {
         const float *src = part + s * step;
         const float f = exp2f(src[p.d] - safe);
@@ -651,12 +652,41 @@ cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
 
 }  // namespace
 
-// Parts: about three CTAs an SM (two at a time of the bfloat16 kernel's, whose ring holds
-// what the memory's latency needs), none below two tiles of keys.  More parts balance
-// ragged lengths better and cost more prologues and joins: 8 x 8 heads of up to 4097 keys
-// 26-30 us at 1.7 to 3 CTAs an SM, 47 at 6; sixteen sequences up to 8192 keys 75 us at
-// 1.7, 66 at 3, 85 at 6; four of 131072 keys 409 us at 1, 260-265 at 2 to 4.  Up to 8 parts are
-// one cluster; more make clusters of one size each.
+// Parts of the visible keys.  More parts fill the SMs and even out ragged lengths; each
+// costs a prologue and a join, and parts beyond the clusters that fit on the device at once
+// (kFit: 72 of four CTAs where 71 fit take two rounds) another round.  Up to 8 parts are one
+// cluster, more are clusters of 8.
+//
+// bfloat16: the number with the least estimated time, in microseconds: rounds (two thirds
+// of them counted by what they hold, as lengths may be ragged) of tiles at the rate of the
+// ring's latency or the SM's share of the memory, 4 for a CTA's prologue and join, 2.5 and more
+// for the join of clusters.  Against as many as make three CTAs an SM: one sequence of 4000
+// keys, 12 heads 22.7 -> 14.8 us; 4 x 2000 keys, 8 key heads 24.6 -> 13.8; 24 x 6000 keys, 4 key
+// heads of 64 46.9 -> 32.3; four of 131072 keys 252 -> 239.
+// float32 (bound by the FMA pipes, five CTAs an SM): the power of two that makes at most 1024
+// CTAs.  Against three CTAs an SM: 24 ragged sequences up to 6000 keys, 4 key heads 173 -> 118
+// us (all of 6000: 186 -> 220), four up to 16384, 8 key heads 282 -> 202 (305 -> 297).
+int bf16_parts(int64_t units, double tiles, int d) {
+    static constexpr int kFit[2][8] = {{444, 222, 142, 104, 82, 71, 56, 48},   // d = 32, 64
+                                       {296, 148, 93, 71, 56, 45, 37, 33}};    // d = 128
+    const int *fit = kFit[d == 128];
+    const double latency = d == 128 ? 1.16 : 0.87, share = d == 128 ? 0.73 : 0.36;
+    int best = 1;
+    double least = 1e30;
+    for (int parts = 1; parts <= 512 && (parts == 1 || tiles >= 2 * parts);
+         parts = parts < 8 ? parts + 1 : 2 * parts) {
+        const int size = parts < kMaxCluster ? parts : kMaxCluster, groups = parts / size;
+        const int64_t clusters = units * groups, room = fit[size - 1];
+        const double held = max(1.0, (double)clusters / room);
+        const double rounds = ((double)((clusters + room - 1) / room) + 2 * held) / 3;
+        const int64_t per_sm = (min(clusters, room) * size + 147) / 148;
+        const double time = rounds * (tiles / parts * max(latency, per_sm * share) + 4) +
+                            (groups > 1 ? 2.5 + 0.1 * groups : 0);
+        if (time < least) least = time, best = parts;
+    }
+    return best;
+}
+
 TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
     TokenPlan t;
     t.row_tiles = (p.Nq * p.G + 15) / 16;
@@ -667,10 +697,11 @@ TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
         const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + p.Nq + p.frame;
         most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
     }
-    const int64_t tile = dtype == MONARCH_BF16 ? 64 : 32;
-    const int64_t want = (148 * 3 + units - 1) / units;
-    const int64_t room = max((int64_t)1, most / (tile * 2));
-    const int64_t parts = max((int64_t)1, min(min(want, room), (int64_t)1024));
+    int64_t parts = 1;
+    if (dtype == MONARCH_BF16)
+        parts = bf16_parts(units, most / 64.0, p.d);
+    else
+        while (units * parts * 2 <= 1024 && most >= 32 * 2 * (parts * 2)) parts *= 2;
     t.clusters = (int)((parts + kMaxCluster - 1) / kMaxCluster);
     t.splits = (int)((parts + t.clusters - 1) / t.clusters) * t.clusters;
     t.bytes = t.clusters > 1 ? (size_t)units * t.clusters * 16 * (p.d + 2) * sizeof(float) : 0;

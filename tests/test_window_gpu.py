@@ -214,6 +214,21 @@ def test_few_queries_against_long_caches(dtype, d, mask):
     check(q[:1, :1], k[:1], v[:1], window=window, sinks=sinks, frame=frame)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,Hkv,d,lens", [(2, 2, 1, 64, (40000, 3)), (1, 5, 1, 128, (30011,)),
+                                            (9, 8, 8, 128, (4097, 1, 0, 65, 640, 2049, 7, 4000, 64)),
+                                            (40, 2, 2, 32, None), (300, 2, 2, 64, None)])
+def test_parts_of_every_number(dtype, B, H, Hkv, d, lens):
+    """From one part a sequence to hundreds in many clusters, most of them empty for short
+    sequences; windows that leave some parts nothing."""
+    lens = list(lens or [(53 * b) % 400 for b in range(B)])
+    q, k, v, _ = make(24, dtype, B, H, Hkv, d, 1, max(max(lens), 1))
+    for b, n in enumerate(lens):
+        k[b, :, n:], v[b, :, n:] = NAN, NAN
+    for window, sinks in (((-1, 0), 0), ((2999, 0), 70)):
+        check(q, k, v, window=window, sinks=sinks, lengths=ints(*lens))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_more_problems_than_sms(d):
     q, k, v, dout = make(21, "bf16", 3, 64, 64, d, 300, 300)
