@@ -152,6 +152,13 @@ cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Groups of this thread's asynchronous copies (cp.async).
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's copies have landed.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The gradients' tensors of a backward call.
 struct WinGrads {
     Strides dout, dq, dk, dv;

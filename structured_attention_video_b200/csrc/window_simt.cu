@@ -51,12 +51,6 @@ __device__ __forceinline__ void load_rows(float *sm, const float *base, int64_t 
                      : "memory");
     }
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest N groups of this thread's copies have landed.
-template <int N> __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Two stages of the streamed tiles, the next one's copies behind this one's arithmetic,
 // where two CTAs with them fit on an SM; at d = 128 two CTAs of one stage do instead.
 template <int D> constexpr int kStages = D == 128 ? 1 : 2;

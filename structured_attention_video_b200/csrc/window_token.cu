@@ -20,7 +20,7 @@
 // the memory's latency needs whatever the warps wait for; loading fragments straight
 // from global memory to registers reached 4.1 TB/s instead.  (The products need a tenth of
 // the legacy tensor rate here; tcgen05 would spend a 128-row tile on 16 rows.)
-// float32: FMA pipes, tiles of 32 keys through shared memory, one lane a key.
+// float32: FMA pipes, tiles of 32 keys through shared memory.
 #include "window_tc.cuh"
 
 #include <cooperative_groups.h>
@@ -189,6 +189,34 @@ __device__ __forceinline__ void join_cluster(const TokenArgs &a, const TokenUnit
         }
     }
     if (parts > 1) cluster.sync();   // the others have read this CTA's part
+}
+
+// The CTA's part from those of its four warps, which lie behind it.
+template <int D> __device__ __forceinline__ void join_warps(float *part, int rows) {
+    constexpr int kPitch = Part<D>::kPitch, kFloats = Part<D>::kFloats;
+    for (int at = threadIdx.x; at < rows * (D / 4); at += blockDim.x) {
+        const int r = at / (D / 4), c = at % (D / 4) * 4;
+        const float *src = part + kFloats;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kTokWarps; x++) mx = fmaxf(mx, src[x * kFloats + 16 * kPitch + r]);
+        const float safe = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kTokWarps; x++) {
+            const float *s = src + x * kFloats;
+            const float f = exp2f(s[16 * kPitch + r] - safe);
+            const float4 y = *reinterpret_cast<const float4 *>(s + r * kPitch + c);
+            sum = fmaf(f, s[16 * kPitch + 16 + r], sum);
+            acc.x = fmaf(f, y.x, acc.x);
+            acc.y = fmaf(f, y.y, acc.y);
+            acc.z = fmaf(f, y.z, acc.z);
+            acc.w = fmaf(f, y.w, acc.w);
+        }
+        *reinterpret_cast<float4 *>(part + r * kPitch + c) = acc;
+        if (c == 0) part[16 * kPitch + r] = mx, part[16 * kPitch + 16 + r] = sum;
+    }
 }
 
 // ---------------------------------------------------------------- bfloat16
@@ -464,142 +492,153 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
         }
     }
     __syncthreads();
-    const int real = min(16, rows - u.rt * 16);
-    for (int at = threadIdx.x; at < real * (D / 4); at += blockDim.x) {
-        const int r = at / (D / 4), c = at % (D / 4) * 4;
-        const float *src = part + kFloats;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kTokWarps; x++) mx = fmaxf(mx, src[x * kFloats + 16 * kPitch + r]);
-        const float safe = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kTokWarps; x++) {
-            const float *s = src + x * kFloats;
-            const float f = exp2f(s[16 * kPitch + r] - safe);
-            const float4 y = *reinterpret_cast<const float4 *>(s + r * kPitch + c);
-            sum = fmaf(f, s[16 * kPitch + 16 + r], sum);
-            acc.x = fmaf(f, y.x, acc.x);
-            acc.y = fmaf(f, y.y, acc.y);
-            acc.z = fmaf(f, y.z, acc.z);
-            acc.w = fmaf(f, y.w, acc.w);
-        }
-        *reinterpret_cast<float4 *>(part + r * kPitch + c) = acc;
-        if (c == 0) part[16 * kPitch + r] = mx, part[16 * kPitch + 16 + r] = sum;
-    }
+    join_warps<D>(part, min(16, rows - u.rt * 16));
     join_cluster<D>(a, u, part, out, lse);
 }
 
 // ---------------------------------------------------------------- float32
-// Warp w owns rows w, w + 4, w + 8, w + 12 of the tile; lane = key in the logits and
-// column (mod 32) in the output.
-template <int D>
+// 16 bytes to shared memory, asynchronously; zeros where `there` is false.
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// Tiles of 32 keys, the next one's copies behind this one's arithmetic; 8 keys a warp.  In the logits four lanes share a key, a quarter of the
+// columns each, which stay in registers for all rows (at most R); in the output a lane has
+// columns lane, lane + 32, ..., and a value serves all rows.  Each warp has its own maxima
+// and sums; they join at the end.  Bound by memory up to four rows (8 key heads of 32768
+// keys, d = 128: 70.6 us, 3.8 TB/s), then by the FMA pipes.  One tile at a time, its rows
+// divided among the warps and a lane a key, took 128; 24 sequences of 6000 keys, 4 heads a
+// key head 186 us instead of 101.
+template <int D, int R>
 __global__ void __launch_bounds__(kTokThreads)
 token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, float *out,
                  float *lse) {
-    constexpr int P = D + 4;
-    __shared__ __align__(16) float buf[16 * D + 32 * P + 32 * D];
-    static_assert(Part<D>::kFloats <= 16 * D + 32 * P + 32 * D, "the part fits the buffer");
-    float *sq = buf, *sk = sq + 16 * D, *sv = sk + 32 * P;
+    constexpr int P = D + 4, C = D / 32, kTile = 32 * P + 32 * D;
+    extern __shared__ __align__(16) float buf[];   // two tiles of keys and values, q, sp
+    __shared__ RowKeys row_range[R];
+    float *sq = buf + 2 * kTile;
     const WinProblem &p = a.p;
     if (a.clusters > 1) let_next_start();
     const TokenUnit u = token_unit<32>(a);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = p.Nq * p.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
+    float *sp = sq + 16 * D + warp * R * 8;   // the warp's probabilities, [row][8]
+    const int rows = min(R, p.Nq * p.G - u.rt * 16);
     const float *kb = k + u.hk * p.k.head + (p.table ? 0 : u.b * p.k.batch);
     const float *vb = v + u.hk * p.v.head + (p.table ? 0 : u.b * p.v.batch);
     const KeyPlace kp = key_place(p, u.b, p.k.token, p.k.batch, a.status);
     const KeyPlace vp = key_place(p, u.b, p.v.token, p.v.batch, a.status);
-    for (int x = threadIdx.x; x < 16 * D / 4; x += kTokThreads) {
+    for (int x = threadIdx.x; x < rows * D / 4; x += kTokThreads) {
         const int r = x / (D / 4), c = x % (D / 4) * 4, rr = u.rt * 16 + r;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (rr < rows)
-            y = *reinterpret_cast<const float4 *>(q + u.b * p.q.batch +
-                                                  (u.hk * p.G + rr % p.G) * p.q.head +
-                                                  (rr / p.G) * p.q.token + c);
-        *reinterpret_cast<float4 *>(sq + r * D + c) = y;
+        *reinterpret_cast<float4 *>(sq + r * D + c) = *reinterpret_cast<const float4 *>(
+            q + u.b * p.q.batch + (u.hk * p.G + rr % p.G) * p.q.head + (rr / p.G) * p.q.token + c);
     }
-    RowKeys rk[4];
-    float m[4], l[4], o[4][D / 32];
+    if (threadIdx.x < rows) row_range[threadIdx.x] = row_keys(p, u.seq, (u.rt * 16 + threadIdx.x) / p.G);
+    float m[R], l[R], o[R][C];
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
-        const int rr = u.rt * 16 + warp + 4 * x;
-        rk[x] = RowKeys{0, 0, 0};
-        if (rr < rows) rk[x] = row_keys(p, u.seq, rr / p.G);
-        m[x] = -INFINITY;
-        l[x] = 0.f;
+    for (int r = 0; r < R; r++) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 32; c++) o[x][c] = 0.f;
+        for (int c = 0; c < C; c++) o[r][c] = 0.f;
     }
-    for (int g = u.g0; g < u.g1; g++) {
+    // tile g to its buffer, asynchronously; keys that no row sees, or whose page does not
+    // exist, become zeros
+    auto load = [&](int g) {
         const int j0 = u.kt.tile(g) * 32;
-        __syncthreads();
+        float *sk = buf + (g & 1) * kTile, *sv = sk + 32 * P;
         for (int x = threadIdx.x; x < 32 * D / 4; x += kTokThreads) {
             const int r = x / (D / 4), c = x % (D / 4) * 4, j = j0 + r;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-            if (u.any.sees(j)) {
-                const int64_t ka = kp.at(j), va = vp.at(j);
-                if (ka >= 0) y = *reinterpret_cast<const float4 *>(kb + ka + c);
-                if (va >= 0) z = *reinterpret_cast<const float4 *>(vb + va + c);
-            }
-            *reinterpret_cast<float4 *>(sk + r * P + c) = y;
-            *reinterpret_cast<float4 *>(sv + r * D + c) = z;
+            int64_t ka = -1, va = -1;
+            if (u.any.sees(j)) ka = kp.at(j), va = vp.at(j);
+            copy16(sk + r * P + c, kb + (ka >= 0 ? ka + c : 0), ka >= 0);
+            copy16(sv + r * D + c, vb + (va >= 0 ? va + c : 0), va >= 0);
         }
+    };
+    if (u.g0 < u.g1) load(u.g0);
+    copies_commit();
+    for (int g = u.g0; g < u.g1; g++) {
+        const int j0 = u.kt.tile(g) * 32;
+        const float *sk = buf + (g & 1) * kTile, *sv = sk + 32 * P;
+        __syncthreads();   // the other buffer's last readers are done
+        if (g + 1 < u.g1) load(g + 1);
+        copies_commit();
+        copies_wait<1>();
         __syncthreads();
-        const int j = j0 + lane;
+        const int j = j0 + warp * 8 + key;
         const bool there = u.any.sees(j) && kp.at(j) >= 0;
+        float4 kr[D / 16];
+        const float *kp4 = sk + (warp * 8 + key) * P + quarter * (D / 4);
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-            if (u.rt * 16 + warp + 4 * x >= rows) continue;   // the same for the whole warp
-            const float *qr = sq + (warp + 4 * x) * D, *kr = sk + lane * P;
+        for (int c = 0; c < D / 16; c++) kr[c] = *reinterpret_cast<const float4 *>(kp4 + 4 * c);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            if (r >= rows) break;   // the same for the whole CTA
+            const float *qr = sq + r * D + quarter * (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = 0; c < D; c += 4) {
-                const float4 qa = *reinterpret_cast<const float4 *>(qr + c);
-                const float4 ka = *reinterpret_cast<const float4 *>(kr + c);
-                acc.x = fmaf(qa.x, ka.x, acc.x);
-                acc.y = fmaf(qa.y, ka.y, acc.y);
-                acc.z = fmaf(qa.z, ka.z, acc.z);
-                acc.w = fmaf(qa.w, ka.w, acc.w);
+#pragma unroll
+            for (int c = 0; c < D / 16; c++) {
+                const float4 y = *reinterpret_cast<const float4 *>(qr + 4 * c);
+                acc.x = fmaf(y.x, kr[c].x, acc.x);
+                acc.y = fmaf(y.y, kr[c].y, acc.y);
+                acc.z = fmaf(y.z, kr[c].z, acc.z);
+                acc.w = fmaf(y.w, kr[c].w, acc.w);
             }
-            const float z = there && rk[x].sees(j)
-                                ? ((acc.x + acc.y) + (acc.z + acc.w)) * p.scale_log2
-                                : -INFINITY;
+            float z = (acc.x + acc.y) + (acc.z + acc.w);
+            z += __shfl_xor_sync(0xffffffffu, z, 8);
+            z += __shfl_xor_sync(0xffffffffu, z, 16);
+            z = there && row_range[r].sees(j) ? z * p.scale_log2 : -INFINITY;
             float mx = z;
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = fmaxf(mx, m[x]);
+            for (int s = 4; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            mx = fmaxf(mx, m[r]);
             const float safe = mx == -INFINITY ? 0.f : mx;
-            const float alpha = exp2f(m[x] - safe), e = exp2f(z - safe);
-            m[x] = mx;
-            l[x] = l[x] * alpha + e;
+            const float alpha = exp2f(m[r] - safe), e = exp2f(z - safe);
+            m[r] = mx;
+            l[r] = l[r] * alpha + e;   // of this lane's key
 #pragma unroll
-            for (int c = 0; c < D / 32; c++) o[x][c] *= alpha;
-#pragma unroll 4
-            for (int jj = 0; jj < 32; jj++) {
-                const float w = __shfl_sync(0xffffffffu, e, jj);
+            for (int c = 0; c < C; c++) o[r][c] *= alpha;
+            if (quarter == 0) sp[r * 8 + key] = e;
+        }
+        __syncwarp();
 #pragma unroll
-                for (int c = 0; c < D / 32; c++)
-                    o[x][c] = fmaf(w, sv[jj * D + c * 32 + lane], o[x][c]);
+        for (int jj = 0; jj < 8; jj += 4) {
+            float vr[4][C];
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+#pragma unroll
+                for (int c = 0; c < C; c++) vr[x][c] = sv[(warp * 8 + jj + x) * D + c * 32 + lane];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                if (r >= rows) break;
+                const float4 w = *reinterpret_cast<const float4 *>(sp + r * 8 + jj);
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    o[r][c] = fmaf(w.w, vr[3][c], fmaf(w.z, vr[2][c], fmaf(w.y, vr[1][c],
+                                                                        fmaf(w.x, vr[0][c], o[r][c]))));
             }
         }
     }
-    // the CTA's part over the tile buffer (every warp is done with it)
+    // the warps' parts, then the CTA's, over the tiles (every warp is done with them, and no
+    // copy is under way)
+    copies_wait<0>();
     __syncthreads();
-    float *part = buf;
     constexpr int kPitch = Part<D>::kPitch;
+    static_assert(5 * Part<D>::kFloats <= 2 * kTile, "the parts fit the tiles");
+    float *part = buf, *mine = part + (1 + warp) * Part<D>::kFloats;
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
-        const int r = warp + 4 * x;
-        if (u.rt * 16 + r >= rows) continue;
-        float sum = l[x];
+    for (int r = 0; r < R; r++) {
+        if (r >= rows) break;
+        float sum = l[r];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        for (int s = 4; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
 #pragma unroll
-        for (int c = 0; c < D / 32; c++) part[r * kPitch + c * 32 + lane] = o[x][c];
-        if (lane == 0) part[16 * kPitch + r] = m[x], part[16 * kPitch + 16 + r] = sum;
+        for (int c = 0; c < C; c++) mine[r * kPitch + c * 32 + lane] = o[r][c];
+        if (lane == 0) mine[16 * kPitch + r] = m[r], mine[16 * kPitch + 16 + r] = sum;
     }
+    __syncthreads();
+    join_warps<D>(part, rows);
     join_cluster<D>(a, u, part, out, lse);
 }
 
@@ -657,16 +696,14 @@ cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
 // (kFit: 72 of four CTAs where 71 fit take two rounds) another round.  Up to 8 parts are one
 // cluster, more are clusters of 8.
 //
-// bfloat16: the number with the least estimated time, in microseconds: rounds (two thirds
-// of them counted by what they hold, as lengths may be ragged) of tiles at the rate of the
-// ring's latency or the SM's share of the memory, 4 for a CTA's prologue and join, 2.5 and more
-// for the join of clusters.  Against as many as make three CTAs an SM: one sequence of 4000
-// keys, 12 heads 22.7 -> 14.8 us; 4 x 2000 keys, 8 key heads 24.6 -> 13.8; 24 x 6000 keys, 4 key
-// heads of 64 46.9 -> 32.3; four of 131072 keys 252 -> 239.
-// float32 (bound by the FMA pipes, five CTAs an SM): the power of two that makes at most 1024
-// CTAs.  Against three CTAs an SM: 24 ragged sequences up to 6000 keys, 4 key heads 173 -> 118
-// us (all of 6000: 186 -> 220), four up to 16384, 8 key heads 282 -> 202 (305 -> 297).
-int bf16_parts(int64_t units, double tiles, int d) {
+// Taken is the number with the least estimated time, in microseconds: rounds (two thirds of
+// them counted by what they hold, as lengths may be ragged) of tiles at the rate of the
+// latency of a CTA's copies or of the SM's share of the memory, 4 for a CTA's prologue and
+// join, 2.5 and more for the join of clusters.  Against as many as make three CTAs an SM,
+// bfloat16: one sequence of 4000 keys, 12 heads 22.7 -> 14.8 us; 4 x 2000 keys, 8 key heads
+// 24.6 -> 13.8; 24 x 6000 keys, 4 key heads of 64 46.9 -> 32.3; four of 131072 keys 252 -> 242.
+// A float32 tile has half the keys and the same bytes.
+int parts_of(int64_t units, double tiles, int d) {
     static constexpr int kFit[2][8] = {{444, 222, 142, 104, 82, 71, 56, 48},   // d = 32, 64
                                        {296, 148, 93, 71, 56, 45, 37, 33}};    // d = 128
     const int *fit = kFit[d == 128];
@@ -697,11 +734,8 @@ TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
         const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + p.Nq + p.frame;
         most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
     }
-    int64_t parts = 1;
-    if (dtype == MONARCH_BF16)
-        parts = bf16_parts(units, most / 64.0, p.d);
-    else
-        while (units * parts * 2 <= 1024 && most >= 32 * 2 * (parts * 2)) parts *= 2;
+    // (a tile of 64 bfloat16 or 32 float32 keys)
+    const int64_t parts = parts_of(units, most / (dtype == MONARCH_BF16 ? 64.0 : 32.0), p.d);
     t.clusters = (int)((parts + kMaxCluster - 1) / kMaxCluster);
     t.splits = (int)((parts + t.clusters - 1) / t.clusters) * t.clusters;
     t.bytes = t.clusters > 1 ? (size_t)units * t.clusters * 16 * (p.d + 2) * sizeof(float) : 0;
@@ -732,7 +766,12 @@ cudaError_t launch_parts(void (*kernel)(Params...), const TokenArgs &a, const di
 template <int D>
 cudaError_t launch_f32(const TokenArgs &a, const dim3 &grid, const void *q, const void *k,
                        const void *v, void *out, float *lse, cudaStream_t stream) {
-    return launch_parts(token_f32_kernel<D>, a, grid, kTokThreads, 0, stream, a, (const float *)q,
+    const bool few = a.p.Nq * a.p.G <= 4;
+    const auto kernel = few ? token_f32_kernel<D, 4> : token_f32_kernel<D, 16>;
+    const uint32_t smem = (2 * (32 * (D + 4) + 32 * D) + 16 * D + kTokWarps * (few ? 4 : 16) * 8) * 4;
+    const cudaError_t e = tcs::set_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_parts(kernel, a, grid, kTokThreads, smem, stream, a, (const float *)q,
                         (const float *)k, (const float *)v, (float *)out, lse);
 }
 
