@@ -293,12 +293,10 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
     // query blocks over the group's heads; this CTA's
     const int u0 = (int)((int64_t)nt * p.G * split / a.splits);
     const int n = (int)((int64_t)nt * p.G * (split + 1) / a.splits) - u0;
-    if (a.splits > 1) let_next_start();
     // (row of this CTA's part: dV, then dK, in 32 bits)
     float *const part_base = a.parts + (int64_t)blockIdx.x * 128 * 2 * D;
 
     if (n == 0) {             // no query sees these keys (the same for the whole CTA)
-        wait_for_last();
         const int j = j0 + threadIdx.x;
         if (a.splits > 1) {
             for (int x = threadIdx.x; x < 128 * 2 * D / 4; x += kThreads)
@@ -345,7 +343,6 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         // -lse (in log2 units) and -delta of each block's queries.  (A warp of its own: in
         // the loading warp, its global reads held up the copies, 722 -> 915 us.)
         Slot<N1> cur;
-        wait_for_last();   // delta
         for (int u = 0; u < n; u++) {
             int h, i0;
             coords(u, h, i0);
@@ -527,7 +524,6 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
 template <int D>
 __global__ void __launch_bounds__(256) window_dkv_join_kernel(BwdArgs a) {
     const WinProblem &p = a.p;
-    wait_for_last();
     const int tile_unit = blockIdx.x, unit = tile_unit % (p.B * p.Hkv);
     const int hk = unit % p.Hkv, b = unit / p.Hkv, j0 = tile_unit / (p.B * p.Hkv) * 128;
     const Sequence seq = sequence(p, b);
@@ -579,10 +575,8 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
     // the first n - nt blocks only sum delta
     const int n = nt <= kExactBlocks ? 2 * nt : nt;
     __nv_bfloat16 *const dq = a.dq + b * a.g.dq.batch + h * a.g.dq.head;
-    let_next_start();
 
     if (n == 0) {
-        wait_for_last();
         const int i = i0 + threadIdx.x;
         if (threadIdx.x < 128 && i < p.Nq) zero_row(dq + (int64_t)i * a.g.dq.token, p.d);
         return;
@@ -672,7 +666,6 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
         const bool real = rk.hi > 0;   // (others take every key, and zeros are stored)
         if (!real) rk = RowKeys{0, 0x7fffffff, 0};
         const float nl = real ? -a.lse[at] * kLog2e : 0.f;
-        wait_for_last();   // delta
         float nd = real && n == nt ? -a.delta[at] : 0.f;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
         bool ok = true, summed = n == nt;
@@ -777,13 +770,14 @@ cudaError_t launch(const WinProblem &p, const WinGrads &g, const void *q, const 
     const unsigned gk = key_tiles * a.splits;
     const unsigned gq = (unsigned)p.B * p.H * ((p.Nq + 127) / 128);
     // dq first: it completes delta
-    e = launch_next(tc_window_dq_kernel<D>, dim3(gq), kThreads, smem_dq, stream, k64, v64, a);
+    tc_window_dq_kernel<D><<<gq, kThreads, smem_dq, stream>>>(k64, v64, a);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_next(tc_window_dkv_kernel<D>, dim3(gk), kThreads, smem_dkv, stream, q64, k128, v128,
-                    d64, a);
+    tc_window_dkv_kernel<D><<<gk, kThreads, smem_dkv, stream>>>(q64, k128, v128, d64, a);
+    e = cudaGetLastError();
     if (e != cudaSuccess || a.splits == 1) return e;
-    return launch_next(window_dkv_join_kernel<D>, dim3(key_tiles, 128 * 2 * D / 4 / 256), 256, 0,
-                       stream, a);
+    window_dkv_join_kernel<D><<<dim3(key_tiles, 128 * 2 * D / 4 / 256), 256, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 // Parts of a key tile's query blocks in the dk/dv kernel: where the key tiles are fewer

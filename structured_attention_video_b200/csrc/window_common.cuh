@@ -125,33 +125,6 @@ __device__ __forceinline__ void query_rows(const WinProblem &p, const Sequence &
     last = (int)max(hi, (int64_t)0);
 }
 
-// The bfloat16 backward's kernels and the joins start while the kernel before them still
-// runs (a call's first starts when everything earlier in the stream is done, so inputs may
-// be read at once): training on 2 x 1023 tokens 56.1 -> 53.9 us.  In the float32 backward, two
-// CTAs an SM, the early ones get in the way: 780 tokens 117 -> 133.  Each kernel lets the next one start as soon as its own CTAs have, and each CTA waits for
-// the end of the kernel before it touches what that wrote, or at the latest before it
-// exits: the end of a call's last kernel is then the end of them all.
-__device__ __forceinline__ void let_next_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... Params, typename... Args>
-cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                        cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Groups of this thread's asynchronous copies (cp.async).
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest N groups of this thread's copies have landed.

@@ -453,7 +453,6 @@ row_delta_kernel(WinProblem p, WinGrads g, const T *out, const T *dout, float *d
     constexpr int V = 16 / sizeof(T), LANES = D / V, ROWS = 256 / LANES;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
     const int x = threadIdx.x % LANES * V;
-    let_next_start();   // (the bfloat16 dq kernel; the float32 ones, two CTAs an SM, lose by it)
     float sum = 0.f;
     if (row < (int64_t)p.B * p.H * p.Nq) {
         const int i = (int)(row % p.Nq), bh = (int)(row / p.Nq), h = bh % p.H, b = bh / p.H;

@@ -255,7 +255,6 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *line = reinterpret_cast<int *>(sm + L::kLine);
-    if (a.how == kLine) let_next_start();
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; t++) {
@@ -669,7 +668,6 @@ template <int D>
 __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
     const WinProblem &p = a.p;
     __shared__ int slots[kMaxCtas], parts;
-    wait_for_last();
     const int2 head = a.meta[2 * blockIdx.x + 1];
     if (head.x < 0) return;
     if (threadIdx.x < 32) {
@@ -769,7 +767,8 @@ cudaError_t launch(const WinProblem &p, const void *q, const void *k, const void
                                                                               mv128, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.how != kLine) return e;
-    return launch_next(window_join_kernel<D>, dim3(grid, 16), 256, 0, stream, a, grid);
+    window_join_kernel<D><<<dim3(grid, 16), 256, 0, stream>>>(a, grid);
+    return cudaGetLastError();
 }
 
 size_t meta_bytes(int sms) { return ((size_t)sms * 2 * sizeof(int2) + 255) & ~(size_t)255; }

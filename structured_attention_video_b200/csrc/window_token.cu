@@ -274,7 +274,6 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
     volatile uint32_t *good = reinterpret_cast<volatile uint32_t *>(empty + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + NS) + NS;
     const WinProblem &p = a.p;
-    if (a.clusters > 1) let_next_start();
     if (threadIdx.x == 0) {
         prefetch_map(&tmK);
         prefetch_map(&tmV);
@@ -520,7 +519,6 @@ token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, fl
     __shared__ RowKeys row_range[R];
     float *sq = buf + 2 * kTile;
     const WinProblem &p = a.p;
-    if (a.clusters > 1) let_next_start();
     const TokenUnit u = token_unit<32>(a);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
     float *sp = sq + 16 * D + warp * R * 8;   // the warp's probabilities, [row][8]
@@ -646,7 +644,6 @@ token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, fl
 // One warp a row (query, head).
 template <typename T>
 __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, float *lse) {
-    wait_for_last();
     const WinProblem &p = a.p;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, rows = p.Nq * p.G;
@@ -685,8 +682,8 @@ __global__ void __launch_bounds__(256) token_join_kernel(TokenArgs a, T *out, fl
 template <typename T>
 cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.p.B * a.p.H * a.p.Nq;
-    return launch_next(token_join_kernel<T>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, a, out,
-                       lse);
+    token_join_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a, out, lse);
+    return cudaGetLastError();
 }
 
 }  // namespace
