@@ -141,7 +141,7 @@ size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc) {
     const int path = choose(p, desc->dtype);
     return at_least_256(path == kPathToken    ? win::token_plan(p, desc->dtype).bytes
                         : path == kPathTensor ? win::tc_forward_bytes(p)
-                                              : 0);
+                                              : win::simt_forward_bytes(p));
 }
 
 int monarch_window_attn_path(const monarch_window_desc *desc) {
@@ -165,11 +165,12 @@ monarch_status monarch_window_attn_fwd_ws(const monarch_window_desc *desc, const
     cudaStream_t s = (cudaStream_t)stream;
     if (path == kPathToken)
         return run_token(p, desc->dtype, q, k, v, out, lse, workspace, ws_bytes, s);
+    const monarch_status ws = check_workspace(
+        path == kPathSimt ? win::simt_forward_bytes(p) : win::tc_forward_bytes(p), workspace, ws_bytes);
+    if (ws != MONARCH_OK) return ws;
     if (path == kPathSimt)
         return status_of(win::simt_forward(p, (const float *)q, (const float *)k, (const float *)v,
-                                           (float *)out, lse, s));
-    const monarch_status ws = check_workspace(win::tc_forward_bytes(p), workspace, ws_bytes);
-    if (ws != MONARCH_OK) return ws;
+                                           (float *)out, lse, workspace, s));
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
     return status_of(
@@ -180,7 +181,8 @@ size_t monarch_window_attn_bwd_workspace_bytes(const monarch_window_desc *desc) 
     WinProblem p;
     if (validate_window(desc, &p) != MONARCH_OK) return 0;
     return at_least_256(delta_bytes(p) +
-                        (desc->dtype == MONARCH_BF16 ? win::tc_backward_bytes(p) : 0));
+                        (desc->dtype == MONARCH_BF16 ? win::tc_backward_bytes(p)
+                                                     : win::simt_backward_bytes(p)));
 }
 
 monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
@@ -214,7 +216,8 @@ monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
     if (desc->dtype == MONARCH_F32)
         return status_of(win::simt_backward(p, g, (const float *)q, (const float *)k,
                                             (const float *)v, lse, delta, (const float *)dout,
-                                            (float *)dq, (float *)dk, (float *)dv, s));
+                                            (float *)dq, (float *)dk, (float *)dv,
+                                            (char *)workspace + delta_bytes(p), s));
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
     return status_of(win::tc_backward(p, g, q, k, v, lse, delta, dout, dq, dk, dv,

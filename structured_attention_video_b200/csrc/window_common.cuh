@@ -12,6 +12,8 @@
 
 #include "monarch_common.cuh"
 
+#include <algorithm>
+
 namespace monarch {
 namespace win {
 
@@ -132,17 +134,32 @@ template <int N> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The most keys that a tile of `rows` queries can meet, from the mask and the tensors' sizes
+// (lengths are on the device); the most queries that a tile of keys can.
+inline int64_t most_keys(const WinProblem &p, int64_t rows) {
+    if (p.left < 0 || p.right < 0) return p.Nk;
+    const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + rows + p.frame;
+    return std::min<int64_t>(p.Nk, span + std::min<int64_t>(p.sink_end, p.Nk));
+}
+inline int64_t most_queries(const WinProblem &p, int64_t keys) {
+    if (p.left < 0 || p.right < 0 || p.sink_end > 0) return p.Nq;
+    return std::min<int64_t>(p.Nq, ((int64_t)p.left + p.right + 1) * p.frame + keys + p.frame);
+}
+
 // The gradients' tensors of a backward call.
 struct WinGrads {
     Strides dout, dq, dk, dv;
 };
 
-// SIMT kernels, 32-bit arithmetic (window_simt.cu).
+// SIMT kernels, 32-bit arithmetic (window_simt.cu).  Workspace bytes, 0 where none are
+// needed.
+size_t simt_forward_bytes(const WinProblem &p);
 cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, const float *v,
-                         float *out, float *lse, cudaStream_t stream);
+                         float *out, float *lse, void *workspace, cudaStream_t stream);
+size_t simt_backward_bytes(const WinProblem &p);   // of `parts`
 cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                           const float *v, const float *lse, const float *delta, const float *dout,
-                          float *dq, float *dk, float *dv, cudaStream_t stream);
+                          float *dq, float *dk, float *dv, void *parts, cudaStream_t stream);
 // delta_i = dO_i . O_i of every query row, [B][H][Nq].
 cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
                       const void *dout, float *delta, cudaStream_t stream);

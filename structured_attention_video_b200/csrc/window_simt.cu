@@ -150,6 +150,16 @@ __device__ __forceinline__ float half_warp_sum(float x) {
     return x;
 }
 
+// The streamed tiles of part blockIdx.z of gridDim.z: [part_begin, part_end) of n.
+__device__ __forceinline__ int part_begin(int n) { return (int)((int64_t)n * blockIdx.z / gridDim.z); }
+__device__ __forceinline__ int part_end(int n) {
+    return (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+}
+// This part's rows of this head: [part][head][row][D].
+template <int D> __device__ __forceinline__ float *part_rows(float *parts, int rows) {
+    return parts + ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * rows * D;
+}
+
 // ---------------------------------------------------------------- forward
 // 16 RT queries of one head against tiles of 64 keys.  With one stage K and V take turns
 // in one buffer.
@@ -161,7 +171,7 @@ constexpr int fwd_smem() {
 template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, float *out,
-                float *lse) {
+                float *lse, float *parts) {
     extern __shared__ __align__(16) float smf[];
     constexpr int kTileFloats = 64 * kPitch<D>;
     float *sq = smf, *sp = sq + 16 * RT * kPitch<D>, *skv = sp + 16 * RT * 68;
@@ -173,10 +183,10 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
     load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    const int first = part_begin(kt.count()), n = part_end(kt.count()) - first;
     auto load = [&](float *dst, const float *src, int64_t stride, int it) {
-        load_rows<D, 64>(dst, src, stride, kt.tile(it) * 64, seq.len);
+        load_rows<D, 64>(dst, src, stride, kt.tile(first + it) * 64, seq.len);
     };
-    const int n = kt.count();
     if (kStages<D> == 2 && n > 0) {
         load(skv, kb, p.k.token, 0);
         load(skv + kTileFloats, vb, p.v.token, 0);
@@ -194,7 +204,7 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
         for (int x = 0; x < D / 32; x++) o[i][x] = 0;
     }
     for (int it = 0; it < n; it++) {
-        const int j0 = kt.tile(it) * 64;
+        const int j0 = kt.tile(first + it) * 64;
         const float *sk = skv, *sv = skv;
         __syncthreads();   // the buffer's last readers are done
         if (kStages<D> == 2) {
@@ -255,6 +265,14 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
 #pragma unroll
     for (int i = 0; i < RT; i++) {
         const float total = half_warp_sum(l[i]);
+        if (gridDim.z > 1) {   // the unscaled sums, and behind all of them (maximum, sum)
+            const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * p.Nq + i0 + RT * ty + i;
+            inv[i] = 1.f;
+            if (tx == 0 && i0 + RT * ty + i < p.Nq)
+                *reinterpret_cast<float2 *>(parts + (int64_t)gridDim.z * gridDim.y * p.Nq * D + 2 * row) =
+                    make_float2(m[i], total);
+            continue;
+        }
         inv[i] = total > 0.f ? 1.f / total : 0.f;
         if (total != total) inv[i] = total;   // NaN inputs stay visible
         const int r = i0 + RT * ty + i;
@@ -262,7 +280,41 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
             lse[((int64_t)b * p.H + h) * p.Nq + r] =
                 total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
     }
-    store_rows<D, RT>(out + b * p.o.batch + h * p.o.head, p.o.token, i0, p.Nq, ty, tx, o, inv);
+    if (gridDim.z > 1)
+        store_rows<D, RT>(part_rows<D>(parts, p.Nq), D, i0, p.Nq, ty, tx, o, inv);
+    else
+        store_rows<D, RT>(out + b * p.o.batch + h * p.o.head, p.o.token, i0, p.Nq, ty, tx, o, inv);
+}
+
+// Rows from the parts of their keys, in order; a thread has 4 columns.
+template <int D>
+__global__ void __launch_bounds__(256)
+simt_fwd_join_kernel(WinProblem p, int splits, const float *parts, float *out, float *lse) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)p.B * p.H * p.Nq;
+    const int64_t row = at / (D / 4);
+    const int c = (int)(at % (D / 4)) * 4;
+    if (row >= rows) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(parts + splits * rows * D);
+    float mx = -INFINITY, sum = 0.f;
+    for (int s = 0; s < splits; s++) mx = fmaxf(mx, ml[s * rows + row].x);
+    const float safe = mx == -INFINITY ? 0.f : mx;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; s++) {
+        const float2 y = ml[s * rows + row];
+        const float4 x = *reinterpret_cast<const float4 *>(parts + (s * rows + row) * D + c);
+        const float f = exp2f(y.x - safe);
+        sum = fmaf(f, y.y, sum);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // (a NaN stays visible)
+    const int i = (int)(row % p.Nq), h = (int)(row / p.Nq % p.H), b = (int)(row / p.Nq / p.H);
+    *reinterpret_cast<float4 *>(out + b * p.o.batch + h * p.o.head + i * p.o.token + c) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lse && c == 0) lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // ---------------------------------------------------------------- backward
@@ -276,7 +328,7 @@ constexpr int dq_smem() {
 template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
-               const float *lse, const float *delta, const float *dout, float *dq) {
+               const float *lse, const float *delta, const float *dout, float *dq, float *parts) {
     extern __shared__ __align__(16) float smf[];
     constexpr int kTileFloats = 32 * kPitch<D>;
     float *sq = smf, *sdo = sq + 16 * RT * kPitch<D>, *sds = sdo + 16 * RT * kPitch<D>;
@@ -290,11 +342,11 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
     load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
     load_rows<D, 16 * RT>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
-    const int n = kt.count();
+    const int first = part_begin(kt.count()), n = part_end(kt.count()) - first;
     auto load = [&](int it) {
         float *dst = skv + it % kStages<D> * 2 * kTileFloats;
-        load_rows<D, 32>(dst, kb, p.k.token, kt.tile(it) * 32, seq.len);
-        load_rows<D, 32>(dst + kTileFloats, vb, p.v.token, kt.tile(it) * 32, seq.len);
+        load_rows<D, 32>(dst, kb, p.k.token, kt.tile(first + it) * 32, seq.len);
+        load_rows<D, 32>(dst + kTileFloats, vb, p.v.token, kt.tile(first + it) * 32, seq.len);
     };
     if (kStages<D> == 2 && n > 0) load(0);
     copies_commit();
@@ -312,7 +364,7 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
         for (int x = 0; x < D / 32; x++) o[i][x] = 0;
     }
     for (int it = 0; it < n; it++) {
-        const int j0 = kt.tile(it) * 32;
+        const int j0 = kt.tile(first + it) * 32;
         const float *sk = skv + it % kStages<D> * 2 * kTileFloats, *sv = sk + kTileFloats;
         __syncthreads();
         if (it + kStages<D> - 1 < n) load(it + kStages<D> - 1);
@@ -335,8 +387,11 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
     }
     float sc[RT];
 #pragma unroll
-    for (int i = 0; i < RT; i++) sc[i] = p.scale;
-    store_rows<D, RT>(dq + b * g.dq.batch + h * g.dq.head, g.dq.token, i0, p.Nq, ty, tx, o, sc);
+    for (int i = 0; i < RT; i++) sc[i] = gridDim.z > 1 ? 1.f : p.scale;
+    if (gridDim.z > 1)
+        store_rows<D, RT>(part_rows<D>(parts, p.Nq), D, i0, p.Nq, ty, tx, o, sc);
+    else
+        store_rows<D, RT>(dq + b * g.dq.batch + h * g.dq.head, g.dq.token, i0, p.Nq, ty, tx, o, sc);
 }
 
 // dk, dv: 16 RT keys of one key head against tiles of 32 queries of every head of its
@@ -349,7 +404,8 @@ constexpr int dkv_smem() {
 template <int D, int RT>
 __global__ void __launch_bounds__(256, 2)
 simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const float *v,
-                const float *lse, const float *delta, const float *dout, float *dk, float *dv) {
+                const float *lse, const float *delta, const float *dout, float *dk, float *dv,
+                float *parts) {
     extern __shared__ __align__(16) float smf[];
     constexpr int kTileFloats = 32 * kPitch<D>;
     float *sk = smf, *sv = sk + 16 * RT * kPitch<D>, *sw = sv + 16 * RT * kPitch<D>;
@@ -370,7 +426,8 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
     int rfirst, rlast;
     real_rows(p, seq, 0, p.Nq, rfirst, rlast);
     // tiles of 32 queries of every head of the group
-    const int t0 = first / 32, nt = last > first ? (last + 31) / 32 - t0 : 0, n = nt * p.G;
+    const int t0 = first / 32, nt = last > first ? (last + 31) / 32 - t0 : 0;
+    const int u0 = part_begin(nt * p.G), u1 = part_end(nt * p.G);
     auto load = [&](int u) {
         float *dst = sqd + u % kStages<D> * 2 * kTileFloats;
         const int h = hk * p.G + u / nt, i0 = (t0 + u % nt) * 32;
@@ -379,14 +436,14 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
         load_rows<D, 32>(dst + kTileFloats, dout + b * g.dout.batch + h * g.dout.head, g.dout.token,
                          i0, rlast, rfirst);
     };
-    if (kStages<D> == 2 && n > 0) load(0);
+    if (kStages<D> == 2 && u0 < u1) load(u0);
     copies_commit();
-    for (int u = 0; u < n; u++) {
+    for (int u = u0; u < u1; u++) {
         const int64_t row = ((int64_t)b * p.H + hk * p.G + u / nt) * p.Nq;
         const int i0 = (t0 + u % nt) * 32;
         const float *sq = sqd + u % kStages<D> * 2 * kTileFloats, *sdo = sq + kTileFloats;
         __syncthreads();
-        if (u + kStages<D> - 1 < n) load(u + kStages<D> - 1);
+        if (u + kStages<D> - 1 < u1) load(u + kStages<D> - 1);
         copies_commit();
         copies_wait<kStages<D> - 1>();
         __syncthreads();
@@ -423,9 +480,36 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
     }
     float sc[RT], one[RT];
 #pragma unroll
-    for (int i = 0; i < RT; i++) sc[i] = p.scale, one[i] = 1.f;
+    for (int i = 0; i < RT; i++) sc[i] = gridDim.z > 1 ? 1.f : p.scale, one[i] = 1.f;
+    if (gridDim.z > 1) {   // all parts of dk, then those of dv
+        float *rows = part_rows<D>(parts, p.Nk);
+        store_rows<D, RT>(rows, D, j0, p.Nk, ty, tx, ok, sc);
+        store_rows<D, RT>(rows + (int64_t)gridDim.z * gridDim.y * p.Nk * D, D, j0, p.Nk, ty, tx, ov, one);
+        return;
+    }
     store_rows<D, RT>(dk + b * g.dk.batch + hk * g.dk.head, g.dk.token, j0, p.Nk, ty, tx, ok, sc);
     store_rows<D, RT>(dv + b * g.dv.batch + hk * g.dv.head, g.dv.token, j0, p.Nk, ty, tx, ov, one);
+}
+
+// A gradient's rows [B][heads][tokens] from their parts, added in order; a thread has 4
+// columns.
+template <int D>
+__global__ void __launch_bounds__(256)
+simt_sum_kernel(const float *parts, int splits, int B, int heads, int tokens, float scale,
+                Strides to, float *grad) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)B * heads * tokens;
+    const int64_t row = at / (D / 4);
+    const int c = (int)(at % (D / 4)) * 4;
+    if (row >= rows) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; s++) {
+        const float4 x = *reinterpret_cast<const float4 *>(parts + (s * rows + row) * D + c);
+        acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    }
+    const int i = (int)(row % tokens), h = (int)(row / tokens % heads), b = (int)(row / tokens / heads);
+    *reinterpret_cast<float4 *>(grad + b * to.batch + h * to.head + i * to.token + c) =
+        make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
 }
 
 // ---------------------------------------------------------------- delta
@@ -488,82 +572,137 @@ cudaError_t allow_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows a thread: 4 (tiles of 64 rows), or 2 where those tiles would leave SMs without a
-// CTA.  A tile's time is its shared-memory reads, most of them of the streamed side and
-// the same for any number of rows, next to the FMAs, which halve; with 1 row a thread two
-// CTAs share an SM's shared memory and take longer (4 heads of 780 tokens, 255 keys a row,
-// d = 64: forward 43 us at 4 rows, 33 at 1).
-int rows_a_thread(int64_t heads, int rows) { return heads * ((rows + 63) / 64) >= 148 ? 4 : 2; }
+// How a kernel divides its work.  Rows a thread: 4 (tiles of 64 rows), or 2 where those
+// tiles, and parts of them, would leave SMs without a CTA.  A tile's time is its
+// shared-memory reads, most of them of the streamed side and the same for any number of
+// rows, next to the FMAs, which halve; with 1 row a thread two CTAs share an SM's shared
+// memory and take longer (4 heads of 780 tokens, 255 keys a row, d = 64: forward 43 us at 4
+// rows, 33 at 1).  Parts of a tile's walk over the other side: as many as make the CTAs that
+// run at once (two an SM), of four streamed tiles at least (12 heads of 100 queries over 9000
+// keys, d = 64: forward 520 -> 157 us; backward of 4 heads of 300 over 2000 358 -> 131).
+struct Division {
+    int rows, parts;
+};
+Division divide(int64_t heads, int rows, int64_t streamed) {
+    const int64_t tiles = heads * ((rows + 63) / 64), most = std::max<int64_t>(1, streamed / 4);
+    Division d;
+    d.rows = tiles >= 148 || tiles * most >= 296 ? 4 : 2;
+    d.parts = (int)std::max<int64_t>(
+        1, std::min(296 / (heads * ((rows + 16 * d.rows - 1) / (16 * d.rows))), most));
+    return d;
+}
+Division forward_division(const WinProblem &p) {
+    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 64);
+}
+Division dq_division(const WinProblem &p) {
+    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 32);
+}
+Division dkv_division(const WinProblem &p) {
+    return divide((int64_t)p.B * p.Hkv, p.Nk, most_queries(p, 64) / 32 * p.G);
+}
+
+template <int D>
+unsigned join_grid(int64_t rows) { return (unsigned)((rows * (D / 4) + 255) / 256); }
 
 template <int D, int RT>
 cudaError_t forward_rt(const WinProblem &p, const float *q, const float *k, const float *v,
-                       float *out, float *lse, cudaStream_t stream) {
+                       float *out, float *lse, float *parts, cudaStream_t stream) {
     constexpr int smem = fwd_smem<D, RT>();
     cudaError_t e = allow_smem(simt_fwd_kernel<D, RT>, smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H);
-    simt_fwd_kernel<D, RT><<<grid, 256, smem, stream>>>(p, q, k, v, out, lse);
+    const int splits = forward_division(p).parts;
+    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H, splits);
+    simt_fwd_kernel<D, RT><<<grid, 256, smem, stream>>>(p, q, k, v, out, lse, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || splits == 1) return e;
+    simt_fwd_join_kernel<D><<<join_grid<D>((int64_t)p.B * p.H * p.Nq), 256, 0, stream>>>(
+        p, splits, parts, out, lse);
     return cudaGetLastError();
 }
 template <int D, int RT>
 cudaError_t dq_rt(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                   const float *v, const float *lse, const float *delta, const float *dout,
-                  float *dq, cudaStream_t stream) {
+                  float *dq, float *parts, cudaStream_t stream) {
     constexpr int smem = dq_smem<D, RT>();
     cudaError_t e = allow_smem(simt_dq_kernel<D, RT>, smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H);
-    simt_dq_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dq);
+    const int splits = dq_division(p).parts;
+    const dim3 grid((p.Nq + 16 * RT - 1) / (16 * RT), p.B * p.H, splits);
+    simt_dq_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dq, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || splits == 1) return e;
+    simt_sum_kernel<D><<<join_grid<D>((int64_t)p.B * p.H * p.Nq), 256, 0, stream>>>(
+        parts, splits, p.B, p.H, p.Nq, p.scale, g.dq, dq);
     return cudaGetLastError();
 }
 template <int D, int RT>
 cudaError_t dkv_rt(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                    const float *v, const float *lse, const float *delta, const float *dout,
-                   float *dk, float *dv, cudaStream_t stream) {
+                   float *dk, float *dv, float *parts, cudaStream_t stream) {
     constexpr int smem = dkv_smem<D, RT>();
     cudaError_t e = allow_smem(simt_dkv_kernel<D, RT>, smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((p.Nk + 16 * RT - 1) / (16 * RT), p.B * p.Hkv);
-    simt_dkv_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv);
+    const int splits = dkv_division(p).parts;
+    const dim3 grid((p.Nk + 16 * RT - 1) / (16 * RT), p.B * p.Hkv, splits);
+    simt_dkv_kernel<D, RT><<<grid, 256, smem, stream>>>(p, g, q, k, v, lse, delta, dout, dk, dv, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || splits == 1) return e;
+    const int64_t rows = (int64_t)p.B * p.Hkv * p.Nk;
+    simt_sum_kernel<D><<<join_grid<D>(rows), 256, 0, stream>>>(parts, splits, p.B, p.Hkv, p.Nk,
+                                                               p.scale, g.dk, dk);
+    simt_sum_kernel<D><<<join_grid<D>(rows), 256, 0, stream>>>(parts + splits * rows * D, splits, p.B,
+                                                               p.Hkv, p.Nk, 1.f, g.dv, dv);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const float *v,
-                      float *out, float *lse, cudaStream_t stream) {
-    const int rt = rows_a_thread((int64_t)p.B * p.H, p.Nq);
-    if (rt == 4) return forward_rt<D, 4>(p, q, k, v, out, lse, stream);
-    return forward_rt<D, 2>(p, q, k, v, out, lse, stream);
+                      float *out, float *lse, float *parts, cudaStream_t stream) {
+    if (forward_division(p).rows == 4) return forward_rt<D, 4>(p, q, k, v, out, lse, parts, stream);
+    return forward_rt<D, 2>(p, q, k, v, out, lse, parts, stream);
 }
 
 template <int D>
 cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                        const float *v, const float *lse, const float *delta, const float *dout,
-                       float *dq, float *dk, float *dv, cudaStream_t stream) {
-    const int rq = rows_a_thread((int64_t)p.B * p.H, p.Nq);
-    const cudaError_t e = rq == 4 ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, stream)
-                                  : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, stream);
+                       float *dq, float *dk, float *dv, float *parts, cudaStream_t stream) {
+    const cudaError_t e = dq_division(p).rows == 4
+                              ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, parts, stream)
+                              : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, parts, stream);
     if (e != cudaSuccess) return e;
-    const int rk = rows_a_thread((int64_t)p.B * p.Hkv, p.Nk);
-    if (rk == 4) return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
-    return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, stream);
+    if (dkv_division(p).rows == 4) return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
+    return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
 }
 
 }  // namespace
 
+size_t simt_forward_bytes(const WinProblem &p) {
+    const int splits = forward_division(p).parts;
+    return splits == 1 ? 0 : (size_t)splits * p.B * p.H * p.Nq * (p.d + 2) * sizeof(float);
+}
+size_t simt_backward_bytes(const WinProblem &p) {
+    // dq's parts are joined before those of dk and dv are written
+    const int sq = dq_division(p).parts, sk = dkv_division(p).parts;
+    const size_t q = sq == 1 ? 0 : (size_t)sq * p.B * p.H * p.Nq;
+    const size_t k = sk == 1 ? 0 : (size_t)sk * p.B * p.Hkv * p.Nk * 2;
+    return std::max(q, k) * p.d * sizeof(float);
+}
+
 cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, const float *v,
-                         float *out, float *lse, cudaStream_t stream) {
-    if (p.d == 32) return forward_d<32>(p, q, k, v, out, lse, stream);
-    if (p.d == 64) return forward_d<64>(p, q, k, v, out, lse, stream);
-    return forward_d<128>(p, q, k, v, out, lse, stream);
+                         float *out, float *lse, void *workspace, cudaStream_t stream) {
+    float *parts = (float *)workspace;
+    if (p.d == 32) return forward_d<32>(p, q, k, v, out, lse, parts, stream);
+    if (p.d == 64) return forward_d<64>(p, q, k, v, out, lse, parts, stream);
+    return forward_d<128>(p, q, k, v, out, lse, parts, stream);
 }
 
 cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
                           const float *v, const float *lse, const float *delta, const float *dout,
-                          float *dq, float *dk, float *dv, cudaStream_t stream) {
-    if (p.d == 32) return backward_d<32>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
-    if (p.d == 64) return backward_d<64>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
-    return backward_d<128>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, stream);
+                          float *dq, float *dk, float *dv, void *workspace, cudaStream_t stream) {
+    float *parts = (float *)workspace;
+    if (p.d == 32) return backward_d<32>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
+    if (p.d == 64) return backward_d<64>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
+    return backward_d<128>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
 }
 
 cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,

@@ -732,12 +732,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
 bool use_line(const WinProblem &p, int nprob, int sms) {
     const int64_t entries = (int64_t)((p.Nq + 255) / 256) * p.B;
     if (entries > kMaxEntries || sms > kMaxCtas) return false;
-    int64_t most = p.Nk;
-    if (p.left >= 0 && p.right >= 0) {
-        const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + 256 + p.frame;
-        most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
-    }
-    const int64_t chunks = most / 128 + 1;
+    const int64_t chunks = most_keys(p, 256) / 128 + 1;
     // at most one more: a run of n keys meets at most n / 64 + 2 blocks, the sinks' and the
     // window's n / 64 + 3 together
     const int64_t bound = entries * p.H * (chunks + 1);

@@ -725,12 +725,7 @@ TokenPlan token_plan(const WinProblem &p, monarch_dtype dtype) {
     TokenPlan t;
     t.row_tiles = (p.Nq * p.G + 15) / 16;
     const int64_t units = (int64_t)p.B * p.Hkv * t.row_tiles;
-    // the most keys that one tile of rows can see
-    int64_t most = p.Nk;
-    if (p.left >= 0 && p.right >= 0) {
-        const int64_t span = ((int64_t)p.left + p.right + 1) * p.frame + p.Nq + p.frame;
-        most = min(most, span + min(p.sink_end, (int64_t)p.Nk));
-    }
+    const int64_t most = most_keys(p, p.Nq);
     // (a tile of 64 bfloat16 or 32 float32 keys)
     const int64_t parts = parts_of(units, most / (dtype == MONARCH_BF16 ? 64.0 : 32.0), p.d);
     t.clusters = (int)((parts + kMaxCluster - 1) / kMaxCluster);

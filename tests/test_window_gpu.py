@@ -258,6 +258,15 @@ def test_few_key_tiles_with_many_query_blocks(dtype, H, Hkv):
     check(q, k, v, dout, window=(100, 30), sinks=3, starts=0, lengths=ints(777))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,Nq,Nk", [(64, 100, 3000), (128, 70, 1500), (32, 9, 2500)])
+def test_few_queries_over_many_keys_with_gradients(dtype, d, Nq, Nk):
+    """Each tile's walk over the other side is divided over CTAs (float32: both passes)."""
+    q, k, v, dout = make(25, dtype, 3, 6, 3, d, Nq, Nk)
+    for window, sinks in (((-1, 0), 0), ((-1, -1), 0), ((900, 0), 130)):
+        check(q, k, v, dout, window=window, sinks=sinks, lengths=ints(Nk, Nk // 3, 0))
+
+
 @pytest.mark.parametrize("N", [64, 128, 192, 256, 320, 384, 448, 512])
 def test_rows_of_few_keys_get_exact_deltas(N):
     """Around the number of key blocks up to which delta comes from the products."""
