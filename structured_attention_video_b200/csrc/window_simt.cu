@@ -151,9 +151,12 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 }
 
 // The streamed tiles of part blockIdx.z of gridDim.z: [part_begin, part_end) of n.
-__device__ __forceinline__ int part_begin(int n) { return (int)((int64_t)n * blockIdx.z / gridDim.z); }
+// (One part, which short calls have, spares the divisions: 8.3 -> 7.7 us.)
+__device__ __forceinline__ int part_begin(int n) {
+    return gridDim.z == 1 ? 0 : (int)((int64_t)n * blockIdx.z / gridDim.z);
+}
 __device__ __forceinline__ int part_end(int n) {
-    return (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+    return gridDim.z == 1 ? n : (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
 }
 // This part's rows of this head: [part][head][row][D].
 template <int D> __device__ __forceinline__ float *part_rows(float *parts, int rows) {
