@@ -474,9 +474,9 @@ typedef struct {
 
 /*
  * Workspace bytes of monarch_window_attn_fwd_ws on the current device, or 0 if the
- * arguments fail validation; 256 where none is needed (workspace may then be NULL).  Paths
- * 1 and 2 need one where the keys of a row are split over more CTAs than join by
- * themselves.  Host function.
+ * arguments fail validation; 256 where none is needed (workspace may then be NULL).  One is
+ * needed where the keys of a row are split over more CTAs than join by themselves.  Host
+ * function.
  * Source: no counterpart in the pages (a property of this implementation).
  */
 MONARCH_API size_t monarch_window_attn_workspace_bytes(const monarch_window_desc *desc);
