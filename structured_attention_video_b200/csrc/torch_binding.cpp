@@ -166,9 +166,11 @@ struct Workspace {
     }
 };
 
-// call(stream) on the device's current stream, with the device current.
+// The tensors' device, current for the rest of a call (workspace sizes depend on it too).
+c10::Device on(int dev) { return c10::Device(c10::kCUDA, (c10::DeviceIndex)dev); }
+
+// call(stream) on the device's current stream.
 template <typename Call> void launch(int dev, const char *where, const Call &call) {
-    const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
     const monarch_status status =
         call((monarch_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
     if (status == MONARCH_OK) return;
@@ -281,6 +283,7 @@ PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
                         out.data_ptr() == c.v.data_ptr()))
         refuse("out must not be an input");
     const Tensor lse = with_lse ? c.new_lse() : Tensor();
+    const c10::cuda::CUDAGuard guard(on(c.dev));
     const Workspace ws(monarch_window_attn_workspace_bytes(&c.desc), workspace, c.q);
     launch(c.dev, "monarch_window_attn_fwd_ws", [&](monarch_stream_t s) {
         return monarch_window_attn_fwd_ws(&c.desc, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(),
@@ -322,6 +325,7 @@ PyObject *window_attention_backward(PyObject *, PyObject *const *args, Py_ssize_
     const Tensor dq = at::empty_like(c.q), dk = at::empty_like(c.k), dv = at::empty_like(c.v);
     const monarch_window_grads grads = {strides4(dout, c.bnhd), strides4(dq, c.bnhd),
                                         strides4(dk, c.bnhd), strides4(dv, c.bnhd)};
+    const c10::cuda::CUDAGuard guard(on(c.dev));
     // (always used: never "none")
     const Workspace ws(std::max<size_t>(257, monarch_window_attn_bwd_workspace_bytes(&c.desc)),
                        workspace, c.q);
@@ -385,6 +389,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     desc.out = strides3(out);
     const Tensor lse =
         with_lse ? at::empty({desc.B, desc.H, 1}, q.options().dtype(at::kFloat)) : Tensor();
+    const c10::cuda::CUDAGuard guard(on(dev));
     const Workspace ws(monarch_paged_attn_workspace_bytes(&desc), workspace, q);
     launch(dev, "monarch_paged_attn_ws", [&](monarch_stream_t s) {
         return monarch_paged_attn_ws(&desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -502,6 +507,7 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t n) {
         desc.k = strides4(k, bnhd);
         desc.k_out = strides4(ko, bnhd);
     }
+    const c10::cuda::CUDAGuard guard(on(dev));
     launch(dev, "monarch_rotary", [&](monarch_stream_t s) {
         return monarch_rotary(&desc, q.data_ptr(), k.defined() ? k.data_ptr() : nullptr,
                               (const double *)freqs.data_ptr(), qo.data_ptr(),
