@@ -128,7 +128,9 @@ struct Segment {
 // The CTA's segments into `list`; returns their number.  Whole problems are dealt out
 // forwards and backwards in turn, so that each CTA gets as many and long ones meet short
 // ones: all of them (kEvery; nh = 0: no row sees a key), or those that have keys (kReal).
-// The line (kLine): chunks [total * blockIdx / gridDim, total * (blockIdx + 1) / gridDim).
+// The line (kLine): as many whole problems each as never exceed a CTA's share, CTA c the
+// c-th of every gridDim (they start together, so the heads' keys are read from DRAM about
+// once for all of them), then of the chunks behind those its share less what it has.
 __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list) {
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -160,9 +162,10 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
         a.meta[2 * blockIdx.x + threadIdx.x] = make_int2(-1, 0);
     __syncthreads();
     if (warp == 0) {
-        int sum = 0;
+        int sum = 0, longest = 0;
         for (int e0 = 1; e0 <= entries; e0 += 32) {
             int x = e0 + lane <= entries ? line[e0 + lane] : 0;
+            longest = max(longest, __reduce_max_sync(0xffffffffu, x) / p.H);
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, m);
@@ -172,13 +175,27 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
             sum += __shfl_sync(0xffffffffu, x, 31);
         }
         if (lane == 0 && a.how == kLine) {
-            int at = (int)((int64_t)sum * blockIdx.x / gridDim.x), n = 0, e = 0;
-            const int end = (int)((int64_t)sum * (blockIdx.x + 1) / gridDim.x);
+            const int c = blockIdx.x, ctas = gridDim.x, whole = longest ? sum / ctas / longest : 0;
+            // where problem i (entry i / H, head i % H) begins in the line
+            auto begin = [&](int i) {
+                const int e = i / p.H;
+                return e == entries ? sum : line[e] + (line[e + 1] - line[e]) / p.H * (i - e * p.H);
+            };
+            const int rest = begin(whole * ctas);
+            int at = rest + (int)((int64_t)sum * c / ctas), n = 0, e = 0;
+            int end = rest + (int)((int64_t)sum * (c + 1) / ctas);
+            for (int j = 0; j < whole; j++) {
+                const int i = j * ctas + c;
+                at -= begin(i) - begin(j * ctas);
+                end -= begin(i + 1) - begin(j * ctas);
+                const KeyTiles kt = entry_of(a, i / p.H).kt;
+                if (kt.count() > 0) list[n++] = Record{i, 0, kt.count(), kt.nA, kt.first, 1};
+            }
             while (at < end && n < kMaxSegments) {
                 while (line[e + 1] <= at) e++;
                 const KeyTiles kt = entry_of(a, e).kt;
-                const int blocks = kt.count(), chunks = (blocks + 1) / 2, rest = at - line[e];
-                const int h = rest / chunks, c0 = rest - h * chunks, c1 = min(chunks, c0 + end - at);
+                const int blocks = kt.count(), chunks = (blocks + 1) / 2;
+                const int h = (at - line[e]) / chunks, c0 = at - line[e] - h * chunks, c1 = min(chunks, c0 + end - at);
                 list[n++] = Record{e * p.H + h, 2 * c0, min(blocks, 2 * c1) - 2 * c0, kt.nA, kt.first,
                                    c1 == chunks};
                 at += c1 - c0;
