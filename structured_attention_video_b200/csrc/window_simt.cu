@@ -581,27 +581,30 @@ cudaError_t allow_smem(K kernel, int bytes) {
 // rows, next to the FMAs, which halve; with 1 row a thread two CTAs share an SM's shared
 // memory and take longer (4 heads of 780 tokens, 255 keys a row, d = 64: forward 43 us at 4
 // rows, 33 at 1).  Parts of a tile's walk over the other side: as many as make the CTAs that
-// run at once (two an SM), of four streamed tiles at least (12 heads of 100 queries over 9000
-// keys, d = 64: forward 520 -> 157 us; backward of 4 heads of 300 over 2000 358 -> 131).
+// run at once (two an SM), of four streamed tiles at least, or of `shared` where they would
+// share SMs and gain less than the join takes.  d = 64: 12 heads of 100 queries over 9000
+// keys forward 520 -> 113 us, backward 1049 -> 407; 4 heads of 1000 tokens backward 234 ->
+// 139; those of 780, forward and backward, 100 us whole and 110 with parts of five tiles.
 struct Division {
     int rows, parts;
 };
-Division divide(int64_t heads, int rows, int64_t streamed) {
+Division divide(int64_t heads, int rows, int64_t streamed, int shared) {
     const int64_t tiles = heads * ((rows + 63) / 64), most = std::max<int64_t>(1, streamed / 4);
     Division d;
     d.rows = tiles >= 148 || tiles * most >= 296 ? 4 : 2;
-    d.parts = (int)std::max<int64_t>(
-        1, std::min(296 / (heads * ((rows + 16 * d.rows - 1) / (16 * d.rows))), most));
+    const int64_t ctas = heads * ((rows + 16 * d.rows - 1) / (16 * d.rows));
+    d.parts = (int)std::max<int64_t>(1, std::min(296 / ctas, most));
+    while (d.parts > 1 && ctas * d.parts > 148 && streamed / d.parts < shared) d.parts--;
     return d;
 }
 Division forward_division(const WinProblem &p) {
-    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 64);
+    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 64, 4);
 }
 Division dq_division(const WinProblem &p) {
-    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 32);
+    return divide((int64_t)p.B * p.H, p.Nq, most_keys(p, 64) / 32, 7);
 }
 Division dkv_division(const WinProblem &p) {
-    return divide((int64_t)p.B * p.Hkv, p.Nk, most_queries(p, 64) / 32 * p.G);
+    return divide((int64_t)p.B * p.Hkv, p.Nk, most_queries(p, 64) / 32 * p.G, 7);
 }
 
 template <int D>

@@ -17,8 +17,9 @@
 //
 // Bound by the exponentials (16 a clock and SM, 2 tiles x 128 x 64 a half) together with
 // the issue slots of the softmax warps, then by the products.  A 480p chunk of 4680
-// queries that see 18720 keys, 12 heads, d = 128: 541 us (996 TFLOP/s; 641 us where the
-// power limit lowers the clocks of a long run), against 331 for the products alone.  Rejected: one
+// queries that see 18720 keys, 12 heads, d = 128: 497 us (1083 TFLOP/s; 579 us where the
+// power limit lowers the clocks of a long run), against 331 for the products alone.
+// Rejected: one
 // maximum a block guessed from the last one's (fewer instructions on the common path, but
 // 27% more time for the test and the repeat behind it).
 #include "window_tc.cuh"
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
 // rounds of the longest problem as there are problems a CTA; the line takes the mean, and
 // about ten chunks' time (20 us) for the parts and the join.  4680 queries
 // that see 18720 keys, 12 heads (228 pairs of 147 chunks on 148 SMs): 620 us whole, 541 by
-// the line.  Chunks are estimated from
+// the line alone, whose CTAs read 1.42 GB from DRAM, 497 with whole problems first (0.53 GB).  Chunks are estimated from
 // the tensors' sizes and the window, as the lengths are on the device.
 bool use_line(const WinProblem &p, int nprob, int sms) {
     const int64_t entries = (int64_t)((p.Nq + 255) / 256) * p.B;
