@@ -676,7 +676,8 @@ cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, c
                               ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, parts, stream)
                               : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, parts, stream);
     if (e != cudaSuccess) return e;
-    if (dkv_division(p).rows == 4) return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
+    if (dkv_division(p).rows == 4)
+        return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
     return dkv_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
 }
 

@@ -196,7 +196,8 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
                 while (line[e + 1] <= at) e++;
                 const KeyTiles kt = entry_of(a, e).kt;
                 const int blocks = kt.count(), chunks = (blocks + 1) / 2;
-                const int h = (at - line[e]) / chunks, c0 = at - line[e] - h * chunks, c1 = min(chunks, c0 + end - at);
+                const int h = (at - line[e]) / chunks, c0 = at - line[e] - h * chunks;
+                const int c1 = min(chunks, c0 + end - at);
                 list[n++] = Record{e * p.H + h, 2 * c0, min(blocks, 2 * c1) - 2 * c0, kt.nA, kt.first,
                                    c1 == chunks};
                 at += c1 - c0;
@@ -322,7 +323,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                         ok = false;
                         break;
                     }
-                    if (lane == 0) load_chunk<D>(sm + L::kK + sk * kTile, &tmK, &tmK128, sg, j, p.G, k_full + sk);
+                    if (lane == 0)
+                        load_chunk<D>(sm + L::kK + sk * kTile, &tmK, &tmK128, sg, j, p.G, k_full + sk);
                     issued[sk]++;
                 }
             }
@@ -360,7 +362,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                         ok = false;
                         break;
                     }
-                    if (lane == 0) load_chunk<D>(sm + L::kV + st * kTile, &tmV, &tmV128, sg, j, p.G, v_full + st);
+                    if (lane == 0)
+                        load_chunk<D>(sm + L::kV + st * kTile, &tmV, &tmV128, sg, j, p.G, v_full + st);
                     issued[st]++;
                 }
             }
@@ -745,8 +748,9 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
 // rounds of the longest problem as there are problems a CTA; the line takes the mean, and
 // about ten chunks' time (20 us) for the parts and the join.  4680 queries
 // that see 18720 keys, 12 heads (228 pairs of 147 chunks on 148 SMs): 620 us whole, 541 by
-// the line alone, whose CTAs read 1.42 GB from DRAM, 497 with whole problems first (0.53 GB).  Chunks are estimated from
-// the tensors' sizes and the window, as the lengths are on the device.
+// the line alone, whose CTAs read 1.42 GB from DRAM, 497 with whole problems first (0.53
+// GB).  Chunks are estimated from the tensors' sizes and the window, as the lengths are on
+// the device.
 bool use_line(const WinProblem &p, int nprob, int sms) {
     const int64_t entries = (int64_t)((p.Nq + 255) / 256) * p.B;
     if (entries > kMaxEntries || sms > kMaxCtas) return false;

@@ -503,13 +503,13 @@ __device__ __forceinline__ void copy16(float *dst, const float *src, bool there)
                  : "memory");
 }
 
-// Tiles of 32 keys, the next one's copies behind this one's arithmetic; 8 keys a warp.  In the logits four lanes share a key, a quarter of the
-// columns each, which stay in registers for all rows (at most R); in the output a lane has
-// columns lane, lane + 32, ..., and a value serves all rows.  Each warp has its own maxima
-// and sums; they join at the end.  Bound by memory up to four rows (8 key heads of 32768
-// keys, d = 128: 70.6 us, 3.8 TB/s), then by the FMA pipes.  One tile at a time, its rows
-// divided among the warps and a lane a key, took 128; 24 sequences of 6000 keys, 4 heads a
-// key head 186 us instead of 101.
+// Tiles of 32 keys, the next one's copies behind this one's arithmetic; 8 keys a warp.  In
+// the logits four lanes share a key, a quarter of the columns each, which stay in registers
+// for all rows (at most R); in the output a lane has columns lane, lane + 32, ..., and a
+// value serves all rows.  Each warp has its own maxima and sums; they join at the end.
+// Bound by memory up to four rows (8 key heads of 32768 keys, d = 128: 70.6 us, 3.8 TB/s),
+// then by the FMA pipes.  One tile at a time, its rows divided among the warps and a lane a
+// key, took 128; 24 sequences of 6000 keys, 4 heads a key head 186 us instead of 101.
 template <int D, int R>
 __global__ void __launch_bounds__(kTokThreads)
 token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, float *out,
