@@ -175,6 +175,7 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
             if (e0 + lane <= entries) line[e0 + lane] = sum + x;
             sum += __shfl_sync(0xffffffffu, x, 31);
         }
+        __syncwarp();   // lane 0 reads what the other lanes have written
         if (lane == 0 && a.how == kLine) {
             const int c = blockIdx.x, ctas = gridDim.x, whole = longest ? sum / ctas / longest : 0;
             // where problem i (entry i / H, head i % H) begins in the line

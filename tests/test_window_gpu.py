@@ -214,6 +214,22 @@ def test_few_queries_against_long_caches(dtype, d, mask):
     check(q[:1, :1], k[:1], v[:1], window=window, sinks=sinks, frame=frame)
 
 
+@pytest.mark.parametrize("B,H,Nq,Nk", [(6, 3, 1500, 5000), (33, 1, 250, 6000)])
+def test_line_of_many_entries(B, H, Nq, Nk):
+    """More than 32 pairs of query tiles on the line of all chunks, each with another number
+    of keys: the CTAs divide it by the sums that the lanes of one warp have left to each
+    other."""
+    lens = [Nk - (Nk * b) // B - b % 3 for b in range(B)]
+    q, k, v, _ = make(27, "bf16", B, H, 1, 64, Nq, Nk)
+    for b, n in enumerate(lens):
+        k[b, :, n:], v[b, :, n:] = NAN, NAN
+    for window in ((-1, -1), (-1, 0)):
+        out, lse = check(q, k, v, window=window, lengths=ints(*lens))
+        for _ in range(3):
+            again = window_attention(q, k, v, window=window, lengths=ints(*lens), return_lse=True)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,H,Hkv,d,lens", [(2, 2, 1, 64, (40000, 3)), (1, 5, 1, 128, (30011,)),
                                             (9, 8, 8, 128, (4097, 1, 0, 65, 640, 2049, 7, 4000, 64)),
