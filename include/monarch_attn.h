@@ -446,6 +446,11 @@ MONARCH_API int monarch_attn_path(int B, int H, int f, int h, int w, int d, int 
  * lengths[b] should be finite: a NaN or an infinity there can reach every query that
  * shares a tile with one that sees it.
  *
+ * lengths, starts and a page table are read on the device, so they stay allocated and as
+ * they are until the call, or each replay of a graph that holds it, has finished.  (A
+ * caller that changes them meanwhile gets rows of either state or of a mixture; within one
+ * CTA all threads use the values that were read first.)
+ *
  * Every call may be captured into a CUDA graph once a call of its kind has run in the
  * context (the first one loads its kernels); each captured call wants a workspace of its
  * own where two replays can overlap.  The kernels wait with the limit of

@@ -169,6 +169,7 @@ template <int N1, int N2, int READERS> struct Bars {
     uint64_t stall_bar;                 // never completed (fault injection)
     uint32_t tmem_slot;
     int abort_flag;
+    Sequence seq;                       // of the whole CTA
 
     __device__ __forceinline__ void init() {
         mbar_init(&fix_full, 1);
@@ -286,7 +287,9 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int tile_unit = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
     const int unit = tile_unit % (p.B * p.Hkv), hk = unit % p.Hkv, b = unit / p.Hkv;
     const int j0 = tile_unit / (p.B * p.Hkv) * 128;
-    const Sequence seq = sequence(p, b);
+    Sequence seq = first_threads_sequence(p, b);
+    if (threadIdx.x == 32) bar->init();
+    share_sequence(seq, &bar->seq);
     int first, last;
     query_rows(p, seq, j0, j0 + 128, first, last);
     const int t0 = first / 64, nt = last > first ? (last + 63) / 64 - t0 : 0;
@@ -307,7 +310,6 @@ tc_window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         return;
     }
-    if (threadIdx.x == 0) bar->init();
     if (warp == kIssueWarp) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -569,7 +571,9 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
     // the last tiles first: they see the most keys under a causal mask
     const int unit = blockIdx.x % (p.B * p.H), h = unit % p.H, b = unit / p.H;
     const int i0 = ((int)gridDim.x - 1 - (int)blockIdx.x) / (p.B * p.H) * 128;
-    const Sequence seq = sequence(p, b);
+    Sequence seq = first_threads_sequence(p, b);
+    if (threadIdx.x == 32) bar->init();
+    share_sequence(seq, &bar->seq);
     const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + 128);
     const int nt = kt.count();
     // the first n - nt blocks only sum delta
@@ -581,7 +585,6 @@ tc_window_dq_kernel(const __grid_constant__ CUtensorMap tmK,
         if (threadIdx.x < 128 && i < p.Nq) zero_row(dq + (int64_t)i * a.g.dq.token, p.d);
         return;
     }
-    if (threadIdx.x == 0) bar->init();
     if (warp == kIssueWarp) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();

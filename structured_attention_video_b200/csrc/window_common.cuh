@@ -55,6 +55,19 @@ __device__ __forceinline__ Sequence sequence(const WinProblem &p, int b) {
     return s;
 }
 
+// The sequence of a whole CTA, read once: trip counts and barriers follow from it, so all
+// threads must have the same one whatever happens to lengths and starts meanwhile.  The
+// first thread reads it; the block meets in share_sequence, and what needs no sequence
+// goes between the two.
+__device__ __forceinline__ Sequence first_threads_sequence(const WinProblem &p, int b) {
+    return threadIdx.x == 0 ? sequence(p, b) : Sequence{0, 0};
+}
+__device__ __forceinline__ void share_sequence(Sequence &s, Sequence *shared) {
+    if (threadIdx.x == 0) *shared = s;
+    __syncthreads();
+    s = *shared;
+}
+
 // Keys of one query row: [lo, hi) and [0, sink), sink <= lo.
 struct RowKeys {
     int lo, hi, sink;

@@ -181,11 +181,13 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
     const int i0 = blockIdx.x * 16 * RT;
-    const Sequence seq = sequence(p, b);
+    __shared__ Sequence shared_seq;
+    Sequence seq = first_threads_sequence(p, b);
+    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    share_sequence(seq, &shared_seq);
     const KeyTiles kt = key_tiles<64>(p, seq, i0, i0 + 16 * RT);
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
     const int first = part_begin(kt.count()), n = part_end(kt.count()) - first;
     auto load = [&](float *dst, const float *src, int64_t stride, int it) {
         load_rows<D, 64>(dst, src, stride, kt.tile(first + it) * 64, seq.len);
@@ -339,12 +341,14 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = blockIdx.y % p.H, b = blockIdx.y / p.H;
     const int i0 = blockIdx.x * (16 * RT);
-    const Sequence seq = sequence(p, b);
+    __shared__ Sequence shared_seq;
+    Sequence seq = first_threads_sequence(p, b);
+    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
+    load_rows<D, 16 * RT>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
+    share_sequence(seq, &shared_seq);
     const KeyTiles kt = key_tiles<32>(p, seq, i0, i0 + (16 * RT));
     const float *kb = k + b * p.k.batch + (h / p.G) * p.k.head;
     const float *vb = v + b * p.v.batch + (h / p.G) * p.v.head;
-    load_rows<D, 16 * RT>(sq, q + b * p.q.batch + h * p.q.head, p.q.token, i0, p.Nq);
-    load_rows<D, 16 * RT>(sdo, dout + b * g.dout.batch + h * g.dout.head, g.dout.token, i0, p.Nq);
     const int first = part_begin(kt.count()), n = part_end(kt.count()) - first;
     auto load = [&](int it) {
         float *dst = skv + it % kStages<D> * 2 * kTileFloats;
@@ -416,7 +420,9 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int hk = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv;
     const int j0 = blockIdx.x * (16 * RT);
-    const Sequence seq = sequence(p, b);
+    __shared__ Sequence shared_seq;
+    Sequence seq = first_threads_sequence(p, b);
+    share_sequence(seq, &shared_seq);
     int first, last;
     query_rows(p, seq, j0, j0 + (16 * RT), first, last);
     load_rows<D, 16 * RT>(sk, k + b * p.k.batch + hk * p.k.head, p.k.token, j0, seq.len);

@@ -45,8 +45,13 @@ struct Record {
     int unit;            // entry * H + head
     int first, nh;
     int sinks, window;   // blocks of the problem's sinks; first block of its window
-    int ends;            // the problem's last block is among them
+    int len;             // keys of the problem's sequence, with the sign bit set where the
+                         // problem's last block is among these
+    int start;           // position of the sequence's first query
+    __device__ __forceinline__ Sequence seq() const { return {len & 0x7fffffff, start}; }
+    __device__ __forceinline__ bool ends() const { return len < 0; }
 };
+constexpr int kEnds = (int)0x80000000;
 
 // Shared memory for a head of D columns (tiles of 128 rows).
 template <int D> struct Layout {
@@ -56,6 +61,7 @@ template <int D> struct Layout {
     static constexpr uint32_t kV = kK + 2 * kTile;
     static constexpr uint32_t kL = kV + 2 * kTile;          // row sums [parity][tile][128]
     static constexpr uint32_t kStg = kL + 2048;             // epilogue: 4 warps x 32 rows x 128 B
+    static_assert(kMaxEntries * sizeof(Sequence) <= 4 * 4096, "the sequences of the line");
     static constexpr uint32_t kLine = kStg + 4 * 4096;      // first chunk of each entry
     static constexpr uint32_t kList = kLine + (kMaxEntries + 1) * 4 + 12;
     static constexpr uint32_t kBar = kList + kMaxSegments * sizeof(Record);
@@ -87,19 +93,13 @@ __host__ __device__ constexpr int part_floats(int d) { return 512 + 256 * d; }
 
 // Entry e of the line: pair npairs - 1 - e / B of batch e % B.  Later rows see more keys
 // under a causal mask, so the longest problems come first and short ones fill the end.
-struct Entry {
-    int b, i0;
-    Sequence seq;
-    KeyTiles kt;    // 64-key blocks
-};
-__device__ __forceinline__ Entry entry_of(const FwdArgs &a, int e) {
-    const WinProblem &p = a.p;
-    Entry x;
-    x.b = e % p.B;
-    x.i0 = (a.npairs - 1 - e / p.B) * 128 * a.tiles;
-    x.seq = sequence(p, x.b);
-    x.kt = key_tiles<64>(p, x.seq, x.i0, x.i0 + 128 * a.tiles);
-    return x;
+__device__ __forceinline__ int entry_batch(const FwdArgs &a, int e) { return e % a.p.B; }
+__device__ __forceinline__ int entry_row(const FwdArgs &a, int e) {
+    return (a.npairs - 1 - e / a.p.B) * 128 * a.tiles;
+}
+// Its 64-key blocks.
+__device__ __forceinline__ KeyTiles entry_tiles(const FwdArgs &a, int e, const Sequence &seq) {
+    return key_tiles<64>(a.p, seq, entry_row(a, e), entry_row(a, e) + 128 * a.tiles);
 }
 
 // A segment, read from its record by each role.
@@ -110,14 +110,14 @@ struct Segment {
         const int e = r.unit / a.p.H;
         unit = r.unit;
         h = unit - e * a.p.H;
-        b = e % a.p.B;
-        i0 = (a.npairs - 1 - e / a.p.B) * 128 * a.tiles;
+        b = entry_batch(a, e);
+        i0 = entry_row(a, e);
         first = r.first;
         nh = r.nh;
         turn = r.sinks - first;   // blocks before it are the sinks', the others lie
         skip = r.window - r.sinks;   // `skip` further
         begins = first == 0;
-        ends = r.ends != 0;
+        ends = r.ends();
     }
     __device__ __forceinline__ bool whole() const { return begins && ends; }
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (begins ? 1 : 0); }
@@ -132,7 +132,9 @@ struct Segment {
 // The line (kLine): as many whole problems each as never exceed a CTA's share, CTA c the
 // c-th of every gridDim (they start together, so the heads' keys are read from DRAM about
 // once for all of them), then of the chunks behind those its share less what it has.
-__device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list) {
+// lengths and starts are read once: what follows from them, the roles take from the list.
+__device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record *list,
+                                             Sequence *seqs) {
     const WinProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ int count;
@@ -144,18 +146,24 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
         const int rounds = (total + (int)gridDim.x - 1) / (int)gridDim.x;
         return rounds == 0 || problem(rounds - 1) < total ? rounds : rounds - 1;
     };
+    auto whole_problem = [&](int unit, const Sequence &seq) {
+        const KeyTiles kt = entry_tiles(a, unit / p.H, seq);
+        return Record{unit, 0, kt.count(), kt.nA, kt.first, seq.len | kEnds, (int)seq.start};
+    };
     if (a.how == kEvery) {
         const int n = rounds_of(a.nprob);
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const int unit = problem(i);
-            const KeyTiles kt = entry_of(a, unit / p.H).kt;
-            list[i] = Record{unit, 0, kt.count(), kt.nA, kt.first, 1};
+            list[i] = whole_problem(unit, sequence(p, entry_batch(a, unit / p.H)));
         }
         return n;
     }
     const int entries = a.npairs * p.B;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) seqs[b] = sequence(p, b);
+    __syncthreads();
+    auto tiles_of = [&](int e) { return entry_tiles(a, e, seqs[entry_batch(a, e)]); };
     for (int e = threadIdx.x; e < entries; e += kThreads) {
-        const int chunks = (entry_of(a, e).kt.count() + 1) / 2;
+        const int chunks = (tiles_of(e).count() + 1) / 2;
         line[e + 1] = (a.how == kLine ? chunks : min(chunks, 1)) * p.H;
     }
     if (threadIdx.x == 0) line[0] = 0;
@@ -190,17 +198,18 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
                 const int i = j * ctas + c;
                 at -= begin(i) - begin(j * ctas);
                 end -= begin(i + 1) - begin(j * ctas);
-                const KeyTiles kt = entry_of(a, i / p.H).kt;
-                if (kt.count() > 0) list[n++] = Record{i, 0, kt.count(), kt.nA, kt.first, 1};
+                const Record r = whole_problem(i, seqs[entry_batch(a, i / p.H)]);
+                if (r.nh > 0) list[n++] = r;
             }
             while (at < end && n < kMaxSegments) {
                 while (line[e + 1] <= at) e++;
-                const KeyTiles kt = entry_of(a, e).kt;
+                const KeyTiles kt = tiles_of(e);
+                const Sequence &seq = seqs[entry_batch(a, e)];
                 const int blocks = kt.count(), chunks = (blocks + 1) / 2;
                 const int h = (at - line[e]) / chunks, c0 = at - line[e] - h * chunks;
                 const int c1 = min(chunks, c0 + end - at);
                 list[n++] = Record{e * p.H + h, 2 * c0, min(blocks, 2 * c1) - 2 * c0, kt.nA, kt.first,
-                                   c1 == chunks};
+                                   seq.len | (c1 == chunks ? kEnds : 0), (int)seq.start};
                 at += c1 - c0;
             }
             count = n;
@@ -216,8 +225,7 @@ __device__ __forceinline__ int list_segments(const FwdArgs &a, int *line, Record
             const int mid = (lo + hi) / 2;
             (line[mid] <= x ? lo : hi) = mid;
         }
-        const KeyTiles kt = entry_of(a, lo).kt;
-        list[i] = Record{lo * p.H + (x - line[lo]), 0, kt.count(), kt.nA, kt.first, 1};
+        list[i] = whole_problem(lo * p.H + (x - line[lo]), seqs[entry_batch(a, lo)]);
     }
     return n;
 }
@@ -300,7 +308,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     if (warp == 13) tmem_alloc(tmem_slot, 512);
     Record *list = reinterpret_cast<Record *>(sm + L::kList);
-    const int nseg = list_segments(a, line, list);
+    // (the sequences lie where the epilogue stages its rows later)
+    const int nseg = list_segments(a, line, list, reinterpret_cast<Sequence *>(sm + L::kStg));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -541,8 +550,8 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         int pc = 0, hc = 0, jc0 = 0;
         // rows of a pair that sees no key: zeros
         auto write_zeros = [&](int unit) {
-            const int e = unit / p.H, h = unit % p.H, bb = e % p.B;
-            const int m = (a.npairs - 1 - e / p.B) * 128 * a.tiles + t * 128 + wq * 32 + lane;
+            const int e = unit / p.H, h = unit % p.H, bb = entry_batch(a, e);
+            const int m = entry_row(a, e) + t * 128 + wq * 32 + lane;
             if (m >= p.Nq) return;
             uint4 *row = reinterpret_cast<uint4 *>(a.out + bb * p.o.batch + h * p.o.head +
                                                    (int64_t)m * p.o.token);
@@ -560,12 +569,12 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 continue;
             }
             const int m = sg.i0 + t * 128 + wq * 32 + lane;
-            const Sequence seq = sequence(p, sg.b);
-            // a row that is not real takes every key, so that its warp needs no masks (its
-            // sums touch nothing else), and its row sum goes out as 0
+            const Sequence seq = list[si].seq();
+            // a row that is not real takes every key of the sequence, so that its warp needs
+            // no masks (its sums touch nothing else), and its row sum goes out as 0
             RowKeys rk = row_keys(p, seq, m);
             const bool real = rk.hi > 0;
-            if (!real) rk = RowKeys{0, 0x7fffffff, 0};
+            if (!real) rk = RowKeys{0, seq.len, 0};
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = 0; i < sg.nh; i++, hc++) {
                 const int b = hc & 1;
@@ -593,6 +602,18 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     for (int k = 0; k < 32; k++) {
                         x[k] = (see0 >> k) & 1 ? x[k] : -INFINITY;
                         x[k + 32] = (see1 >> k) & 1 ? x[k + 32] : -INFINITY;
+                    }
+                    if (j0 + 64 > seq.len) {   // (no row takes such a block whole)
+                        // values past the sequence may hold anything, and 0 * NaN is NaN: they
+                        // become zeros before this half's PV (both tiles write the same zeros)
+                        const int jc = jc0 + (i >> 1), st = jc & 1;
+                        if (!wait_warp(v_full + st, (jc >> 1) & 1, w)) {
+                            ok = false;
+                            break;
+                        }
+                        zero_rows(sm + L::kV + st * kTile + (i & 1) * 64 * 128,
+                                  max(0, seq.len - j0), 64, PN, kPanel, wq * 32 + lane, 128);
+                        fence_proxy_async_smem();
                     }
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -625,18 +646,6 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                 float s0, s1;
                 f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), s0, s1);
                 l_run = l_run * alpha + (s0 + s1);
-                if (j0 + 64 > seq.len) {
-                    // values past the sequence may hold anything, and 0 * NaN is NaN: they
-                    // become zeros before this half's PV (both tiles write the same zeros)
-                    const int jc = jc0 + (i >> 1), st = jc & 1;
-                    if (!wait_warp(v_full + st, (jc >> 1) & 1, w)) {
-                        ok = false;
-                        break;
-                    }
-                    zero_rows(sm + L::kV + st * kTile + (i & 1) * 64 * 128,
-                              max(0, seq.len - j0), 64, PN, kPanel, wq * 32 + lane, 128);
-                    fence_proxy_async_smem();
-                }
                 if (i > 0 && __any_sync(0xffffffffu, rescale)) {
                     // O holds the products up to the previous half once that PV is done
                     if (!wait_warp(pv_done + t, (hc - 1) & 1, w)) {
@@ -711,11 +720,10 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
     }
     __syncthreads();
     const int n = parts;
-    const Entry x = entry_of(a, head.x / p.H);
-    const int h = head.x % p.H;
+    const int b = entry_batch(a, head.x / p.H), i0 = entry_row(a, head.x / p.H), h = head.x % p.H;
     for (int at = threadIdx.x; at < 16 * (D / 4); at += 256) {
         const int row = blockIdx.y * 16 + at / (D / 4), col = at % (D / 4) * 4;
-        const int m = x.i0 + row;
+        const int m = i0 + row;
         if (m >= p.Nq || col >= p.d) continue;
         float mx = -INFINITY;
         for (int i = 0; i < n; i++) {
@@ -736,11 +744,10 @@ __global__ void __launch_bounds__(256) window_join_kernel(FwdArgs a, int ctas) {
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<uint2 *>(a.out + x.b * p.o.batch + h * p.o.head + (int64_t)m * p.o.token +
-                                   col) =
+        *reinterpret_cast<uint2 *>(a.out + b * p.o.batch + h * p.o.head + (int64_t)m * p.o.token + col) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (a.lse && col == 0)
-            a.lse[((int64_t)x.b * p.H + h) * p.Nq + m] =
+            a.lse[((int64_t)b * p.H + h) * p.Nq + m] =
                 sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
 }

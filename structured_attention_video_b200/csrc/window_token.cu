@@ -92,14 +92,14 @@ struct TokenUnit {
 };
 
 template <int T>
-__device__ __forceinline__ TokenUnit token_unit(const TokenArgs &a) {
+__device__ __forceinline__ TokenUnit token_unit(const TokenArgs &a, const Sequence &seq) {
     const WinProblem &p = a.p;
     TokenUnit u;
     u.split = blockIdx.x;
     u.rt = blockIdx.y;
     u.b = blockIdx.z / p.Hkv;
     u.hk = blockIdx.z % p.Hkv;
-    u.seq = sequence(p, u.b);
+    u.seq = seq;
     const int i0 = u.rt * 16 / p.G, i1 = min(p.Nq, (u.rt * 16 + 15) / p.G + 1);
     u.kt = key_tiles<T>(p, u.seq, i0, i1);
     const int64_t n = u.kt.count();
@@ -274,11 +274,8 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
     volatile uint32_t *good = reinterpret_cast<volatile uint32_t *>(empty + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + NS) + NS;
     const WinProblem &p = a.p;
-    if (threadIdx.x == 0) {
-        prefetch_map(&tmK);
-        prefetch_map(&tmV);
-    }
-    const TokenUnit u = token_unit<64>(a);
+    __shared__ TokenUnit shared_unit;
+    TokenUnit u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
     const int rows = p.Nq * p.G;
     const WaitCtx w{a.limit, a.status, abort_flag};
@@ -291,16 +288,16 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
         for (int c = 0; c < 4; c++) o[x][c] = 0.f;
 
     if (warp == kTokWarps) {
-        // ---------------- loads; the first ones go out before the block meets
-        if (lane == 0) {
-            for (int s = 0; s < NS; s++) {
-                mbar_init(full + s, 1);
-                mbar_init(empty + s, kTokWarps);
-            }
-            *abort_flag = 0;
-            fence_mbar_init();
-        }
-        __syncwarp();
+        // ---------------- loads; the first ones go out before the block meets.  The other
+        // warps take the unit from this one, which reads the sequence once, and the barriers
+        // are initialised by warp 0 meanwhile.
+        Sequence seq{0, 0};
+        if (lane == 0) seq = sequence(p, blockIdx.z / p.Hkv);
+        seq.len = __shfl_sync(0xffffffffu, seq.len, 0);
+        seq.start = __shfl_sync(0xffffffffu, seq.start, 0);
+        u = token_unit<64>(a, seq);
+        if (lane == 0) shared_unit = u;
+        asm volatile("bar.sync 1, 64;" ::: "memory");
         int issued = 0;
         auto load = [&](int g) {
             const int st = issued % NS, j0 = u.kt.tile(g) * 64;
@@ -359,26 +356,45 @@ token_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
             for (int it = max(0, issued - NS); it < issued; it++)
                 wait_phase_cleanup(full + it % NS, (it / NS) & 1, kCleanupPolls);
     } else {
-        // ---------------- rows n and n + 8 of the tile; keys 16 warp .. + 15 of each tile
+        if (warp == 0) {
+            if (lane == 0) {
+                prefetch_map(&tmK);
+                prefetch_map(&tmV);
+                for (int s = 0; s < NS; s++) {
+                    mbar_init(full + s, 1);
+                    mbar_init(empty + s, kTokWarps);
+                }
+                *abort_flag = 0;
+                fence_mbar_init();
+            }
+            __syncwarp();
+            asm volatile("bar.arrive 1, 64;" ::: "memory");
+        }
+        // ---------------- rows n and n + 8 of the tile (real or not); keys 16 warp .. + 15 of
+        // each tile
         uint32_t qf[D / 16][4];
-        RowKeys rk[2];
 #pragma unroll
         for (int y = 0; y < 2; y++) {
-            const int rr = u.rt * 16 + n + 8 * y, i = rr / p.G;
-            rk[y] = RowKeys{0, 0, 0};
-            if (rr < rows) rk[y] = row_keys(p, u.seq, i);
-            const __nv_bfloat16 *src =
-                q + u.b * p.q.batch + (u.hk * p.G + rr % p.G) * p.q.head + i * p.q.token + 2 * t;
+            const int rr = blockIdx.y * 16 + n + 8 * y, i = rr / p.G;
+            const __nv_bfloat16 *src = q + blockIdx.z / p.Hkv * p.q.batch +
+                                       (blockIdx.z % p.Hkv * p.G + rr % p.G) * p.q.head +
+                                       i * p.q.token + 2 * t;
 #pragma unroll
             for (int x = 0; x < D / 16; x++)
 #pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const bool in = rr < rows && rk[y].hi > 0 && x * 16 + c * 8 < p.d;
-                    qf[x][y + 2 * c] =
-                        in ? *reinterpret_cast<const uint32_t *>(src + x * 16 + c * 8) : 0u;
-                }
+                for (int c = 0; c < 2; c++)
+                    qf[x][y + 2 * c] = rr < rows && x * 16 + c * 8 < p.d
+                                           ? *reinterpret_cast<const uint32_t *>(src + x * 16 + c * 8)
+                                           : 0u;
         }
-        __syncthreads();   // the barriers are initialised
+        __syncthreads();
+        u = shared_unit;
+        RowKeys rk[2];   // (none for a row that is not real: its logits do not count)
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            const int rr = u.rt * 16 + n + 8 * y;
+            rk[y] = rr < rows ? row_keys(p, u.seq, rr / p.G) : RowKeys{0, 0, 0};
+        }
         // this lane's row of an 8 x 8 matrix: key r8 (+ 8) of the 16, 16-byte column c
         const int r8 = lane & 7, mi = lane >> 3;
         const uint32_t base = smem_u32(sm) + warp * 16 * 128;
@@ -519,7 +535,10 @@ token_f32_kernel(TokenArgs a, const float *q, const float *k, const float *v, fl
     __shared__ RowKeys row_range[R];
     float *sq = buf + 2 * kTile;
     const WinProblem &p = a.p;
-    const TokenUnit u = token_unit<32>(a);
+    __shared__ Sequence shared_seq;
+    Sequence seq = first_threads_sequence(p, blockIdx.z / p.Hkv);
+    share_sequence(seq, &shared_seq);
+    const TokenUnit u = token_unit<32>(a, seq);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
     float *sp = sq + 16 * D + warp * R * 8;   // the warp's probabilities, [row][8]
     const int rows = min(R, p.Nq * p.G - u.rt * 16);

@@ -1,6 +1,9 @@
 """Window, paged and rotary entry points without a GPU: what they refuse, before
 anything is enqueued, and the rotary frequencies."""
+import glob
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -185,3 +188,40 @@ def test_cpu_tensors_are_refused():
         window_attention(q, q, q)
     with pytest.raises(ValueError):
         rotary(q, q, torch.ones(32, dtype=torch.float64))
+
+
+def functions(source):
+    """(name, body) of the functions of a C++ file whose braces open at namespace level."""
+    text = re.sub(r"//[^\n]*|/\*.*?\*/", "", source, flags=re.S)
+    depth, at, spaces = 0, 0, []
+    for m in re.finditer(r"[{}]", text):
+        if m.group() == "{":
+            head = text[at:m.start()]
+            spaces.append((re.search(r"\bnamespace\b[^;]*$", head) is not None, head, m.end()))
+        else:
+            namespace, head, begin = spaces.pop()
+            if not namespace and all(n for n, _, _ in spaces):
+                names = re.findall(r"(\w+)\s*\(", re.split(r"[;}]", head)[-1])
+                yield (names[-1] if names else ""), text[begin:m.start()]
+        at = m.end()
+
+
+def test_a_cta_reads_its_sequence_once():
+    """Trip counts and barriers of a CTA follow from lengths[b] and starts[b].  They are read
+    in one function, and by every thread for itself only where no barrier depends on them."""
+    csrc = os.path.join(os.path.dirname(_lib.__file__), "csrc")
+    reads, calls, per_cta = set(), set(), set()
+    for path in glob.glob(os.path.join(csrc, "window_*.cu*")):
+        for name, body in functions(open(path).read()):
+            if re.search(r"\b(lengths|starts)\s*\[", body):
+                reads.add(name)
+            if re.search(r"\bsequence\(", body):
+                calls.add(name)
+            if "share_sequence(" in body:
+                per_cta.add(name)
+    assert reads == {"sequence"}
+    # one thread for all, or into the CTA's list; a row's sum or store of its own
+    assert calls == {"first_threads_sequence", "token_bf16_kernel", "list_segments",
+                     "row_delta_kernel", "window_dkv_join_kernel"}
+    assert per_cta == {"token_f32_kernel", "simt_fwd_kernel", "simt_dq_kernel", "simt_dkv_kernel",
+                       "tc_window_dq_kernel", "tc_window_dkv_kernel"}
