@@ -10,7 +10,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _lib, positions
+from . import _lib
 
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
@@ -28,6 +28,7 @@ class Rotary(NamedTuple):
     def turn(self, q, k, f, h, w, first=0, backward=False, out=None):
         """(q, k) of f frames turned by their positions, `first` frames behind start;
         backward: gradients turned back.  [B, H, f*h*w, d] tensors."""
+        from . import positions   # (needs the torch binding, which the Monarch kernels do not)
         three = self.dims is not None and len(self.dims) == 3
         call = positions.rotary_backward if backward else positions.rotary
         return call(q, k, self.freqs, dims=self.dims, style=self.style,
