@@ -1,6 +1,6 @@
-"""Loads monarch_torch.so: argument checks and marshalling of the window attention, the
+"""Loads the torch binding: argument checks and marshalling of the window attention, the
 paged attention and the rotary positions (csrc/torch_binding.cpp).  Importing this module
-fails with an ImportError when it has not been built."""
+fails with an ImportError when it has not been built for the installed torch."""
 from __future__ import annotations
 
 import importlib.machinery
@@ -13,7 +13,7 @@ from . import _lib
 from . import build as _build
 
 if not os.path.exists(_build.BINDING):
-    raise ImportError("monarch_torch.so is not built (%s); run "
+    raise ImportError("the torch binding is not built (%s); run "
                       "`python -m structured_attention_video_b200.build`" % _build.BINDING)
 
 _loader = importlib.machinery.ExtensionFileLoader("monarch_torch", _build.BINDING)

@@ -5,14 +5,17 @@
 Each .cu file under csrc/ compiles to an object in parallel; the objects link
 into structured_attention_video_b200/_build/libmonarch.so (CUDA runtime linked
 statically, so the library needs only the NVIDIA driver at run time).
-csrc/torch_binding.cpp becomes the CPython module monarch_torch.so, which marshals torch
-tensors onto the library's C ABI.
+csrc/torch_binding.cpp becomes a CPython module, monarch_torch.<python>.torch-<version>.so,
+which marshals torch tensors onto the library's C ABI.  It is compiled against the installed
+torch's headers, so each version of torch (and of Python) has a module of its own.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import os
+import re
 import subprocess
 import sys
 
@@ -20,7 +23,18 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmonarch.so")
-BINDING = os.path.join(OUT_DIR, "monarch_torch.so")
+
+
+def _binding() -> str:
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    return os.path.join(OUT_DIR, "monarch_torch.%s.torch-%s.so"
+                        % (sys.implementation.cache_tag, re.sub(r"[^\w.]", "-", version)))
+
+
+BINDING = _binding()
 HEADERS = [os.path.join(os.path.dirname(PKG), "include", "monarch_attn.h")]
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

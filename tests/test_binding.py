@@ -28,3 +28,41 @@ for name in ("window_attention", "paged_attention", "rotary"):
         raise AssertionError(name + " without a binding")
 """)
     assert r.returncode == 0, r.stderr
+
+
+# A process that finds another version of torch installed than the one that runs.
+UPGRADED = """
+import importlib.metadata
+installed = importlib.metadata.version
+importlib.metadata.version = lambda name: "99.1+cu999" if name == "torch" else installed(name)
+from structured_attention_video_b200 import build
+"""
+
+
+def test_binding_of_another_torch_is_not_loaded():
+    """The binding is compiled against one torch's headers: after an upgrade it counts as not
+    built, whatever its age, and the Monarch entry points work meanwhile."""
+    r = python(UPGRADED + """
+import structured_attention_video_b200 as pkg
+pkg.monarch_attention
+try:
+    pkg.window_attention
+except ImportError as e:
+    assert "is not built" in str(e) and "99.1" in str(e), e
+else:
+    raise AssertionError("loaded a binding of another torch")
+""")
+    assert r.returncode == 0, r.stderr
+
+
+def test_binding_of_another_torch_is_built_anew():
+    r = python(UPGRADED + """
+targets = []
+class Done:
+    returncode = 0
+build.subprocess.run = lambda cmd, **kw: targets.append(cmd) or Done()
+build.os.replace = lambda a, b: targets.append(b)
+build._build_binding(False)
+assert targets and targets[-1] == build.BINDING, targets
+""")
+    assert r.returncode == 0, r.stderr
