@@ -7,7 +7,9 @@ into structured_attention_video_b200/_build/libmonarch.so (CUDA runtime linked
 statically, so the library needs only the NVIDIA driver at run time).
 csrc/torch_binding.cpp becomes a CPython module, monarch_torch.<python>.torch-<version>.so,
 which marshals torch tensors onto the library's C ABI.  It is compiled against the installed
-torch's headers, so each version of torch (and of Python) has a module of its own.
+torch's headers, so each version of torch (and of Python) has a module of its own.  Where it
+cannot be built (no torch, no headers), that is said and the library stands without it: the
+C ABI and the Monarch attention need none, and the others fail to import.
 """
 from __future__ import annotations
 
@@ -62,7 +64,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = sources()
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + HEADERS
     if not force and not _stale(LIB, deps):
-        _build_binding(force)
+        _try_binding(force)
         return LIB
     nvcc = _nvcc()
 
@@ -88,8 +90,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB)
-    _build_binding(force)
+    _try_binding(force)
     return LIB
+
+
+def _try_binding(force: bool) -> None:
+    try:
+        _build_binding(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING):   # older than its source
+            os.remove(BINDING)
+        sys.stderr.write("The torch binding was not built, so the window attention, the paged "
+                         "attention and the rotary positions are not there: %s\n" % e)
 
 
 def _build_binding(force: bool) -> None:

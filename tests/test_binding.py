@@ -66,3 +66,30 @@ build._build_binding(False)
 assert targets and targets[-1] == build.BINDING, targets
 """)
     assert r.returncode == 0, r.stderr
+
+
+def test_library_builds_where_the_binding_cannot(tmp_path):
+    """Without torch, without a C++ compiler or with headers that do not fit: the library is
+    there, the reason is said, and no module that is older than its source stays."""
+    for broken in ('sys.modules["torch"] = None',
+                   'build.subprocess.run = fails',
+                   'build.subprocess.run = missing'):
+        r = python("""
+import os, subprocess, sys
+from structured_attention_video_b200 import build
+real, out = build.BINDING, %r
+build.BINDING = os.path.join(out, "binding.so")
+open(build.BINDING, "w").close()
+os.utime(build.BINDING, (0, 0))
+older = build._stale
+build._stale = lambda target, deps: target != build.LIB and older(target, deps)   # it is built
+def fails(cmd, **kw):
+    return subprocess.CompletedProcess(cmd, 1, "", "headers do not fit")
+def missing(cmd, **kw):
+    raise FileNotFoundError("g++")
+%s
+assert build.build() == build.LIB and os.path.exists(build.LIB)
+assert not os.path.exists(build.BINDING)
+""" % (str(tmp_path), broken))
+        assert r.returncode == 0, r.stderr
+        assert "was not built" in r.stderr
