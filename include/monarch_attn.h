@@ -571,8 +571,9 @@ MONARCH_API monarch_status monarch_paged_attn_ws(const monarch_window_desc *desc
  *   (first + n / (grid_h*grid_w), n / grid_w % grid_h, n % grid_w).
  * Angles are formed exactly modulo one turn, so far positions lose no accuracy.
  *   freqs   device, float64 [pairs], radians per position, finite.
- *   k, k_out  may be NULL with Hkv = 0.  Outputs may be the inputs (in place) or must
- *   not overlap them.  d is a multiple of 16 bytes of elements, at most 1024.
+ *   k, k_out  may be NULL with Hkv = 0.  q_out may be q and k_out may be k, with the same
+ *   strides (in place); otherwise outputs overlap neither inputs nor each other, and ones
+ *   that begin where another tensor does are refused (MONARCH_ERR_INVALID_ARG).  d is a multiple of 16 bytes of elements, at most 1024.
  * Source: no counterpart in the pages (the positions of the video models whose
  * attention they replace).
  */

@@ -90,6 +90,13 @@ monarch_status status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK :
 // A pointer field whose target (lengths, starts) must be 4-byte aligned.
 bool aligned4(const void *p) { return aligned(p, 4); }
 
+// In place means element by element: whether the strides that count are the same.
+bool same_place(const monarch_rotary_desc *c, int heads, const monarch_strides &a,
+                const monarch_strides &b) {
+    return (c->B == 1 || a.batch == b.batch) && (heads == 1 || a.head == b.head) &&
+           (c->N == 1 || a.token == b.token);
+}
+
 // delta_i of every query row, at the front of the backward's workspace.
 size_t delta_bytes(const WinProblem &p) {
     return ((size_t)p.B * p.H * p.Nq * sizeof(float) + 255) & ~(size_t)255;
@@ -299,6 +306,12 @@ monarch_status monarch_rotary(const monarch_rotary_desc *c, const void *q, const
     if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(k_out, 16) ||
         !aligned(freqs, 8) || !aligned4(c->starts) || !aligned4(c->positions))
         return MONARCH_ERR_ALIGN;
+    // a thread reads what it writes and nothing else: an output in another place of an input,
+    // or two outputs in one place, would hold whatever block came last
+    if ((q_out == q && !same_place(c, c->H, c->q, c->q_out)) ||
+        (c->Hkv && ((k_out == k && !same_place(c, c->Hkv, c->k, c->k_out)) || q_out == k ||
+                    k_out == q || q_out == k_out)))
+        return MONARCH_ERR_INVALID_ARG;
     rot::RotaryProblem p;
     p.B = c->B;
     p.N = c->N;

@@ -47,8 +47,8 @@ def rotary(q, k, freqs, *, dims=None, style="interleaved", grid=None, positions=
     split the pairs; one axis by default.  Positions: `positions` int32 [N] or [B, N] (with
     several axes [.., N, axes]); or one axis from `start` on; or with three axes the
     tokens of grid = (frames, rows, columns) with `start` the first frame.  start is an
-    int, or int32 [B] on the device.  out = (q_out, k_out) may be the inputs, or slices
-    of a cache."""
+    int, or int32 [B] on the device.  out = (q_out, k_out) may be the inputs, each in its
+    own place, or slices of a cache."""
     return _native.rotary(q, k, freqs, dims, style, grid, positions, start, magnitude, layout,
                           out, False)
 

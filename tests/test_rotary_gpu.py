@@ -168,3 +168,20 @@ def test_backward_is_the_gradient():
     f = lambda x: float((rotary(x, None, freqs, **kw)[0].double() * w.double()).sum())  # noqa: E731
     slope = (f(q + d) - f(q - d)) / 2     # the map is linear: exact but for roundings
     assert abs(slope - float((dq.double() * d.double()).sum())) < 1e-3
+
+
+def test_outputs_in_the_place_of_others_are_refused():
+    freqs, _ = rotary_frequencies(64)
+    q, k = make(13, "f32", 1, 24, 24, 64, "bhnd"), make(14, "f32", 1, 24, 24, 64, "bhnd")
+    before = q.clone(), k.clone()
+    new = torch.empty_like(q)
+    for a, b, out in ((q, k, (k, q)), (q, k, (new, new)), (q, q, (q, new)),
+                      (q, k, (q.transpose(1, 2), k))):
+        with pytest.raises(_lib.MonarchError):
+            rotary(a, b, freqs, out=out)
+    assert torch.equal(q, before[0]) and torch.equal(k, before[1])
+    a, b = rotary(q, k, freqs)
+    c, d = rotary(q, q, freqs)      # the same queries and keys, each turned into its own place
+    assert torch.equal(a, c) and torch.equal(c, d)
+    rotary(q, k, freqs, out=(q, k))
+    assert torch.equal(q, a) and torch.equal(k, b)

@@ -150,6 +150,20 @@ def test_rotary_pointers():
     assert _lib.monarch_rotary(None, P, P, P, P, P, None) == INVALID
 
 
+def test_rotary_outputs_in_the_place_of_others_are_refused():
+    d, A, B_, C = rotary_desc(), P, 2 * P, 3 * P
+    call = lambda d, q, k, qo, ko: _lib.monarch_rotary(d, q, k, P, qo, ko, None)   # noqa: E731
+    assert call(d, A, B_, B_, A) == INVALID      # swapped
+    assert call(d, A, B_, C, C) == INVALID       # both in one place
+    assert call(d, A, A, A, C) == INVALID        # queries in place that are the keys as well
+    assert call(d, A, B_, C, A) == INVALID
+    for name, i in (("q_out", 0), ("k_out", 1)):   # in place, tokens and heads exchanged
+        x = rotary_desc(**{name + ".head": 64, name + ".token": 4 * 64})
+        outs = [C, 4 * P]
+        outs[i] = (A, B_)[i]
+        assert call(x, A, B_, *outs) == INVALID
+
+
 def test_rotary_frequencies():
     f, m = rotary_frequencies(64, device="cpu")
     want = torch.tensor([10000.0 ** (-i / 32) for i in range(32)], dtype=torch.float64)
