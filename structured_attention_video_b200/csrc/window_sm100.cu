@@ -471,8 +471,12 @@ tc_window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int si = 0; ok && si < nseg; si++) {
             const Segment sg(a, list[si]);
             if (sg.nh == 0) continue;
+            // these waits last as long as the whole segment, so their limit grows with it
+            // (each block's own waits have the plain one and raise the abort flag)
+            const WaitCtx whole{a.limit * (1 + sg.nh / 16), a.status, abort_flag};
             for (int t = 0; t < a.tiles; t++) {
-                if (!wait_warp(o_full + t, pc & 1, w) || !wait_warp(l_full + t, pc & 1, w)) {
+                if (!wait_warp(o_full + t, pc & 1, whole) ||
+                    !wait_warp(l_full + t, pc & 1, whole)) {
                     ok = false;
                     break;
                 }

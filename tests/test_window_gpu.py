@@ -390,6 +390,22 @@ def test_waits_give_up_and_the_next_call_is_right():
     check(q, k, v, dout)
 
 
+def test_wait_limit_is_not_a_limit_on_the_length():
+    """A CTA's epilogue waits for all of a problem's blocks (here 3125, for 2 ms).  With a limit
+    on polls that this wait passes, and each block's own waits do not, the call completes."""
+    H = torch.cuda.get_device_properties(0).multi_processor_count
+    q, k, v, _ = make(28, "bf16", 1, H, 1, 64, 256, 200000)
+    want = window_attention(q, k, v, window=(-1, -1))
+    torch.cuda.synchronize()
+    old = _lib.monarch_set_wait_limit(256)
+    try:
+        got = window_attention(q, k, v, window=(-1, -1))
+        assert _lib.monarch_last_device_status(None) == 0
+    finally:
+        _lib.monarch_set_wait_limit(old)
+    assert torch.equal(got, want)
+
+
 # ---------------------------------------------------------------- paged
 def pages_of(k, v, page, lengths, layout, seed=0, extra=3):
     """Scattered pages that hold each sequence's keys, and NaN everywhere else."""
