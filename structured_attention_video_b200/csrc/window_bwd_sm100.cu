@@ -7,9 +7,9 @@
 //
 // Two kernels, so that every gradient is summed by one CTA in a fixed order (no
 // atomics) at the price of forming S and dO V^T twice (7 products instead of 5):
-//   tc_window_dkv_kernel  128 keys of one key head against the 128-query tiles of
+//   tc_window_dkv_kernel  128 keys of one key head against the 64-query blocks of
 //                         every head of its group that see them;
-//   tc_window_dq_kernel   128 queries of one head against their 128-key tiles.
+//   tc_window_dq_kernel   128 queries of one head against their 64-key blocks.
 // 640 threads a CTA, one CTA an SM: warps 0-15 the elementwise work, warp 16 loads, one
 // thread of warp 17 issues S and dV, one of warp 18 dP and dK (or dQ), warp 19 stages lse
 // and delta (dkv).
@@ -42,8 +42,9 @@
 // sequences of 1023 and 681 tokens, d = 64: dq is 2.6e-3 from 64 bits without it.)
 // Bound by the tensor pipe and, nearly as long, the elementwise warps' issue slots: 4 (3)
 // products of 128 x 128 x d a tile against 16384 exponentials at 16 a clock.  The same
-// frames, forward included: 1638 us against 967 of the fewest products at the rate of a
-// large matrix product.
+// frames, forward included: 1667 us in a burst and 1913 in a long run, where the power
+// limit lowers the clocks, against 967 of the fewest products at the rate of a large matrix
+// product.
 #include "window_tc.cuh"
 
 namespace monarch {

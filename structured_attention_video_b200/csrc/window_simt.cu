@@ -590,7 +590,10 @@ cudaError_t allow_smem(K kernel, int bytes) {
 // run at once (two an SM), of four streamed tiles at least, or of `shared` where they would
 // share SMs and gain less than the join takes.  d = 64: 12 heads of 100 queries over 9000
 // keys forward 520 -> 113 us, backward 1049 -> 407; 4 heads of 1000 tokens backward 234 ->
-// 139; those of 780, forward and backward, 100 us whole and 110 with parts of five tiles.
+// 139.  Backward without / with short parts that share SMs: 780 tokens of 4 heads, 255 keys a
+// row, d = 64 79 / 89 us; 1000 tokens of 3 heads, 201 keys, d = 128 127 / 138; 2 x 400 tokens,
+// 4 heads, d = 64 109 / 111; but 780 tokens of 2 heads, 511 keys, d = 128 140 / 130 and 3 x 512
+// tokens, 2 heads, d = 64 123 / 95.  148 and 296 are the device's SMs and two CTAs on each.
 struct Division {
     int rows, parts;
 };

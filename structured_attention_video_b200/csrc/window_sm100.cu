@@ -17,11 +17,12 @@
 //
 // Bound by the exponentials (16 a clock and SM, 2 tiles x 128 x 64 a half) together with
 // the issue slots of the softmax warps, then by the products.  A 480p chunk of 4680
-// queries that see 18720 keys, 12 heads, d = 128: 497 us (1083 TFLOP/s; 579 us where the
-// power limit lowers the clocks of a long run), against 331 for the products alone.
-// Rejected: one
-// maximum a block guessed from the last one's (fewer instructions on the common path, but
-// 27% more time for the test and the repeat behind it).
+// queries that see 18720 keys, 12 heads, d = 128: 489 us (1101 TFLOP/s; 565 us where the
+// power limit lowers the clocks of a long run), against 331 for the products alone.  A test
+// in the common block costs 2% of that, which is why values past the sequence are cleared
+// inside the branch for blocks that the mask cuts.
+// Rejected: one maximum a block guessed from the last one's (fewer instructions on the
+// common path, but 27% more time for the test and the repeat behind it).
 #include "window_tc.cuh"
 
 namespace monarch {

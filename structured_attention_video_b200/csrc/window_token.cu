@@ -10,7 +10,9 @@
 // several clusters, whose results a second kernel joins.  Every join adds the parts
 // in their order, so results do not depend on which CTA came first.
 // The rows of a key head (queries x heads of its group) form tiles of 16, the height
-// of mma.m16n8k16: every key is read once for all of them.  The split counts the
+// of mma.m16n8k16: every key is read once for each such tile, so once for a group of up to
+// 16 heads and one query, and up to four times at the 64 rows where other kernels take
+// over (window_api.cu).  The split counts the
 // visible keys only (the sinks, then the window), from each sequence's own length,
 // so ragged batches and windows divide evenly.
 //
@@ -718,7 +720,10 @@ cudaError_t join(const TokenArgs &a, T *out, float *lse, cudaStream_t stream) {
 // join, 2.5 and more for the join of clusters.  Against as many as make three CTAs an SM,
 // bfloat16: one sequence of 4000 keys, 12 heads 22.7 -> 14.8 us; 4 x 2000 keys, 8 key heads
 // 24.6 -> 13.8; 24 x 6000 keys, 4 key heads of 64 46.9 -> 32.3; four of 131072 keys 252 -> 242.
-// A float32 tile has half the keys and the same bytes.
+// kFit, latency and share are the bfloat16 kernels' on 148 SMs.  A float32 tile has half the keys
+// and the same bytes, and the float32 kernels use the same numbers although more of their
+// CTAs fit on an SM: for them the estimate is a rule of thumb.  Keys are counted by what the
+// tensors hold, as the lengths are on the device.
 int parts_of(int64_t units, double tiles, int d) {
     static constexpr int kFit[2][8] = {{444, 222, 142, 104, 82, 71, 56, 48},   // d = 32, 64
                                        {296, 148, 93, 71, 56, 45, 37, 33}};    // d = 128
