@@ -362,7 +362,7 @@ MONARCH_API monarch_status monarch_last_device_status(monarch_stream_t stream);
 
 /*
  * Test hook: the iteration limit of the device-side bounded waits (spins on an
- * mbarrier).  0 restores the default.  Takes effect for launches enqueued after
+ * mbarrier), at most 2^40.  0 restores the default.  Takes effect for launches enqueued after
  * the call, on every device.  Returns the previous limit.
  * Source: no counterpart in the pages (a test facility of this library).
  */

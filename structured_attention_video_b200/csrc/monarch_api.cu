@@ -571,7 +571,10 @@ monarch_status monarch_last_device_status(monarch_stream_t stream) {
 }
 
 long long monarch_set_wait_limit(long long spins) {
-    return g_wait_limit.exchange(spins > 0 ? spins : kDefaultWaitLimit);
+    // (kernels multiply the limit: by 16 where polls are short, by a problem's length where
+    // one wait covers all of it)
+    return g_wait_limit.exchange(spins > 0 ? (spins < kMostWaitLimit ? spins : kMostWaitLimit)
+                                           : kDefaultWaitLimit);
 }
 
 int monarch_debug_inject_stall(int on) { return g_inject_stall.exchange(on != 0 ? 1 : 0); }

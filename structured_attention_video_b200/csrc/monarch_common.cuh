@@ -97,6 +97,7 @@ __host__ __device__ __forceinline__ int64_t head_base(const Problem &p, int bh, 
 // status word of the library (one int per device, read and cleared by
 // monarch_last_device_status) and record MONARCH_ERR_TIMEOUT there.
 constexpr long long kDefaultWaitLimit = 1LL << 22;
+constexpr long long kMostWaitLimit = 1LL << 40;   // a day of polls
 
 __device__ __forceinline__ void record_status(int *status, int code) {
     atomicCAS(status, 0, code);

@@ -204,6 +204,16 @@ def test_cpu_tensors_are_refused():
         rotary(q, q, torch.ones(32, dtype=torch.float64))
 
 
+def test_wait_limit_stays_below_what_kernels_multiply():
+    """16 times and more of a limit near 2^63 would be negative: every wait would give up."""
+    old = _lib.monarch_set_wait_limit(2 ** 63 - 1)
+    try:
+        assert _lib.monarch_set_wait_limit(12345) == 2 ** 40
+        assert _lib.monarch_set_wait_limit(0) == 12345
+    finally:
+        _lib.monarch_set_wait_limit(old)
+
+
 def functions(source):
     """(name, body) of the functions of a C++ file whose braces open at namespace level."""
     text = re.sub(r"//[^\n]*|/\*.*?\*/", "", source, flags=re.S)
