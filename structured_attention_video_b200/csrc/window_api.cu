@@ -192,7 +192,7 @@ size_t monarch_window_attn_bwd_workspace_bytes(const monarch_window_desc *desc) 
     WinProblem p;
     if (validate_window(desc, &p) != MONARCH_OK) return 0;
     return at_least_256(delta_bytes(p) +
-                        (desc->dtype == MONARCH_BF16 ? win::tc_backward_bytes(p)
+                        (desc->dtype == MONARCH_BF16 ? win::mma_backward_bytes(p)
                                                      : win::simt_backward_bytes(p)));
 }
 
@@ -222,18 +222,16 @@ monarch_status monarch_window_attn_bwd_ws(const monarch_window_desc *desc,
     const WinGrads g{to_win(grads->dout), to_win(grads->dq), to_win(grads->dk), to_win(grads->dv)};
     cudaStream_t s = (cudaStream_t)stream;
     float *delta = (float *)workspace;
-    const cudaError_t e = win::row_delta(p, g, desc->dtype, out, dout, delta, s);
-    if (e != cudaSuccess) return MONARCH_ERR_CUDA;
+    void *parts = (char *)workspace + delta_bytes(p);
     if (desc->dtype == MONARCH_F32)
         return status_of(win::simt_backward(p, g, (const float *)q, (const float *)k,
-                                            (const float *)v, lse, delta, (const float *)dout,
-                                            (float *)dq, (float *)dk, (float *)dv,
-                                            (char *)workspace + delta_bytes(p), s));
+                                            (const float *)v, (const float *)out, lse, delta,
+                                            (const float *)dout, (float *)dq, (float *)dk,
+                                            (float *)dv, parts, s));
     int *status = device_status_word();
     if (!status) return MONARCH_ERR_CUDA;
-    return status_of(win::tc_backward(p, g, q, k, v, lse, delta, dout, dq, dk, dv,
-                                      (char *)workspace + delta_bytes(p), status,
-                                      device_wait_limit(), s));
+    return status_of(win::mma_backward(p, g, q, k, v, out, lse, delta, dout, dq, dk, dv, parts,
+                                       status, device_wait_limit(), s));
 }
 
 size_t monarch_paged_attn_workspace_bytes(const monarch_window_desc *desc) {

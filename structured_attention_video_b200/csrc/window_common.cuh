@@ -171,12 +171,9 @@ cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, co
                          float *out, float *lse, void *workspace, cudaStream_t stream);
 size_t simt_backward_bytes(const WinProblem &p);   // of `parts`
 cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
-                          const float *v, const float *lse, const float *delta, const float *dout,
-                          float *dq, float *dk, float *dv, void *parts, cudaStream_t stream);
-// delta_i = dO_i . O_i of every query row, [B][H][Nq].
-cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
-                      const void *dout, float *delta, cudaStream_t stream);
-
+                          const float *v, const float *out, const float *lse, float *delta,
+                          const float *dout, float *dq, float *dk, float *dv, void *parts,
+                          cudaStream_t stream);
 // Few query rows a key head against many keys, split over the keys (window_token.cu).
 struct TokenPlan {
     int row_tiles;   // tiles of 16 rows (query, head of the group) a key head
@@ -189,17 +186,17 @@ cudaError_t token_forward(const WinProblem &p, monarch_dtype dtype, const TokenP
                           const void *q, const void *k, const void *v, void *out, float *lse,
                           void *workspace, int *status, long long limit, cudaStream_t stream);
 
-// Tensor-core kernels, bfloat16 (window_sm100.cu, window_bwd_sm100.cu).
+// Tensor-core kernels, bfloat16 (window_sm100.cu; backward window_bwd_mma.cu).
 size_t tc_forward_bytes(const WinProblem &p);   // workspace, 0 where none is needed
 cudaError_t tc_forward(const WinProblem &p, const void *q, const void *k, const void *v, void *out,
                        float *lse, void *workspace, int *status, long long limit,
                        cudaStream_t stream);
 
-size_t tc_backward_bytes(const WinProblem &p);   // of `parts`, 0 where none are needed
-cudaError_t tc_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
-                        const void *v, const float *lse, float *delta, const void *dout,
-                        void *dq, void *dk, void *dv, void *parts, int *status, long long limit,
-                        cudaStream_t stream);
+size_t mma_backward_bytes(const WinProblem &p);   // of `parts`, 0 where none are needed
+cudaError_t mma_backward(const WinProblem &p, const WinGrads &g, const void *q, const void *k,
+                         const void *v, const void *out, const float *lse, float *delta,
+                         const void *dout, void *dq, void *dk, void *dv, void *parts, int *status,
+                         long long limit, cudaStream_t stream);
 
 }  // namespace win
 }  // namespace monarch

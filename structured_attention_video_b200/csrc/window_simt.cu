@@ -1,6 +1,5 @@
 // window_simt.cu -- window attention in 32-bit arithmetic on the FMA pipes, forward
-// and backward (float32 inputs; the tensor cores round operands to fewer bits), and
-// the row sums delta = dO.O of both types' backward.
+// and backward (float32 inputs; the tensor cores round operands to fewer bits).
 //
 // One CTA of 256 threads takes 16 RT rows of one side (queries; keys for dk and dv)
 // and walks tiles of the other side.  Thread (ty, tx) of a 16 x 16 grid owns rows
@@ -522,58 +521,30 @@ simt_sum_kernel(const float *parts, int splits, int B, int heads, int tokens, fl
 }
 
 // ---------------------------------------------------------------- delta
-// 16-byte loads, d / (elements of 16 bytes) lanes a row; rows without keys get 0 (their
-// dO may be anything).  Bound by memory: dO and O are read once.
-__device__ __forceinline__ float dot16(const float *a, const float *b) {
-    const float4 x = *reinterpret_cast<const float4 *>(a), y = *reinterpret_cast<const float4 *>(b);
-    return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
-}
-__device__ __forceinline__ float dot16(const __nv_bfloat16 *a, const __nv_bfloat16 *b) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(a), y = *reinterpret_cast<const uint4 *>(b);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
-        sum = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), sum);
-    }
-    return sum;
-}
-
-template <typename T, int D>
+// delta_i = dO_i . O_i: 16-byte loads, d / 4 lanes a row; rows without keys get 0 (their dO
+// may be anything).  Bound by memory: dO and O are read once.
+template <int D>
 __global__ void __launch_bounds__(256)
-row_delta_kernel(WinProblem p, WinGrads g, const T *out, const T *dout, float *delta) {
-    constexpr int V = 16 / sizeof(T), LANES = D / V, ROWS = 256 / LANES;
+row_delta_kernel(WinProblem p, WinGrads g, const float *out, const float *dout, float *delta) {
+    constexpr int LANES = D / 4, ROWS = 256 / LANES;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
-    const int x = threadIdx.x % LANES * V;
+    const int c = threadIdx.x % LANES * 4;
     float sum = 0.f;
     if (row < (int64_t)p.B * p.H * p.Nq) {
         const int i = (int)(row % p.Nq), bh = (int)(row / p.Nq), h = bh % p.H, b = bh / p.H;
         const Sequence seq = sequence(p, b);
         const int64_t pos = seq.start + i;
-        if (pos >= 0 && pos < seq.len)   // a real row
-            sum = dot16(out + b * p.o.batch + h * p.o.head + i * p.o.token + x,
-                        dout + b * g.dout.batch + h * g.dout.head + i * g.dout.token + x);
+        if (pos >= 0 && pos < seq.len) {   // a real row
+            const float4 x = *reinterpret_cast<const float4 *>(
+                out + b * p.o.batch + h * p.o.head + i * p.o.token + c);
+            const float4 y = *reinterpret_cast<const float4 *>(
+                dout + b * g.dout.batch + h * g.dout.head + i * g.dout.token + c);
+            sum = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+        }
     }
 #pragma unroll
     for (int m = LANES / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (x == 0 && row < (int64_t)p.B * p.H * p.Nq) delta[row] = sum;
-}
-
-template <typename T>
-cudaError_t run_delta(const WinProblem &p, const WinGrads &g, const void *out, const void *dout,
-                      float *delta, cudaStream_t stream) {
-    const int64_t rows = (int64_t)p.B * p.H * p.Nq;
-    const int per = 256 / (p.d * (int)sizeof(T) / 16);
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
-    const T *o = (const T *)out, *d = (const T *)dout;
-    if (p.d == 32)
-        row_delta_kernel<T, 32><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
-    else if (p.d == 64)
-        row_delta_kernel<T, 64><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
-    else
-        row_delta_kernel<T, 128><<<grid, 256, 0, stream>>>(p, g, o, d, delta);
-    return cudaGetLastError();
+    if (c == 0 && row < (int64_t)p.B * p.H * p.Nq) delta[row] = sum;
 }
 
 template <typename K>
@@ -679,11 +650,16 @@ cudaError_t forward_d(const WinProblem &p, const float *q, const float *k, const
 
 template <int D>
 cudaError_t backward_d(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
-                       const float *v, const float *lse, const float *delta, const float *dout,
-                       float *dq, float *dk, float *dv, float *parts, cudaStream_t stream) {
-    const cudaError_t e = dq_division(p).rows == 4
-                              ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, parts, stream)
-                              : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, parts, stream);
+                       const float *v, const float *out, const float *lse, float *delta,
+                       const float *dout, float *dq, float *dk, float *dv, float *parts,
+                       cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.B * p.H * p.Nq, per = 256 / (D / 4);
+    row_delta_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(p, g, out, dout, delta);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = dq_division(p).rows == 4
+            ? dq_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dq, parts, stream)
+            : dq_rt<D, 2>(p, g, q, k, v, lse, delta, dout, dq, parts, stream);
     if (e != cudaSuccess) return e;
     if (dkv_division(p).rows == 4)
         return dkv_rt<D, 4>(p, g, q, k, v, lse, delta, dout, dk, dv, parts, stream);
@@ -713,18 +689,14 @@ cudaError_t simt_forward(const WinProblem &p, const float *q, const float *k, co
 }
 
 cudaError_t simt_backward(const WinProblem &p, const WinGrads &g, const float *q, const float *k,
-                          const float *v, const float *lse, const float *delta, const float *dout,
-                          float *dq, float *dk, float *dv, void *workspace, cudaStream_t stream) {
+                          const float *v, const float *out, const float *lse, float *delta,
+                          const float *dout, float *dq, float *dk, float *dv, void *workspace,
+                          cudaStream_t stream) {
     float *parts = (float *)workspace;
-    if (p.d == 32) return backward_d<32>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
-    if (p.d == 64) return backward_d<64>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
-    return backward_d<128>(p, g, q, k, v, lse, delta, dout, dq, dk, dv, parts, stream);
-}
-
-cudaError_t row_delta(const WinProblem &p, const WinGrads &g, monarch_dtype dtype, const void *out,
-                      const void *dout, float *delta, cudaStream_t stream) {
-    return dtype == MONARCH_F32 ? run_delta<float>(p, g, out, dout, delta, stream)
-                                : run_delta<__nv_bfloat16>(p, g, out, dout, delta, stream);
+    return p.d == 32 ? backward_d<32>(p, g, q, k, v, out, lse, delta, dout, dq, dk, dv, parts, stream)
+           : p.d == 64
+               ? backward_d<64>(p, g, q, k, v, out, lse, delta, dout, dq, dk, dv, parts, stream)
+               : backward_d<128>(p, g, q, k, v, out, lse, delta, dout, dq, dk, dv, parts, stream);
 }
 
 }  // namespace win

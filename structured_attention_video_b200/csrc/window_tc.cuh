@@ -1,5 +1,5 @@
-// window_tc.cuh -- what the tensor-core forward (window_sm100.cu) and backward
-// (window_bwd_sm100.cu) of the window attention share.
+// window_tc.cuh -- what the bfloat16 kernels of the window attention share: products on
+// tensor memory (window_sm100.cu) and the tensor maps (window_sm100.cu, window_token.cu).
 #pragma once
 
 #include "monarch_tc_shared.cuh"
@@ -48,37 +48,6 @@ __device__ __forceinline__ void mma_head(uint32_t d_tmem, uint64_t a, uint64_t b
     for (int k = 0; k < HD / 16; k++)
         mma_one(d_tmem, a + (k >> 2) * (kPanel >> 4) + (k & 3) * 2,
                 b + (k >> 2) * (BROWS * 128 >> 4) + (k & 3) * 2, idesc, k > 0);
-}
-
-// The same with A in tensor memory (bfloat16 pairs, 8 columns a K-step): shared memory
-// then feeds B alone.
-template <int HD, int BROWS>
-__device__ __forceinline__ void mma_head_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                            uint32_t idesc) {
-#pragma unroll
-    for (int k = 0; k < HD / 16; k++)
-        mma_one_ts(d_tmem, a_tmem + 8 * k, b + (k >> 2) * (BROWS * 128 >> 4) + (k & 3) * 2, idesc,
-                   k > 0);
-}
-
-// One row of HD bfloat16 elements (d of them real, the others zero) from global memory
-// to this lane's row of tensor memory, as the A operand of mma_head_ts.
-template <int HD>
-__device__ __forceinline__ void row_to_tmem(uint32_t taddr, const __nv_bfloat16 *src, int d,
-                                            bool real) {
-#pragma unroll
-    for (int c = 0; c < HD / 2; c += 32) {
-        uint32_t r[32];
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int x = 2 * c + 8 * e;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (real && x < d) v = *reinterpret_cast<const uint4 *>(src + x);
-            r[4 * e] = v.x, r[4 * e + 1] = v.y, r[4 * e + 2] = v.z, r[4 * e + 3] = v.w;
-        }
-        tmem_st32(taddr + c, r);
-    }
-    tmem_wait_st();
 }
 
 // D (+)= A B over 64 keys or queries: A bfloat16 pairs in tensor memory (8 columns a

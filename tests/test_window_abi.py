@@ -246,6 +246,6 @@ def test_a_cta_reads_its_sequence_once():
     assert reads == {"sequence"}
     # one thread for all, or into the CTA's list; a row's sum or store of its own
     assert calls == {"first_threads_sequence", "token_bf16_kernel", "list_segments",
-                     "row_delta_kernel", "window_dkv_join_kernel"}
+                     "row_delta_kernel"}
     assert per_cta == {"token_f32_kernel", "simt_fwd_kernel", "simt_dq_kernel", "simt_dkv_kernel",
-                       "tc_window_dq_kernel", "tc_window_dkv_kernel"}
+                       "mma_dq_kernel", "mma_dkv_kernel"}

@@ -192,3 +192,23 @@ def test_float32_pages_past_32_bit_offsets():
     out = paged_attention(q[:, :, 0], pools[0], pools[1], ints(*at).view(1, 2), ints(128))
     assert status() == 0
     assert_within(out, ref["out"][:, :, 0], ref["out_bound"][:, :, 0], "out")
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("H,Hkv,Nq,Nk", [(3, 3, 6, 3), (12, 3, 1, 241), (2, 1, 70, 70)])
+def test_gradients_of_many_short_ragged_sequences(d, H, Hkv, Nq, Nk):
+    """Forty sequences of no to a few hundred keys, a block of them without any: many short
+    blocks one after another, many times."""
+    B = 40
+    lens = [(0, 0, Nk, 1, Nk, (7 * b) % (Nk + 1), 0, Nk)[b % 8] for b in range(B)]
+    q, k, v, dout = make(38, "bf16", B, H, Hkv, d, Nq, Nk)
+    kw = dict(window=(300, -1), sinks=3, lengths=ints(*lens))
+    ref = attention(q, k, v, dout, **kw)
+    out, lse = window_attention(q, k, v, return_lse=True, **kw)
+    first = window_attention_backward(q, k, v, out, lse, dout, **kw)
+    for name, got in zip(("dq", "dk", "dv"), first):
+        assert_within(got, ref[name], ref[name + "_bound"], name)
+    for _ in range(100):
+        again = window_attention_backward(q, k, v, out, lse, dout, **kw)
+    assert status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(first, again))
