@@ -265,6 +265,7 @@ simt_fwd_kernel(WinProblem p, const float *q, const float *k, const float *v, fl
         }
         add_product<D, RT, 64, 68>(sp, sv, ty, tx, o);
     }
+    copies_wait<0>();   // without keys the queries' copies may still be under way
     float inv[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) {
@@ -391,6 +392,7 @@ simt_dq_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const f
         __syncwarp();
         add_product<D, RT, 32, 36>(sds, sk, ty, tx, o);
     }
+    copies_wait<0>();   // (see the forward)
     float sc[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) sc[i] = gridDim.z > 1 ? 1.f : p.scale;
@@ -486,6 +488,7 @@ simt_dkv_kernel(WinProblem p, WinGrads g, const float *q, const float *k, const 
             add_product<D, RT, 32, 36>(sw, sq, ty, tx, ok);
         }
     }
+    copies_wait<0>();   // (see the forward)
     float sc[RT], one[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) sc[i] = gridDim.z > 1 ? 1.f : p.scale, one[i] = 1.f;

@@ -212,3 +212,21 @@ def test_gradients_of_many_short_ragged_sequences(d, H, Hkv, Nq, Nk):
         again = window_attention_backward(q, k, v, out, lse, dout, **kw)
     assert status() == 0
     assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("starts", [2 ** 31 - 1, -2 ** 31 + 1])
+def test_float32_blocks_that_see_no_key_drain_their_copies(d, starts):
+    """Every row lies outside its sequence, so each block has only its own rows' copies and
+    must not end before they do."""
+    q, k, v, dout = make(39, "f32", 4, 8, 2, d, 700, 300)
+    good = make(40, "f32", 1, 2, 1, d, 200, 200)
+    want = window_attention(*good[:3], return_lse=True)
+    for _ in range(20):
+        out, lse = window_attention(q, k, v, starts=starts, return_lse=True)
+        grads = window_attention_backward(q, k, v, out, lse, dout, starts=starts)
+        again = window_attention(*good[:3], return_lse=True)
+    assert status() == 0
+    assert (lse == -math.inf).all()
+    assert all((x == 0).all() for x in (out, *grads))
+    assert all(torch.equal(x, y) for x, y in zip(want, again))
