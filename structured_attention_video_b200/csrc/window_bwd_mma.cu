@@ -16,10 +16,15 @@
 // an ldmatrix cover all banks.
 //
 // Not on tcgen05.  A form with tensor memory and TMA (dq and dk/dv with two issuing threads
-// and sixteen elementwise warps) took a third of the time or less, but about one call in 400 on
-// small ragged batches ended in an illegal address, its cause not found by reading, and with
-// checks in the kernels it did not show.  These kernels have no waits, no tensor memory and no
-// asynchronous copy that outlives its CTA.
+// and sixteen elementwise warps) took 1.2 ms instead of 6.4 on nine 480p frames, but about one
+// call in 400 on small ragged batches ended in an illegal address, its cause not found by
+// reading, and with checks in the kernels it did not show.  These kernels have no waits, no
+// tensor memory and no asynchronous copy that outlives its CTA.
+//
+// Bound by the products of mma.sync (45 to 47% of that pipe, about 540 TFLOP/s at most) with
+// the reads of their fragments from shared memory close behind.  Nine 480p frames, each seeing
+// four, 12 heads, d = 128: dq 2.81 ms, dk/dv 3.59; 2 x 1023 causal tokens, 8 heads on 2 key
+// heads, d = 64: 40, 41 and 5 us for the join.
 //
 // delta comes from out as the forward rounded it, an error of 2^-8 |dO.O| at most.  A
 // row of n keys of like weight has |O| of about n^(-1/2) |v|, so against dP it matters
@@ -446,7 +451,8 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t stream) {
 }
 
 // Parts of a key tile's query blocks in the dk/dv kernel: where the key tiles are fewer than
-// two CTAs an SM, as many as fill those, of four blocks at least.
+// two CTAs an SM, as many as fill those, of four blocks at least (a part's prologue, its
+// store and the join cost about two).
 int dkv_splits(const WinProblem &p) {
     const int64_t tiles = (int64_t)p.B * p.Hkv * ((p.Nk + kRows - 1) / kRows);
     const int block = p.d == 128 ? kBlock<128> : kBlock<64>;
