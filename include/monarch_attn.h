@@ -455,7 +455,8 @@ MONARCH_API int monarch_attn_path(int B, int H, int f, int h, int w, int d, int 
  * context (the first one loads its kernels); each captured call wants a workspace of its
  * own where two replays can overlap.  The kernels wait with the limit of
  * monarch_set_wait_limit and report through monarch_last_device_status;
- * monarch_debug_inject_stall reaches those of path 1 and the bfloat16 backward.  The
+ * monarch_debug_inject_stall reaches path 1 and the bfloat16 backward (which has no waits of
+ * its own and, while the fault is on, does nothing but wait and give up).  The
  * monarch_profile_* hooks do not cover these kernels.
  * ------------------------------------------------------------------------ */
 typedef struct {
